@@ -61,7 +61,13 @@ extern "C" {
 /* Same type as cudaStream_t. */
 typedef struct CUstream_st* bi_stream;
 
-typedef enum { BI_BF16 = 0, BI_F16 = 1, BI_F32 = 2 } bi_dtype;
+typedef enum {
+  BI_BF16 = 0,
+  BI_F16 = 1,
+  BI_F32 = 2,
+  BI_I32 = 3, /* index operands of the serving operations only */
+  BI_I64 = 4
+} bi_dtype;
 
 typedef enum {
   BI_OK = 0,
@@ -370,9 +376,193 @@ bi_status bi_addmm_packed(const bi_tensor* bias, const bi_tensor* a, const bi_pa
                           const bi_tensor* c, bi_stream stream);
 
 /*
+ * Serving operations around a paged key-value cache.
+ *
+ * One layer's cache is two tensors k_cache and v_cache [P, page_size, Hkv, D]
+ * of P pages.  Request b's j-th token lies in page page_table[b, j / page_size],
+ * row j % page_size; its "slot" is page * page_size + row.  One decode step is
+ * bi_paged_plan (once), then per layer bi_paged_store and bi_paged_attention,
+ * then bi_token_logprobs on the logits.  Each is one launch (the attention two
+ * when a request's keys may be split), allocates nothing and reads lengths and
+ * tables on the device, so a step can be captured into a CUDA graph and
+ * replayed as the batch grows within the captured extents; graphs whose
+ * replays may overlap need workspaces of their own.
+ *
+ * Invariance: a request's rows depend on that request alone -- not on the
+ * batch, on which pages hold its tokens or on the page size.
+ *
+ * Index operands are int32 or int64 tensors as each entry states, contiguous.
+ * A slot, page or length that the cache or the table does not have is found on
+ * the device: nothing is read or written through it, and bi_device_status
+ * reports BI_ERR_INVALID_ARG.  No output may overlap an input or another
+ * output in memory unless the entry says so (BI_ERR_INVALID_ARG).
+ */
+
+/*
+ * Block tables and slot maps from request lengths.
+ *   context_lens [B], new_lens [B] int32: tokens already cached, tokens to add
+ *     (negative ones count as 0);
+ *   page_table [B, W] int32, unit stride on W, updated: the first
+ *     ceil(context / page_size) entries of a row are its pages;
+ *   free_pages [F] int32: pages handed out in this order.
+ * Requests take ceil((context+new) / page_size) - ceil(context / page_size)
+ * pages each, in request order, appended to their rows; other entries are not
+ * written.  Outputs:
+ *   seq_lens [B] int32 = context + new;
+ *   token_offsets [B+1] int32: first token of each request, then their number;
+ *   positions [T] int32, slots [T] int64: of the new tokens, request after
+ *     request; entries past the last token get position 0 and slot -1;
+ *   totals [2] int32: pages wanted, tokens.
+ * totals[0] > F says that the pool was too small: entries past it are -1, and
+ * so are the slots of tokens on such pages or past the table's last column.
+ * totals[1] > T says that T was too small: the tokens past it are left out.
+ * Sums past 2^31 - 1 are given as 2^31 - 1.  Calling again with the same
+ * operands writes the same values.
+ */
+bi_status bi_paged_plan(const bi_tensor* context_lens, const bi_tensor* new_lens,
+                        const bi_tensor* page_table, const bi_tensor* free_pages, int32_t page_size,
+                        const bi_tensor* seq_lens, const bi_tensor* token_offsets,
+                        const bi_tensor* positions, const bi_tensor* slots, const bi_tensor* totals,
+                        bi_stream stream);
+
+/*
+ * Rotary positions.  Pair i of a head at position n is turned by n * f_i:
+ *   y1 = a (x1 cos - x2 sin),  y2 = a (x1 sin + x2 cos),   i < rotary_dim / 2,
+ * with (x1, x2) the elements (i, i + rotary_dim/2) of the head, or (2i, 2i+1)
+ * when interleaved; elements from rotary_dim on are copied.  a = magnitude.
+ * A configuration is host memory that a program fills once; calls copy it.
+ * Angles are exact to the fp32 rounding of the reduced angle at any position
+ * (the product n * f_i is taken modulo one turn in 64-bit integers).
+ */
+#define BI_ROPE_MAX_PAIRS 128
+
+typedef enum {
+  BI_ROPE_PLAIN = 0,       /* f_i = base^(-2i / rotary_dim) */
+  BI_ROPE_LINEAR = 1,      /* f_i / factor */
+  BI_ROPE_BASE = 2,        /* base * factor^(R / (R - 2)) in base's place, R = rotary_dim > 2 */
+  BI_ROPE_RAMP_TURNS = 3,  /* f_i (g + (1 - g) / factor), g = clamp((r - low) / (high - low), 0, 1),
+                              r = original_length f_i / (2 pi): turns over the original length */
+  BI_ROPE_RAMP_INDEX = 4   /* the same with g = 1 - clamp((i - i_high) / (i_low - i_high), 0, 1),
+                              i_high = max(floor(idx(high)), 0), i_low = min(ceil(idx(low)), R - 1),
+                              idx(r) = R ln(original_length / (2 pi r)) / (2 ln base) */
+} bi_rope_scaling_kind;
+
+typedef struct {
+  int32_t kind;            /* a bi_rope_scaling_kind */
+  int32_t reserved;        /* 0 */
+  double factor;           /* > 0 */
+  double original_length;  /* > 0, the two ramps */
+  double low, high;        /* 0 < low < high in turns, the two ramps */
+} bi_rope_scaling;
+
+typedef struct {
+  int32_t rotary_dim;                /* even, 2 .. 2 * BI_ROPE_MAX_PAIRS */
+  int32_t interleaved;               /* 0 or 1 */
+  float magnitude;                   /* a */
+  int32_t reserved;
+  uint64_t phase[BI_ROPE_MAX_PAIRS]; /* 2^64 * (f_i / (2 pi) mod 1) */
+} bi_rope_config;
+
+/* Fills *out; scaling may be NULL (plain).  base > 1; magnitude finite.  Host only. */
+bi_status bi_rope_init(bi_rope_config* out, int32_t rotary_dim, int32_t interleaved, double base,
+                       const bi_rope_scaling* scaling, double magnitude);
+/* The same with the rotary_dim / 2 angular frequencies given (finite). */
+bi_status bi_rope_init_frequencies(bi_rope_config* out, int32_t rotary_dim, int32_t interleaved,
+                                   const double* frequencies, double magnitude);
+
+/*
+ * y = rotate(x):  x, y [T,H,D] bf16, fp16 or fp32 (each its own type), unit
+ * stride on D; positions [T] int32 or int64, of any value; rotary_dim <= D <=
+ * 1024.  transpose != 0 applies the transposed map (angles negated, the
+ * magnitude kept): the gradient with respect to x of bi_rope.  Arithmetic in
+ * fp32, one rounding to y's type.  y may be x itself (same pointer, strides
+ * and type); other overlaps are refused.  Rows and heads that are multiples of
+ * 16 bytes, with rotary_dim / 2 a multiple of 8 and D - rotary_dim of 16, run
+ * a wider kernel with the same bits.
+ */
+bi_status bi_rope(const bi_rope_config* config, const bi_tensor* x, const bi_tensor* positions,
+                  int32_t transpose, const bi_tensor* y, bi_stream stream);
+
+/*
+ * Writes a step's keys and values into the cache: for every token t with
+ * slots[t] >= 0, k_cache[slot] = rotate(k[t]) and v_cache[slot] = v[t]; and,
+ * when q is given, q_out[t] = rotate(q[t]) for every t (stored or not).
+ *   config NULL: nothing is rotated, q and positions must be absent;
+ *   positions [T] int32 or int64; slots [T] int64, negative: not stored;
+ *   k, v [T,Hkv,D] of one type, q [T,Hq,D]; q_out [T,Hq,D] of any of the three
+ *   types (may be q itself, as in bi_rope); k_cache, v_cache
+ *   [P,page_size,Hkv,D] of one type, bf16, fp16 or fp32; unit strides on D;
+ *   P * page_size < 2^31.
+ * Slots must be distinct: which of two tokens with one slot is kept is not
+ * specified.  Cache rows that no token names are left as they were.
+ */
+bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* positions,
+                         const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
+                         const bi_tensor* k, const bi_tensor* v, const bi_tensor* k_cache,
+                         const bi_tensor* v_cache, bi_stream stream);
+
+/*
+ * Attention of one new token per request over its cached keys and values:
+ *   o[b,h,:] = sum_j softmax_j(scale * q[b,h,:] . k_j) v_j,  j < seq_lens[b],
+ * k_j and v_j the cache rows of token j for key-value head h / (Hq / Hkv).
+ *   q [B,Hq,D] bf16 or fp16; k_cache, v_cache [P,page_size,Hkv,D] of q's type;
+ *   o [B,Hq,D] fp32, bf16 or fp16;  Hkv divides Hq;  D = 64, 128 or 256;
+ *   page_table [B,W] int32, unit stride on W; seq_lens [B] int32; any
+ *   page_size >= 1 with P * page_size < 2^31 and W * page_size <= 2^30.
+ *   q, caches and o: unit stride on D, 16-byte aligned, other strides
+ *   multiples of 16 bytes.  scale finite.
+ * A request of length <= 0 gives zeros (the new token itself is normally in
+ * the cache by then).  A length past W * page_size counts as W * page_size,
+ * keys on a page outside [0, P) as absent; both are reported.  Rows past a
+ * request's length are never read.
+ *
+ * Order: a request of n keys is cut into pieces of s = 256 * 2^k keys, k the
+ * least with n <= 128 s -- a rule on its own length.  In a piece, warp w of 8
+ * takes the 16-key tiles w, w + 8, ... in order with a running maximum; p =
+ * 2^(t - m), t = RN(score * RN(scale log2 e)); warps, then pieces, are joined
+ * in fixed order in fp32.  Sums are of the unrounded p; the product with v
+ * takes p rounded to the cache's type, or for an fp32 o the sum of two such
+ * numbers.
+ *
+ * workspace: caller-owned, 16-byte aligned, at least
+ * bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes -- 0 when
+ * W * page_size <= 256, else B * Hq * min(ceil(W * page_size / 256), 128) *
+ * (D + 2) * 4.  Scratch, as in bi_attention_ws.
+ */
+int64_t bi_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len);
+bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const bi_tensor* v_cache,
+                             const bi_tensor* page_table, const bi_tensor* seq_lens, float scale,
+                             const bi_tensor* o, void* workspace, int64_t workspace_bytes,
+                             bi_stream stream);
+
+/*
+ * Log probabilities of given tokens, entropies and the best alternatives of
+ * each row of logits [R,N] (bf16, fp16 or fp32, unit stride on N, N <= 2^24):
+ *   mx, lse as in bi_log_softmax_lastdim, in its order;
+ *   logprobs[r] = RN(RN(x[r,tok] - mx) - lse): bit for bit the element that
+ *     bi_log_softmax_lastdim gives; tokens [R] int32 or int64; a token outside
+ *     [0, N) has probability zero: -inf;
+ *   entropy[r] = lse - (sum_j e_j (x_j - mx)) / (sum_j e_j), e_j = expf(x_j - mx),
+ *     terms with e_j = 0 counting as 0 (forbidden tokens at -inf);
+ *   top_ids[r,:K] the K tokens of the largest logits, largest first, the lower
+ *     index first among equals (a NaN counts as larger than any number);
+ *     top_logprobs[r,:] their log probabilities.
+ * logprobs, entropy fp32 [R]; top_ids int32 and top_logprobs fp32 [R,K], all
+ * contiguous; entropy may be NULL; top_ids and top_logprobs are given together
+ * or not at all, K <= 64 and K <= N.  A row that holds a NaN or +inf, or
+ * nothing but -inf, has NaN log probabilities and entropy (the ids stand).
+ */
+bi_status bi_token_logprobs(const bi_tensor* logits, const bi_tensor* tokens,
+                            const bi_tensor* logprobs, const bi_tensor* entropy,
+                            const bi_tensor* top_logprobs, const bi_tensor* top_ids,
+                            bi_stream stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side status word
- * of the current device: BI_OK, or BI_ERR_TIMEOUT when a kernel's bounded
- * wait ran out since the last call (detail in bi_last_error_message()).
+ * of the current device: BI_OK, BI_ERR_TIMEOUT when a kernel's bounded wait
+ * ran out since the last call, or BI_ERR_INVALID_ARG when a serving operation
+ * met a slot, page or length that does not exist (detail in
+ * bi_last_error_message()).
  */
 bi_status bi_device_status(bi_stream stream);
 

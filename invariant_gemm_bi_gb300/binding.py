@@ -10,7 +10,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -30,10 +32,13 @@ EXPORTED = ("bi_mm", "bi_addmm", "bi_bmm", "bi_conv2d_patch", "bi_softmax_lastdi
             "bi_attention_workspace_bytes", "bi_attention_ws", "bi_attention_noalloc",
             "bi_packed_weight_bytes", "bi_pack_weight", "bi_addmm_packed",
             "bi_conv_packed_weight_bytes", "bi_conv_pack_weight", "bi_conv2d_patch_packed",
+            "bi_paged_plan", "bi_rope_init", "bi_rope_init_frequencies", "bi_rope", "bi_paged_store",
+            "bi_paged_attention", "bi_paged_attention_workspace_bytes", "bi_token_logprobs",
             "bi_device_status", "bi_debug_expire_wait", "bi_status_string",
             "bi_last_error_message", "bi_abi_version")
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_INDEX_DTYPES = {torch.int32: 3, torch.int64: 4}  # index operands of the serving operations
 
 
 class BiTensor(ctypes.Structure):
@@ -51,6 +56,16 @@ class BiConvPackedWeightDesc(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("bytes", ctypes.c_int64), ("Co", ctypes.c_int64),
                 ("C", ctypes.c_int64), ("KH", ctypes.c_int64), ("KW", ctypes.c_int64),
                 ("Kp", ctypes.c_int64)]
+
+
+class BiRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class BiRopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * 128)]
 
 
 class ConvPackedWeight:
@@ -105,6 +120,7 @@ def load(path: str | None = None):
             ptr = ctypes.POINTER(BiTensor)
             i32x2 = ctypes.POINTER(ctypes.c_int32)
             st = ctypes.c_int
+            vp = ctypes.c_void_p
             sig = {
                 "bi_mm": ([ptr, ptr, ptr, ctypes.c_void_p], st),
                 "bi_addmm": ([ptr, ptr, ptr, ptr, ctypes.c_void_p], st),
@@ -130,6 +146,15 @@ def load(path: str | None = None):
                                          ctypes.POINTER(BiConvPackedWeightDesc), ctypes.c_void_p], st),
                 "bi_conv2d_patch_packed": ([ptr, ctypes.POINTER(BiConvPackedWeightDesc), ptr, ptr,
                                             ctypes.c_void_p], st),
+                # descriptors as c_void_p: byref(BiTensor) or a packed BiTensor's bytes
+                "bi_paged_plan": ([vp] * 4 + [ctypes.c_int32] + [vp] * 6, st),
+                "bi_rope_init": ([vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_double, vp, ctypes.c_double], st),
+                "bi_rope_init_frequencies": ([vp, ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_double], st),
+                "bi_rope": ([vp, vp, vp, ctypes.c_int32, vp, vp], st),
+                "bi_paged_store": ([vp] * 10, st),
+                "bi_paged_attention": ([vp] * 5 + [ctypes.c_float, vp, vp, ctypes.c_int64, vp], st),
+                "bi_paged_attention_workspace_bytes": ([ctypes.c_int64] * 4, ctypes.c_int64),
+                "bi_token_logprobs": ([vp] * 7, st),
                 "bi_device_status": ([ctypes.c_void_p], st),
                 "bi_debug_expire_wait": ([ctypes.c_uint64, ctypes.c_void_p], st),
                 "bi_status_string": ([st], ctypes.c_char_p),
@@ -405,6 +430,257 @@ def bi_conv2d_patch_packed(x: torch.Tensor, w: ConvPackedWeight, bias: torch.Ten
     dx, db, dy = _desc(x, "x"), _desc(bias, "bias"), _desc(out, "out")
     _check(lib, "bi_conv2d_patch_packed",
            lib.bi_conv2d_patch_packed(_ref(dx), ctypes.byref(w.desc), _ref(db), _ref(dy), _stream(stream)))
+    return out
+
+
+# -- serving operations around a paged key-value cache --------------------------
+#
+# A decode step makes several of these calls a layer, so their descriptors are
+# packed straight into bytes (a BiTensor's layout) instead of through ctypes
+# fields.
+
+_PACK = tuple(struct.Struct(f"@Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack for n in range(5))
+assert struct.calcsize("@Pii8q") == ctypes.sizeof(BiTensor)
+
+
+def _packed(t: torch.Tensor | None, name: str, device, index: bool = False) -> bytes | None:
+    """A BiTensor describing t, which must be a CUDA tensor on `device` of a
+    floating-point type (of an integer type when `index`)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    code = (_INDEX_DTYPES if index else _DTYPES).get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"{name}: rank {n} > 4")
+    return _PACK[n](t.data_ptr(), n, code, *t.shape, *t.stride())
+
+
+def _call_device(t: torch.Tensor, name: str):
+    """The device a call runs on: that of its leading operand, which must be
+    the current CUDA device (the library launches there)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    d = t.device
+    if d.type != "cuda":
+        raise ValueError(f"{name}: expected a CUDA tensor, got {d}")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {d}, but the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _stream_ptr(stream, device) -> int:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"stream on {s.device}, operands on {device}")
+    return s.cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output or workspace, allocated for the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class PagedPlan(NamedTuple):
+    """What bi_paged_plan writes besides the page table."""
+    seq_lens: torch.Tensor       # [B] int32: context + new
+    token_offsets: torch.Tensor  # [B + 1] int32
+    positions: torch.Tensor      # [T] int32
+    slots: torch.Tensor          # [T] int64, -1 past the last token
+    totals: torch.Tensor         # [2] int32: pages wanted, tokens
+
+
+def bi_paged_plan_buffers(batch: int, num_tokens: int, device="cuda") -> PagedPlan:
+    """Output buffers of bi_paged_plan for a batch and a token capacity, to be kept over steps."""
+    def i32(n):
+        return torch.empty(n, dtype=torch.int32, device=device)
+    return PagedPlan(i32(batch), i32(batch + 1), i32(num_tokens),
+                     torch.empty(num_tokens, dtype=torch.int64, device=device), i32(2))
+
+
+def bi_paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor,
+                  free_pages: torch.Tensor, page_size: int, num_tokens: int | None = None,
+                  out: PagedPlan | None = None, stream=None) -> PagedPlan:
+    """Extends page_table [B, W] in place with pages of free_pages for new_lens more
+    tokens a request, and gives lengths, token offsets, positions and cache slots of
+    the new tokens.  num_tokens: capacity of the token outputs (the tokens' number, or
+    more for a padded buffer); not needed when `out` is given."""
+    lib = load()
+    dev = _call_device(page_table, "page_table")
+    if out is None:
+        if num_tokens is None:
+            raise ValueError("bi_paged_plan: num_tokens or out is needed")
+        with torch.cuda.stream(stream):
+            out = bi_paged_plan_buffers(page_table.shape[0], int(num_tokens), dev)
+    _check(lib, "bi_paged_plan", lib.bi_paged_plan(
+        _packed(context_lens, "context_lens", dev, True), _packed(new_lens, "new_lens", dev, True),
+        _packed(page_table, "page_table", dev, True), _packed(free_pages, "free_pages", dev, True), int(page_size),
+        _packed(out.seq_lens, "seq_lens", dev, True), _packed(out.token_offsets, "token_offsets", dev, True),
+        _packed(out.positions, "positions", dev, True), _packed(out.slots, "slots", dev, True),
+        _packed(out.totals, "totals", dev, True), _stream_ptr(stream, dev)))
+    return out
+
+
+_ROPE_KINDS = {"linear": 1, "base": 2, "ramp_turns": 3, "ramp_index": 4}
+
+
+class RopeScaling:
+    """Frequency scaling for contexts longer than a model was trained on: "linear",
+    "base", "ramp_turns" or "ramp_index" (formulas in include/bi.h)."""
+
+    def __init__(self, kind: str, factor: float, original_length: float = 0.0, low: float = 0.0, high: float = 0.0):
+        if kind not in _ROPE_KINDS:
+            raise ValueError(f"RopeScaling: unknown kind {kind!r}")
+        self.desc = BiRopeScaling(_ROPE_KINDS[kind], 0, factor, original_length, low, high)
+
+
+class RopeConfig:
+    """A rotary configuration (host memory), from bi_rope_config."""
+
+    def __init__(self, desc: BiRopeConfig):
+        self.desc = desc
+        self._ref = ctypes.byref(desc)
+
+    @property
+    def rotary_dim(self) -> int:
+        return int(self.desc.rotary_dim)
+
+    @property
+    def interleaved(self) -> bool:
+        return bool(self.desc.interleaved)
+
+
+def bi_rope_config(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+                   scaling: RopeScaling | None = None, magnitude: float = 1.0, frequencies=None) -> RopeConfig:
+    """The rotary configuration of rotary_dim rotated elements a head: frequencies
+    base^(-2i / rotary_dim), scaled by `scaling`, or the rotary_dim / 2 angular
+    `frequencies` given (a sequence of floats; base and scaling are not used then)."""
+    lib = load()
+    desc = BiRopeConfig()
+    if frequencies is not None:
+        f = [float(x) for x in frequencies]
+        if len(f) != int(rotary_dim) // 2:
+            raise ValueError(f"bi_rope_config: expected {int(rotary_dim) // 2} frequencies, got {len(f)}")
+        arr = (ctypes.c_double * max(len(f), 1))(*f)
+        st = lib.bi_rope_init_frequencies(ctypes.byref(desc), int(rotary_dim), int(bool(interleaved)), arr,
+                                          float(magnitude))
+    else:
+        st = lib.bi_rope_init(ctypes.byref(desc), int(rotary_dim), int(bool(interleaved)), float(base),
+                              ctypes.byref(scaling.desc) if scaling is not None else None, float(magnitude))
+    _check(lib, "bi_rope_config", st)
+    return RopeConfig(desc)
+
+
+def bi_rope(x: torch.Tensor, positions: torch.Tensor, config: RopeConfig, backward: bool = False,
+            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of x [T, H, D] at positions [T] (output in x's dtype unless
+    out / out_dtype says otherwise; out may be x).  backward: the transposed map,
+    which takes the gradient of the result to the gradient of x."""
+    lib = load()
+    dev = _call_device(x, "x")
+    if out is None:
+        out = _empty(x.shape, out_dtype or x.dtype, dev, stream)
+    _check(lib, "bi_rope", lib.bi_rope(
+        config._ref, _packed(x, "x", dev), _packed(positions, "positions", dev, True), int(bool(backward)),
+        _packed(out, "out", dev), _stream_ptr(stream, dev)))
+    return out
+
+
+def bi_paged_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                   config: RopeConfig | None = None, q_out: torch.Tensor | None = None,
+                   q_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor | None:
+    """Writes k, v [T, Hkv, D] into the caches [P, page_size, Hkv, D] at slots [T]
+    (negative: not stored).  With a rotary `config` and positions, k is rotated on
+    the way and q [T, Hq, D], when given, is rotated into q_out (allocated in q_dtype,
+    or the caches' dtype, when not given), which is returned."""
+    lib = load()
+    dev = _call_device(k, "k")
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, q_dtype or k_cache.dtype, dev, stream)
+    _check(lib, "bi_paged_store", lib.bi_paged_store(
+        config._ref if config is not None else None, _packed(positions, "positions", dev, True),
+        _packed(slots, "slots", dev, True), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
+        _packed(k, "k", dev), _packed(v, "v", dev), _packed(k_cache, "k_cache", dev),
+        _packed(v_cache, "v_cache", dev), _stream_ptr(stream, dev)))
+    return q_out
+
+
+def bi_paged_attention_workspace_bytes(B: int, Hq: int, D: int, max_len: int) -> int:
+    """Workspace of bi_paged_attention for B requests of Hq query heads and page tables
+    that name up to max_len keys a request."""
+    return int(load().bi_paged_attention_workspace_bytes(int(B), int(Hq), int(D), int(max_len)))
+
+
+def bi_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                       seq_lens: torch.Tensor, scale: float, out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Attention of one new token per request, q [B, Hq, D], over the first seq_lens[b]
+    keys of its pages page_table[b] in the caches [P, page_size, Hkv, D]; returns
+    [B, Hq, D] (fp32 unless out / out_dtype).  A workspace of
+    bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes is allocated
+    here when one is needed and not given."""
+    lib = load()
+    dev = _call_device(q, "q")
+    if out is None:
+        out = _empty(q.shape, out_dtype, dev, stream)
+    ws = 0
+    wbytes = 0
+    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and page_table.dim() == 2:
+        need = lib.bi_paged_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2],
+                                                      page_table.shape[1] * k_cache.shape[1])
+        if need > 0:
+            workspace = _empty(need, torch.uint8, dev, stream)
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
+        ws, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib, "bi_paged_attention", lib.bi_paged_attention(
+        _packed(q, "q", dev), _packed(k_cache, "k_cache", dev), _packed(v_cache, "v_cache", dev),
+        _packed(page_table, "page_table", dev, True), _packed(seq_lens, "seq_lens", dev, True), float(scale),
+        _packed(out, "out", dev), ws or None, wbytes, _stream_ptr(stream, dev)))
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    """What bi_token_logprobs gives for each row."""
+    logprobs: torch.Tensor             # [R] fp32
+    entropy: torch.Tensor | None       # [R] fp32
+    top_logprobs: torch.Tensor | None  # [R, top] fp32, largest first
+    top_ids: torch.Tensor | None       # [R, top] int32
+
+
+def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, entropy: bool = True,
+                      out: TokenLogprobs | None = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of tokens [R] under logits [R, N], each row's entropy, and its
+    `top` most likely tokens with their log probabilities.  With `out`, its buffers are
+    written (those that are None are not computed; top and entropy are not used)."""
+    lib = load()
+    dev = _call_device(logits, "logits")
+    if out is None:
+        if logits.dim() != 2:
+            raise ValueError(f"logits: expected rank 2, got {logits.dim()}")
+        R = logits.shape[0]
+        out = TokenLogprobs(
+            _empty(R, torch.float32, dev, stream),
+            _empty(R, torch.float32, dev, stream) if entropy else None,
+            _empty((R, int(top)), torch.float32, dev, stream) if top > 0 else None,
+            _empty((R, int(top)), torch.int32, dev, stream) if top > 0 else None)
+    _check(lib, "bi_token_logprobs", lib.bi_token_logprobs(
+        _packed(logits, "logits", dev), _packed(tokens, "tokens", dev, True), _packed(out.logprobs, "logprobs", dev),
+        _packed(out.entropy, "entropy", dev), _packed(out.top_logprobs, "top_logprobs", dev),
+        _packed(out.top_ids, "top_ids", dev, True), _stream_ptr(stream, dev)))
     return out
 
 

@@ -12,6 +12,7 @@
 #include "../../include/bi.h"
 #include "bi_common.h"
 #include "bi_launch.h"
+#include "bi_serve.h"
 
 // First device-side failure since the last bi_device_status() (0 = none).
 __device__ unsigned int g_bi_status_word;
@@ -41,8 +42,8 @@ struct DevState {
   std::string why;
   int num_sms = 0;
   unsigned int* status_word = nullptr;
-  bool smem_set[24] = {};
-  int pairs[24] = {};  // resident 2-CTA clusters per kernel slot (0: not yet asked)
+  bool smem_set[48] = {};
+  int pairs[48] = {};  // resident 2-CTA clusters per kernel slot (0: not yet asked)
   void* scratch = nullptr;  // device address of g_bi_noalloc_scratch (0: not yet asked)
 };
 DevState g_dev[kMaxDevices];
@@ -82,6 +83,8 @@ bi_status finish(bi_status st, const std::string& why) {
 }
 
 }  // namespace
+
+bi_status abi_finish(bi_status st, const std::string& why) { return finish(st, why); }
 
 bi_status current_device_info(DeviceInfo* info, std::string* why) {
   int dev = -1;
@@ -1033,9 +1036,12 @@ extern "C" bi_status bi_device_status(bi_stream stream) {
   static const char* kSites[] = {"?", "producer waiting for a free stage", "MMA waiting for a full stage",
                                  "MMA waiting for a free accumulator", "epilogue waiting for an accumulator",
                                  "draining in-flight work", "debug wait", "conv producer waiting for a free stage",
-                                 "weight packer waiting for its tile", "attention softmax waiting"};
+                                 "weight packer waiting for its tile", "attention softmax waiting",
+                                 "a cache slot past the cache's end",
+                                 "a page outside the cache, or a length past the page table"};
   const unsigned site = (v >> 8) & 0xFF;
-  why = std::string("device wait ran out: ") +
+  why = std::string(site == kSitePagedSlot || site == kSitePagedPage ? "bad index on the device: "
+                                                                     : "device wait ran out: ") +
         (site < sizeof(kSites) / sizeof(kSites[0]) ? kSites[site] : "?");
   return finish((bi_status)(v & 0xFF), why);
 }

@@ -39,6 +39,8 @@ enum : unsigned int {
   kSiteConvProducer = 7,
   kSitePack = 8,
   kSiteAttnSoftmax = 9,
+  kSitePagedSlot = 10,  // a token's cache slot does not exist
+  kSitePagedPage = 11,  // a page or a length that the table does not have
 };
 __host__ __device__ constexpr unsigned int status_code(unsigned int bi_err, unsigned int site) {
   return bi_err | (site << 8);
