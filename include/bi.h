@@ -517,12 +517,14 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  * request's length are never read.
  *
  * Order: a request of n keys is cut into pieces of s = 256 * 2^k keys, k the
- * least with n <= 128 s -- a rule on its own length.  In a piece, warp w of 8
- * takes the 16-key tiles w, w + 8, ... in order with a running maximum; p =
- * 2^(t - m), t = RN(score * RN(scale log2 e)); warps, then pieces, are joined
- * in fixed order in fp32.  Sums are of the unrounded p; the product with v
- * takes p rounded to the cache's type, or for an fp32 o the sum of two such
- * numbers.
+ * least with n <= 128 s -- a rule on its own length.  In a piece, warp w of W
+ * takes the tiles w, w + W, ... in order with a running maximum (tiles of 32
+ * keys, 16 at D = 256; W = 4, or 8 at D = 256 and, for more than 8 query heads
+ * a key-value head, at D = 128); p = 2^(t - m), t = RN(score * RN(scale
+ * log2 e)).  Warp w + W/2 is joined into warp w, then warps 1, 2, ... into
+ * warp 0, groups of 16 pieces in piece order, then the groups in order, all in
+ * fp32.  Sums are of the unrounded p; the product with v takes p rounded to the
+ * cache's type, or for an fp32 o the sum of two such numbers.
  *
  * workspace: caller-owned, 16-byte aligned, at least
  * bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes -- 0 when

@@ -85,6 +85,7 @@ struct PagedAttnParams {
   int32_t head_tiles;    // tiles of query heads per key-value head
   int32_t max_splits;
   int32_t cap;           // keys a table row can name: min(W * ps, INT32_MAX)
+  int32_t ps_shift;      // log2(ps), or -1 when ps is no power of two
   int32_t in_f16, out_kind;
   float score_log2;      // scale * log2(e), rounded once to fp32
   unsigned int* status_word;

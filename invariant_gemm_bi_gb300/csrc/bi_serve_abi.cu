@@ -471,7 +471,7 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   for (int i = 0; i < 5; ++i) c.apart(o, in[i], "bi_paged_attention");
   if (!c.ok() || B == 0 || Hq == 0) return abi_finish(c.st, c.why);
   const int64_t cap = W * ps, need = bi_paged_attention_workspace_bytes(B, Hq, D, cap);
-  c.that(B * Hq <= INT32_MAX && B <= (1 << 23), BI_ERR_INVALID_ARG, "too many requests");
+  c.that(B * Hq * (D / 64) <= INT32_MAX && B <= (1 << 22), BI_ERR_INVALID_ARG, "too many requests");
   c.that(!workspace || on(workspace, 16), BI_ERR_UNSUPPORTED_LAYOUT, "the workspace must be 16-byte aligned");
   c.that(need == 0 || (workspace && workspace_bytes >= need), BI_ERR_INVALID_ARG,
          "key ranges of up to " + std::to_string(cap) + " need a workspace of " + std::to_string(need) +
@@ -501,6 +501,7 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   p.B = (int32_t)B, p.Hq = (int32_t)Hq, p.Hkv = (int32_t)Hkv, p.D = (int32_t)D;
   p.W = (int32_t)W, p.ps = (int32_t)ps, p.P = (int32_t)P, p.cap = (int32_t)cap;
   p.group = (int32_t)(Hq / Hkv);
+  p.ps_shift = (ps & (ps - 1)) == 0 ? __builtin_ctzll((unsigned long long)ps) : -1;
   p.in_f16 = q->dtype == BI_F16;
   p.out_kind = kind_of(o->dtype);
   p.score_log2 = (float)((double)scale * 1.4426950408889634);
