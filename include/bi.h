@@ -540,12 +540,10 @@ bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const
 /*
  * Log probabilities of given tokens, entropies and the best alternatives of
  * each row of logits [R,N] (bf16, fp16 or fp32, unit stride on N, N <= 2^24):
- *   mx, lse as in bi_log_softmax_lastdim, in its order;
- *   logprobs[r] = RN(RN(x[r,tok] - mx) - lse): bit for bit the element that
- *     bi_log_softmax_lastdim gives; tokens [R] int32 or int64; a token outside
- *     [0, N) has probability zero: -inf;
- *   entropy[r] = lse - (sum_j e_j (x_j - mx)) / (sum_j e_j), e_j = expf(x_j - mx),
- *     terms with e_j = 0 counting as 0 (forbidden tokens at -inf);
+ *   logprobs[r] = RN(RN(x[r,tok] - M) - lse), M the row's maximum and lse =
+ *     ln sum_j e^(x_j - M); tokens [R] int32 or int64; a token outside [0, N)
+ *     has probability zero: -inf;
+ *   entropy[r] = -sum_j p_j ln p_j, forbidden tokens (-inf) adding 0;
  *   top_ids[r,:K] the K tokens of the largest logits, largest first, the lower
  *     index first among equals (a NaN counts as larger than any number);
  *     top_logprobs[r,:] their log probabilities.
@@ -553,6 +551,15 @@ bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const
  * contiguous; entropy may be NULL; top_ids and top_logprobs are given together
  * or not at all, K <= 64 and K <= N.  A row that holds a NaN or +inf, or
  * nothing but -inf, has NaN log probabilities and entropy (the ids stand).
+ *
+ * Order: 256 threads; slices of 16 KB of the row, of which thread t has the
+ * 16-byte units t, t + 256, t + 512, t + 768, reduced relative to their own
+ * maximum (sums of 2^(x log2 e - m), one fused multiply-add and the SFU's 2^x);
+ * with s slices, groups of ceil(s / 8) are joined in slice order, then the
+ * groups, then the lanes, then the warps by fixed trees -- by N and the type
+ * alone, whatever the number of rows and the rows' alignment.  One pass: the
+ * log probabilities agree with bi_log_softmax_lastdim's, which takes its sum in
+ * another order and from expf, within rounding, not bit for bit.
  */
 bi_status bi_token_logprobs(const bi_tensor* logits, const bi_tensor* tokens,
                             const bi_tensor* logprobs, const bi_tensor* entropy,

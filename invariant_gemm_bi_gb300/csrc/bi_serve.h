@@ -104,7 +104,8 @@ struct LogprobParams {
   float* top_lp;       // [R][K] contiguous or null
   int32_t* top_ids;    // [R][K]
   int64_t R, N, ld_x;
-  int32_t K, tok64, x_kind, cl;
+  int32_t K, tok64, x_kind;
+  int32_t cl;  // CTAs a row (set by the launcher)
 };
 bi_status launch_logprobs(const LogprobParams& p, cudaStream_t stream, std::string* why);
 

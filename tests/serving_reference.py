@@ -170,17 +170,20 @@ def logprobs(x, tokens, top):
             if R else np.zeros((0, top), np.int64)
         tlp = np.take_along_axis(logp, ids, -1) if R else np.zeros((0, top))
 
-        # expf is good to 2^-22; a thread's chain is at most 64 chunks of 64 adds only for
-        # rows of 2^24, 256 adds for the rows tested, with 5 + 32 + 8 joining: 2^-15 of S.
-        # z is rounded to 2^-24 |z|, which also changes its exponential by that much.
+        # 2^x is good to 2^-21.  Its argument is one rounding of x log2 e - m', so off by
+        # 2^-24 |z| log2 e, and log2 e by 2^-26 of itself: 2^-22 |z| in the exponential.  A
+        # sum goes through at most 16 adds of a chunk, 8 joins of groups and 9 of lanes and
+        # warps, in rows of up to 8 slices a group (longer ones add one join a slice), three
+        # roundings each: 2^-24 * 100 < 2^-17.  Rows out of the ordinary take expf and up to
+        # 600 adds a thread: 2^-24 * 640 < 2^-14.6 at N = 300001.  2^-14 covers both.
         spread = np.where(e > 0, e * np.abs(z), 0.0).sum(-1) / S[:, 0]
         square = np.where(e > 0, e * z * z, 0.0).sum(-1) / S[:, 0]
-        d_lse = 2.0 ** -15 + 2.0 ** -24 * spread + 2.0 ** -22 * np.abs(np.log(S[:, 0]))
+        d_lse = 2.0 ** -14 + 2.0 ** -22 * spread + 2.0 ** -22 * np.abs(np.log(S[:, 0]))
 
         def lp_bound(v):  # z's, the subtraction's and the result's roundings
             return d_lse.reshape((-1,) + (1,) * (v.ndim - 1)) + 2.0 ** -23 * np.abs(np.where(np.isfinite(v), v, 0.0)) + \
                 2.0 ** -23 * np.abs(np.log(S)).reshape((-1,) + (1,) * (v.ndim - 1))
-        ent_bound = d_lse + 2.0 ** -14 * spread + 2.0 ** -24 * square + 2.0 ** -23 * np.abs(ent)
+        ent_bound = d_lse + 2.0 ** -13 * spread + 2.0 ** -21 * square + 2.0 ** -23 * np.abs(ent)
     return lp, ent, tlp, ids, lp_bound(lp), ent_bound, lp_bound(tlp)
 
 
