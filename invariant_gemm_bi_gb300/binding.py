@@ -437,56 +437,70 @@ def bi_conv2d_patch_packed(x: torch.Tensor, w: ConvPackedWeight, bias: torch.Ten
 #
 # A decode step makes several of these calls a layer, so their descriptors are
 # packed straight into bytes (a BiTensor's layout) instead of through ctypes
-# fields.
+# fields, and devices and streams are compared as numbers.
 
 _PACK = tuple(struct.Struct(f"@Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack for n in range(5))
 assert struct.calcsize("@Pii8q") == ctypes.sizeof(BiTensor)
+# The current stream's handle without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _packed(t: torch.Tensor | None, name: str, device, index: bool = False) -> bytes | None:
-    """A BiTensor describing t, which must be a CUDA tensor on `device` of a
-    floating-point type (of an integer type when `index`)."""
-    if t is None:
-        return None
+def _refuse(t, name: str, device: int, table) -> None:
+    """Raises for an operand that _packed cannot describe."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    code = (_INDEX_DTYPES if index else _DTYPES).get(t.dtype)
-    if code is None:
+    if t.dtype not in table:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    n = t.dim()
-    if n > 4:
-        raise ValueError(f"{name}: rank {n} > 4")
-    return _PACK[n](t.data_ptr(), n, code, *t.shape, *t.stride())
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name}: rank {t.dim()} > 4")
 
 
-def _call_device(t: torch.Tensor, name: str):
+def _packed(t: torch.Tensor | None, name: str, device: int, table=_DTYPES) -> bytes | None:
+    """A BiTensor describing t, which must be a CUDA tensor on `device` of one of
+    the table's types."""
+    if t is None:
+        return None
+    try:
+        n = t.dim()
+        if t.get_device() == device:
+            return _PACK[n](t.data_ptr(), n, table[t.dtype], *t.shape, *t.stride())
+    except (AttributeError, IndexError, KeyError, TypeError):
+        pass
+    _refuse(t, name, device, table)
+
+
+def _index(t: torch.Tensor | None, name: str, device: int) -> bytes | None:
+    return _packed(t, name, device, _INDEX_DTYPES)
+
+
+def _call_device(t: torch.Tensor, name: str) -> int:
     """The device a call runs on: that of its leading operand, which must be
     the current CUDA device (the library launches there)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    d = t.device
-    if d.type != "cuda":
-        raise ValueError(f"{name}: expected a CUDA tensor, got {d}")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {d}, but the current device is cuda:{torch.cuda.current_device()}")
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor, got {t.device}")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{d}, but the current device is cuda:{torch.cuda.current_device()}")
     return d
 
 
-def _stream_ptr(stream, device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"stream on {s.device}, operands on {device}")
-    return s.cuda_stream
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An output or workspace, allocated for the stream that the call runs on."""
+def _stream_ptr(stream, device: int) -> int:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if stream.device.index != device:
+        raise ValueError(f"stream on {stream.device}, operands on cuda:{device}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output or workspace on like's device, allocated for the stream that the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 class PagedPlan(NamedTuple):
@@ -513,19 +527,19 @@ def bi_paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, page_table
     tokens a request, and gives lengths, token offsets, positions and cache slots of
     the new tokens.  num_tokens: capacity of the token outputs (the tokens' number, or
     more for a padded buffer); not needed when `out` is given."""
-    lib = load()
+    lib = _lib or load()
     dev = _call_device(page_table, "page_table")
     if out is None:
         if num_tokens is None:
             raise ValueError("bi_paged_plan: num_tokens or out is needed")
         with torch.cuda.stream(stream):
-            out = bi_paged_plan_buffers(page_table.shape[0], int(num_tokens), dev)
+            out = bi_paged_plan_buffers(page_table.shape[0], int(num_tokens), page_table.device)
     _check(lib, "bi_paged_plan", lib.bi_paged_plan(
-        _packed(context_lens, "context_lens", dev, True), _packed(new_lens, "new_lens", dev, True),
-        _packed(page_table, "page_table", dev, True), _packed(free_pages, "free_pages", dev, True), int(page_size),
-        _packed(out.seq_lens, "seq_lens", dev, True), _packed(out.token_offsets, "token_offsets", dev, True),
-        _packed(out.positions, "positions", dev, True), _packed(out.slots, "slots", dev, True),
-        _packed(out.totals, "totals", dev, True), _stream_ptr(stream, dev)))
+        _index(context_lens, "context_lens", dev), _index(new_lens, "new_lens", dev),
+        _index(page_table, "page_table", dev), _index(free_pages, "free_pages", dev), int(page_size),
+        _index(out.seq_lens, "seq_lens", dev), _index(out.token_offsets, "token_offsets", dev),
+        _index(out.positions, "positions", dev), _index(out.slots, "slots", dev),
+        _index(out.totals, "totals", dev), _stream_ptr(stream, dev)))
     return out
 
 
@@ -584,12 +598,12 @@ def bi_rope(x: torch.Tensor, positions: torch.Tensor, config: RopeConfig, backwa
     """Rotary positions of x [T, H, D] at positions [T] (output in x's dtype unless
     out / out_dtype says otherwise; out may be x).  backward: the transposed map,
     which takes the gradient of the result to the gradient of x."""
-    lib = load()
+    lib = _lib or load()
     dev = _call_device(x, "x")
     if out is None:
-        out = _empty(x.shape, out_dtype or x.dtype, dev, stream)
+        out = _empty(x.shape, out_dtype or x.dtype, x, stream)
     _check(lib, "bi_rope", lib.bi_rope(
-        config._ref, _packed(x, "x", dev), _packed(positions, "positions", dev, True), int(bool(backward)),
+        config._ref, _packed(x, "x", dev), _index(positions, "positions", dev), int(bool(backward)),
         _packed(out, "out", dev), _stream_ptr(stream, dev)))
     return out
 
@@ -602,13 +616,13 @@ def bi_paged_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
     (negative: not stored).  With a rotary `config` and positions, k is rotated on
     the way and q [T, Hq, D], when given, is rotated into q_out (allocated in q_dtype,
     or the caches' dtype, when not given), which is returned."""
-    lib = load()
+    lib = _lib or load()
     dev = _call_device(k, "k")
     if q is not None and q_out is None:
-        q_out = _empty(q.shape, q_dtype or k_cache.dtype, dev, stream)
+        q_out = _empty(q.shape, q_dtype or k_cache.dtype, q, stream)
     _check(lib, "bi_paged_store", lib.bi_paged_store(
-        config._ref if config is not None else None, _packed(positions, "positions", dev, True),
-        _packed(slots, "slots", dev, True), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
+        config._ref if config is not None else None, _index(positions, "positions", dev),
+        _index(slots, "slots", dev), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
         _packed(k, "k", dev), _packed(v, "v", dev), _packed(k_cache, "k_cache", dev),
         _packed(v_cache, "v_cache", dev), _stream_ptr(stream, dev)))
     return q_out
@@ -629,26 +643,26 @@ def bi_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     [B, Hq, D] (fp32 unless out / out_dtype).  A workspace of
     bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes is allocated
     here when one is needed and not given."""
-    lib = load()
+    lib = _lib or load()
     dev = _call_device(q, "q")
     if out is None:
-        out = _empty(q.shape, out_dtype, dev, stream)
+        out = _empty(q.shape, out_dtype, q, stream)
     ws = 0
     wbytes = 0
     if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and page_table.dim() == 2:
         need = lib.bi_paged_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2],
                                                       page_table.shape[1] * k_cache.shape[1])
         if need > 0:
-            workspace = _empty(need, torch.uint8, dev, stream)
+            workspace = _empty((need,), torch.uint8, q, stream)
     if workspace is not None:
-        if workspace.device != dev:
-            raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace: expected a tensor on cuda:{dev}, got {workspace.device}")
         if not workspace.is_contiguous():
             raise ValueError("workspace: expected a contiguous tensor")
         ws, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib, "bi_paged_attention", lib.bi_paged_attention(
         _packed(q, "q", dev), _packed(k_cache, "k_cache", dev), _packed(v_cache, "v_cache", dev),
-        _packed(page_table, "page_table", dev, True), _packed(seq_lens, "seq_lens", dev, True), float(scale),
+        _index(page_table, "page_table", dev), _index(seq_lens, "seq_lens", dev), float(scale),
         _packed(out, "out", dev), ws or None, wbytes, _stream_ptr(stream, dev)))
     return out
 
@@ -666,21 +680,21 @@ def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, 
     """Log probabilities of tokens [R] under logits [R, N], each row's entropy, and its
     `top` most likely tokens with their log probabilities.  With `out`, its buffers are
     written (those that are None are not computed; top and entropy are not used)."""
-    lib = load()
+    lib = _lib or load()
     dev = _call_device(logits, "logits")
     if out is None:
         if logits.dim() != 2:
             raise ValueError(f"logits: expected rank 2, got {logits.dim()}")
         R = logits.shape[0]
         out = TokenLogprobs(
-            _empty(R, torch.float32, dev, stream),
-            _empty(R, torch.float32, dev, stream) if entropy else None,
-            _empty((R, int(top)), torch.float32, dev, stream) if top > 0 else None,
-            _empty((R, int(top)), torch.int32, dev, stream) if top > 0 else None)
+            _empty((R,), torch.float32, logits, stream),
+            _empty((R,), torch.float32, logits, stream) if entropy else None,
+            _empty((R, int(top)), torch.float32, logits, stream) if top > 0 else None,
+            _empty((R, int(top)), torch.int32, logits, stream) if top > 0 else None)
     _check(lib, "bi_token_logprobs", lib.bi_token_logprobs(
-        _packed(logits, "logits", dev), _packed(tokens, "tokens", dev, True), _packed(out.logprobs, "logprobs", dev),
+        _packed(logits, "logits", dev), _index(tokens, "tokens", dev), _packed(out.logprobs, "logprobs", dev),
         _packed(out.entropy, "entropy", dev), _packed(out.top_logprobs, "top_logprobs", dev),
-        _packed(out.top_ids, "top_ids", dev, True), _stream_ptr(stream, dev)))
+        _index(out.top_ids, "top_ids", dev), _stream_ptr(stream, dev)))
     return out
 
 
