@@ -470,10 +470,6 @@ def _packed(t: torch.Tensor | None, name: str, device: int, table=_DTYPES) -> by
     _refuse(t, name, device, table)
 
 
-def _index(t: torch.Tensor | None, name: str, device: int) -> bytes | None:
-    return _packed(t, name, device, _INDEX_DTYPES)
-
-
 def _call_device(t: torch.Tensor, name: str) -> int:
     """The device a call runs on: that of its leading operand, which must be
     the current CUDA device (the library launches there)."""
@@ -535,11 +531,11 @@ def bi_paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, page_table
         with torch.cuda.stream(stream):
             out = bi_paged_plan_buffers(page_table.shape[0], int(num_tokens), page_table.device)
     _check(lib, "bi_paged_plan", lib.bi_paged_plan(
-        _index(context_lens, "context_lens", dev), _index(new_lens, "new_lens", dev),
-        _index(page_table, "page_table", dev), _index(free_pages, "free_pages", dev), int(page_size),
-        _index(out.seq_lens, "seq_lens", dev), _index(out.token_offsets, "token_offsets", dev),
-        _index(out.positions, "positions", dev), _index(out.slots, "slots", dev),
-        _index(out.totals, "totals", dev), _stream_ptr(stream, dev)))
+        _packed(context_lens, "context_lens", dev, _INDEX_DTYPES), _packed(new_lens, "new_lens", dev, _INDEX_DTYPES),
+        _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(free_pages, "free_pages", dev, _INDEX_DTYPES), int(page_size),
+        _packed(out.seq_lens, "seq_lens", dev, _INDEX_DTYPES), _packed(out.token_offsets, "token_offsets", dev, _INDEX_DTYPES),
+        _packed(out.positions, "positions", dev, _INDEX_DTYPES), _packed(out.slots, "slots", dev, _INDEX_DTYPES),
+        _packed(out.totals, "totals", dev, _INDEX_DTYPES), _stream_ptr(stream, dev)))
     return out
 
 
@@ -603,7 +599,7 @@ def bi_rope(x: torch.Tensor, positions: torch.Tensor, config: RopeConfig, backwa
     if out is None:
         out = _empty(x.shape, out_dtype or x.dtype, x, stream)
     _check(lib, "bi_rope", lib.bi_rope(
-        config._ref, _packed(x, "x", dev), _index(positions, "positions", dev), int(bool(backward)),
+        config._ref, _packed(x, "x", dev), _packed(positions, "positions", dev, _INDEX_DTYPES), int(bool(backward)),
         _packed(out, "out", dev), _stream_ptr(stream, dev)))
     return out
 
@@ -621,8 +617,8 @@ def bi_paged_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
     if q is not None and q_out is None:
         q_out = _empty(q.shape, q_dtype or k_cache.dtype, q, stream)
     _check(lib, "bi_paged_store", lib.bi_paged_store(
-        config._ref if config is not None else None, _index(positions, "positions", dev),
-        _index(slots, "slots", dev), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
+        config._ref if config is not None else None, _packed(positions, "positions", dev, _INDEX_DTYPES),
+        _packed(slots, "slots", dev, _INDEX_DTYPES), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
         _packed(k, "k", dev), _packed(v, "v", dev), _packed(k_cache, "k_cache", dev),
         _packed(v_cache, "v_cache", dev), _stream_ptr(stream, dev)))
     return q_out
@@ -662,7 +658,7 @@ def bi_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         ws, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib, "bi_paged_attention", lib.bi_paged_attention(
         _packed(q, "q", dev), _packed(k_cache, "k_cache", dev), _packed(v_cache, "v_cache", dev),
-        _index(page_table, "page_table", dev), _index(seq_lens, "seq_lens", dev), float(scale),
+        _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(seq_lens, "seq_lens", dev, _INDEX_DTYPES), float(scale),
         _packed(out, "out", dev), ws or None, wbytes, _stream_ptr(stream, dev)))
     return out
 
@@ -692,9 +688,9 @@ def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, 
             _empty((R, int(top)), torch.float32, logits, stream) if top > 0 else None,
             _empty((R, int(top)), torch.int32, logits, stream) if top > 0 else None)
     _check(lib, "bi_token_logprobs", lib.bi_token_logprobs(
-        _packed(logits, "logits", dev), _index(tokens, "tokens", dev), _packed(out.logprobs, "logprobs", dev),
+        _packed(logits, "logits", dev), _packed(tokens, "tokens", dev, _INDEX_DTYPES), _packed(out.logprobs, "logprobs", dev),
         _packed(out.entropy, "entropy", dev), _packed(out.top_logprobs, "top_logprobs", dev),
-        _index(out.top_ids, "top_ids", dev), _stream_ptr(stream, dev)))
+        _packed(out.top_ids, "top_ids", dev, _INDEX_DTYPES), _stream_ptr(stream, dev)))
     return out
 
 

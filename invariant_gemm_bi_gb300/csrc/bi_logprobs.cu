@@ -32,9 +32,9 @@
 // Alternatives.  The selection is exact, so it is free to use any order.  The
 // K-th largest, tau, of the maxima of 2 K or more groups of threads is a lower
 // bound of the K-th largest logit (K distinct elements reach it) and a close
-// one: K of 2 K groups are reached by about 1.4 K elements.  Threads whose
-// maximum reaches tau read their elements again (out of L2) and collect those
-// that do; these are ranked by counting.  Rows with more than 512 such
+// one: K of 2 K groups are reached by about 1.4 K elements.  The chunks whose
+// maximum reaches tau are read again (out of L2), all at once, and the elements
+// that do are ranked by counting.  Rows with more than 512 such
 // elements (ties) and rows with NaNs extract one element a round instead.
 #include "bi_rows.cuh"
 #include "bi_serve.h"
@@ -50,6 +50,7 @@ constexpr int kGroups = 8;       // groups of slices
 constexpr int kMaxTop = 64;
 constexpr int kMaxima = 128;     // thread groups whose maxima bound the K-th largest
 constexpr int kBuffer = 512;     // candidates
+constexpr int kHits = 1024;      // chunks that hold candidates
 constexpr float kL = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int X>
@@ -96,11 +97,12 @@ struct Shared {
   float best[kGroups][kThreads];  // the threads' maxima in each group of slices
   __align__(16) float group[kMaxima];
   Cand cand[kBuffer];
+  uint16_t hit[kHits];  // thread + kThreads * group
   uint64_t round[kWarps];
   State warp[kWarps];
   float max[kWarps];
   float tau, M, lse;
-  int count, kind;  // kind of row: kUsual, ...
+  int count, hits, kind;  // kind of row: kUsual, ...
 };
 enum : int { kUsual = 0, kNaN = 1, kUnusual = 2 };
 // The first CTA of a cluster also takes the groups' states.
@@ -234,7 +236,16 @@ __device__ __forceinline__ uint64_t order_key(float v, int j) {
   return ((uint64_t)b << 32) | (uint32_t)(~j);
 }
 
-// Collects the elements that reach tau of the thread's chunks that do.
+__device__ __forceinline__ void add_candidate(Shared& sm, float y, int j) {
+  // of the entries at -inf the first 2 kMaxTop are enough: fewer than kMaxTop of
+  // those are not at -inf, or K better elements exist
+  if (!(y > -INFINITY || j < 2 * kMaxTop)) return;
+  const int at = atomicAdd(&sm.count, 1);  // the order of the buffer does not matter
+  if (at < kBuffer) sm.cand[at] = {y, j};
+}
+// Collects the elements that reach tau, by the whole CTA: the chunks (of a
+// thread in a group of slices) whose maximum does are listed, then their units
+// are read again, a unit a thread, so that one load's latency covers them all.
 template <int X>
 __device__ __forceinline__ void collect(Shared& sm, const char* x, int N, const Cut& cut, bool ring) {
   constexpr int E = Slice<X>::E;
@@ -242,33 +253,36 @@ __device__ __forceinline__ void collect(Shared& sm, const char* x, int N, const 
   const float tau = sm.tau;
   for (int g = 0; g < cut.groups; ++g) {
     if (sm.best[g][tid] < tau) continue;
-    for (int s = g * cut.per_group; s < min(cut.slices, (g + 1) * cut.per_group); ++s) {
-      const int j0 = s * Slice<X>::kSlice + tid * E;
-      uint32_t w[kUnits][4];
+    const int at = atomicAdd(&sm.hits, 1);
+    if (at < kHits) sm.hit[at] = (uint16_t)(g * kThreads + tid);
+  }
+  __syncthreads();
+  const int hits = sm.hits;
+  if (hits > kHits) {  // nearly all: the row in order
+    for (int j = tid; j < N; j += kThreads) {
+      const float y = row_load(x, X, j);
+      if (y >= tau) add_candidate(sm, y, j);
+    }
+    return;
+  }
+  const int units = cut.per_group * kUnits;  // of a chunk
+  for (int i = tid; i < hits * units; i += kThreads) {
+    const int h = i / units, r = i - h * units, who = sm.hit[h];
+    const int s = who / kThreads * cut.per_group + r / kUnits;
+    const int j0 = s * Slice<X>::kSlice + ((r % kUnits) * kThreads + who % kThreads) * E;
+    if (j0 >= N) continue;
+    uint32_t w[4];
+    if (ring && j0 + E <= N) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)j0 * Elem<X>::kBytes));
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+      load_unit_any<X>(x, j0, N, w);
+    }
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int j = j0 + u * kThreads * E;
-        if (ring && j + E <= N) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)j * Elem<X>::kBytes));
-          w[u][0] = q.x, w[u][1] = q.y, w[u][2] = q.z, w[u][3] = q.w;
-        } else {
-          load_unit_any<X>(x, j, N, w[u]);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int j = j0 + u * kThreads * E + i;
-          const float y = X == 2 ? __uint_as_float(w[u][i & 3])
-                                 : half_bits_to_float((w[u][i >> 1 & 3] >> (16 * (i & 1))) & 0xffffu, X);
-          // of the entries at -inf the first 2 kMaxTop are enough: fewer than
-          // kMaxTop of those are not at -inf, or K better elements exist
-          if (y >= tau && j < N && (y > -INFINITY || j < 2 * kMaxTop)) {
-            const int at = atomicAdd(&sm.count, 1);  // the order of the buffer does not matter
-            if (at < kBuffer) sm.cand[at] = {y, j};
-          }
-        }
+    for (int k = 0; k < E; ++k) {
+      const float y =
+          X == 2 ? __uint_as_float(w[k & 3]) : half_bits_to_float((w[k >> 1 & 3] >> (16 * (k & 1))) & 0xffffu, X);
+      if (y >= tau && j0 + k < N) add_candidate(sm, y, j0 + k);
     }
   }
 }
@@ -325,7 +339,7 @@ __device__ __forceinline__ void sums_by_definition(Shared& sm, const char* x, in
 }
 
 // A row's results from the threads' states, by the whole CTA; thread 0 brings
-// the token and its logit.  Three barriers; what a barrier of the next row
+// the token and its logit.  Four barriers; what a barrier of the next row
 // protects is not protected again.
 template <int X>
 __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, int64_t row, const char* x, int N,
@@ -353,7 +367,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, i
       const bool u = usual(M);
       const float ln_s = logf(all.S), lse = fmaf(kLn2, fmaf(-M, kL, all.m), ln_s);
       sm.M = M, sm.lse = lse;
-      sm.count = 0;
+      sm.count = 0, sm.hits = 0;
       sm.kind = !u ? kUnusual : all.S != all.S ? kNaN : kUsual;
       if (u) {
         p.lp[row] = tok >= 0 && tok < p.N ? __fsub_rn(__fsub_rn(xt, M), lse) : -INFINITY;
@@ -392,7 +406,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, i
     p.top_ids[row * K + r] = c.j;
     p.top_lp[row * K + r] = __fsub_rn(__fsub_rn(c.v, M), lse);
   };
-  if (kind != kNaN && best >= sm.tau) collect<X>(sm, x, N, cut, ring);
+  if (kind != kNaN) collect<X>(sm, x, N, cut, ring);
   __syncthreads();
   const int n = sm.count;
   if (kind != kNaN && n <= kBuffer) {

@@ -48,7 +48,9 @@
 // 16-bit type, the tensor core's operand type: for a 16-bit result one
 // rounding of p (the weights are positive, so the result is off by at most
 // half a step of the averaged |v|, like its own rounding), for an fp32 result
-// p as the sum of two such numbers, 16 or more bits.  O in fp32.  Warps are
+// p as a sum of such numbers, two of fp16 or three of bf16: 22 or 24 bits (the
+// products run in a third of the time the values take to come, three or not).
+// O in fp32.  Warps are
 // joined in a fixed tree, pieces in fixed groups in piece order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -191,7 +193,8 @@ __device__ __forceinline__ void barrier_arrive(uint32_t id, uint32_t count) {
 // The join's barriers: upper warps' results written; the rest's written; all read.
 constexpr uint32_t kBarUpper = 1, kBarLower = 2, kBarRead = 3;
 
-// PS: 16-bit pieces of p in the value product, 2 for an fp32 result.
+// PS: 16-bit pieces of p in the value product: for an fp32 result 2 of fp16 or
+// 3 of bf16.
 template <int F16, int D, int NT, int PS>
 __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) paged_attn_kernel(const PagedAttnParams p) {
   using Sh = Shape<D, NT>;
@@ -677,7 +680,8 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
   constexpr int kBytes = sizeof(typename Sh::Shared);
   static_assert(kBytes <= 227 * 1024 && Sh::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
   // one slot per instance: 20 of them, from 24 on
-  constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + (PS - 1) : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + (PS - 1));
+  constexpr int kOut = PS > 1;
+  constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + kOut : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + kOut);
   static_assert(kSlot < 48, "set_smem_once's table");
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS>), kBytes, kSlot);
   if (e != cudaSuccess) return e;
@@ -690,7 +694,8 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
 
 template <int F16, int D, int NT>
 cudaError_t launch_out(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
-  return p.out_kind == 2 ? launch<F16, D, NT, 2>(p, num_sms, stream) : launch<F16, D, NT, 1>(p, num_sms, stream);
+  constexpr int kPieces = F16 ? 2 : 3;
+  return p.out_kind == 2 ? launch<F16, D, NT, kPieces>(p, num_sms, stream) : launch<F16, D, NT, 1>(p, num_sms, stream);
 }
 
 template <int F16>

@@ -18,13 +18,18 @@ int kind_of(int dtype) { return dtype == BI_F32 ? 2 : (dtype == BI_F16 ? 1 : 0);
 bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // A check that fails keeps its status and reason; later checks are skipped.
+// Reasons are put together only then: a decode step makes these calls by the
+// hundred.
 struct Check {
   bi_status st = BI_OK;
   std::string why;
 
   bool ok() const { return st == BI_OK; }
-  void that(bool good, bi_status bad, const std::string& reason) {
-    if (ok() && !good) st = bad, why = reason;
+  // `name` (if any): `reason`
+  void that(bool good, bi_status bad, const char* reason, const char* name = nullptr) {
+    if (good || !ok()) return;
+    st = bad;
+    why = name ? std::string(name) + ": " + reason : std::string(reason);
   }
   static int64_t numel(const bi_tensor* t) {
     int64_t n = 1;
@@ -34,35 +39,38 @@ struct Check {
   // rank, type class, extents, strides, element alignment
   void tensor(const bi_tensor* t, const char* name, int ndim, bool index) {
     if (!ok()) return;
-    const std::string n(name);
-    that(t != nullptr, BI_ERR_INVALID_ARG, n + ": null tensor descriptor");
+    that(t != nullptr, BI_ERR_INVALID_ARG, "null tensor descriptor", name);
     if (!ok()) return;
-    that(t->ndim == ndim, BI_ERR_INVALID_ARG,
-         n + ": expected rank " + std::to_string(ndim) + ", got " + std::to_string(t->ndim));
+    if (t->ndim != ndim) {
+      st = BI_ERR_INVALID_ARG;
+      why = std::string(name) + ": expected rank " + std::to_string(ndim) + ", got " + std::to_string(t->ndim);
+      return;
+    }
     that(index ? is_index(t->dtype) : is_float(t->dtype), BI_ERR_UNSUPPORTED_DTYPE,
-         n + (index ? ": an integer type is needed" : ": a bf16, fp16 or fp32 type is needed"));
-    if (!ok()) return;
+         index ? "an integer type is needed" : "a bf16, fp16 or fp32 type is needed", name);
     for (int i = 0; i < ndim; ++i) {
-      that(t->shape[i] >= 0 && t->shape[i] <= INT32_MAX, BI_ERR_INVALID_ARG, n + ": an extent is out of range");
+      that(t->shape[i] >= 0 && t->shape[i] <= INT32_MAX, BI_ERR_INVALID_ARG, "an extent is out of range", name);
       that(t->stride[i] >= 0 && t->stride[i] <= (int64_t)1 << 44, BI_ERR_UNSUPPORTED_LAYOUT,
-           n + ": a stride is negative or out of range");
+           "a stride is negative or out of range", name);
     }
     if (!ok()) return;
     if (numel(t) > 0) {
-      that(t->ptr != nullptr, BI_ERR_INVALID_ARG, n + ": null data pointer");
-      that(on(t->ptr, bytes_of(t->dtype)), BI_ERR_UNSUPPORTED_LAYOUT, n + ": not aligned to its element size");
+      that(t->ptr != nullptr, BI_ERR_INVALID_ARG, "null data pointer", name);
+      that(on(t->ptr, bytes_of(t->dtype)), BI_ERR_UNSUPPORTED_LAYOUT, "not aligned to its element size", name);
     }
-    if (ok() && ndim > 0)
-      that(t->shape[ndim - 1] <= 1 || t->stride[ndim - 1] == 1, BI_ERR_UNSUPPORTED_LAYOUT,
-           n + ": unit stride on the last dimension required");
+    that(ndim == 0 || t->shape[ndim - 1] <= 1 || t->stride[ndim - 1] == 1, BI_ERR_UNSUPPORTED_LAYOUT,
+         "unit stride on the last dimension required", name);
   }
   // a contiguous index vector of n elements of the given type
   void vec(const bi_tensor* t, const char* name, int64_t n, int dtype) {
     tensor(t, name, 1, true);
-    that(!ok() || t->shape[0] == n, BI_ERR_SHAPE_MISMATCH,
-         std::string(name) + ": expected " + std::to_string(n) + " elements");
-    that(!ok() || t->dtype == dtype, BI_ERR_UNSUPPORTED_DTYPE,
-         std::string(name) + (dtype == BI_I64 ? ": int64 is needed" : ": int32 is needed"));
+    if (!ok()) return;
+    if (t->shape[0] != n) {
+      st = BI_ERR_SHAPE_MISMATCH;
+      why = std::string(name) + ": expected " + std::to_string(n) + " elements";
+      return;
+    }
+    that(t->dtype == dtype, BI_ERR_UNSUPPORTED_DTYPE, dtype == BI_I64 ? "int64 is needed" : "int32 is needed", name);
   }
   // every element of an output has an address of its own
   void distinct(const bi_tensor* t, const char* name) {
@@ -76,7 +84,7 @@ struct Check {
     for (int i = 0; i < t->ndim; ++i) {
       const int d = order[i];
       if (t->shape[d] == 1) continue;
-      that(t->stride[d] > span, BI_ERR_UNSUPPORTED_LAYOUT, std::string(name) + ": elements of the output overlap");
+      that(t->stride[d] > span, BI_ERR_UNSUPPORTED_LAYOUT, "elements of the output overlap", name);
       span += (t->shape[d] - 1) * t->stride[d];
     }
   }
@@ -93,7 +101,7 @@ struct Check {
     range(out, &a0, &a1);
     range(in, &b0, &b1);
     if (a1 <= b0 || b1 <= a0) return;
-    that(interleaved(out, in), BI_ERR_INVALID_ARG, std::string(what) + ": an output overlaps another operand");
+    that(interleaved(out, in), BI_ERR_INVALID_ARG, "an output overlaps another operand", what);
   }
   // Views of one buffer that interleave without touching (q, k and v of one
   // projection; keys and values of one cache tensor): with some period s,
@@ -473,10 +481,10 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   const int64_t cap = W * ps, need = bi_paged_attention_workspace_bytes(B, Hq, D, cap);
   c.that(B * Hq * (D / 64) <= INT32_MAX && B <= (1 << 22), BI_ERR_INVALID_ARG, "too many requests");
   c.that(!workspace || on(workspace, 16), BI_ERR_UNSUPPORTED_LAYOUT, "the workspace must be 16-byte aligned");
-  c.that(need == 0 || (workspace && workspace_bytes >= need), BI_ERR_INVALID_ARG,
-         "key ranges of up to " + std::to_string(cap) + " need a workspace of " + std::to_string(need) +
-             " bytes (bi_paged_attention_workspace_bytes)");
   if (!c.ok()) return abi_finish(c.st, c.why);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return abi_finish(BI_ERR_INVALID_ARG, "key ranges of up to " + std::to_string(cap) + " need a workspace of " +
+                                              std::to_string(need) + " bytes (bi_paged_attention_workspace_bytes)");
   if (need > 0) {
     bi_tensor ws;
     memset(&ws, 0, sizeof(ws));
