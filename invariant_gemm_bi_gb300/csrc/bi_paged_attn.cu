@@ -66,7 +66,7 @@ namespace {
 // against 163 for the batch above) but leave a short cache to few SMs (one
 // request of 1021 keys 12.3 us against 9.9).  At most 128 pieces: 256 made
 // 131071 keys at D = 256 wait longer for the join than the evener split saved
-// (97.4 us against 97.0).
+// (97.7 us against 97.1).
 constexpr int kMinSplit = 256;
 constexpr int kManySplits = 128;
 
@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 // summed in piece order relative to the group's maximum, then the groups in
 // order.  Lanes hold two neighbouring dimensions of each 64.
 constexpr int kJoinGroup = 16;
-constexpr int kJoinGroups = 8;
-static_assert(kManySplits <= kJoinGroup * kJoinGroups, "groups of pieces");
+constexpr int kJoinGroups = kManySplits / kJoinGroup;  // at most
+constexpr int kJoinWarps = 8;
 
 // Below this many rows a row is joined by a block a 64 dimensions (four
 // requests of 131071 keys: 97 us against 112 with a warp a row), from it on by
@@ -629,12 +629,12 @@ __device__ __forceinline__ void join_into(Part<V>& r, float m, float l, const fl
 // kSplit: a block joins 64 dimensions of one row, a warp a group; otherwise a
 // warp joins a whole row (V = D / 64), eight rows a block.  The same bits.
 template <int V, bool kSplit>
-__global__ void __launch_bounds__(32 * kJoinGroups) paged_join_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const PagedAttnParams p) {
   __shared__ float2 so[kSplit ? kJoinGroups : 1][32];
   __shared__ float sm[kJoinGroups], sl[kJoinGroups];
   static_assert(!kSplit || V == 1, "64 dimensions a block");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slices = kSplit ? p.D / 64 : 1;
-  const int64_t bh = kSplit ? blockIdx.x / slices : (int64_t)blockIdx.x * kJoinGroups + warp;
+  const int64_t bh = kSplit ? blockIdx.x / slices : (int64_t)blockIdx.x * kJoinWarps + warp;
   if (bh >= (int64_t)p.B * p.Hq) return;
   const int d0 = kSplit ? (int)(blockIdx.x % slices) * 64 : 0;
   const int b = (int)(bh / p.Hq), h = (int)(bh % p.Hq);
@@ -644,10 +644,10 @@ __global__ void __launch_bounds__(32 * kJoinGroups) paged_join_kernel(const Page
   Part<V> r = {};
   r.m = -INFINITY;
   if constexpr (kSplit) {
-    if (warp < groups) {
-      const Part<V> x = join_group<V>(p, row0, n, warp, d0, lane);
-      so[warp][lane] = make_float2(x.o[0][0], x.o[0][1]);
-      if (lane == 0) sm[warp] = x.m, sl[warp] = x.l;
+    for (int g = warp; g < groups; g += kJoinWarps) {
+      const Part<V> x = join_group<V>(p, row0, n, g, d0, lane);
+      so[g][lane] = make_float2(x.o[0][0], x.o[0][1]);
+      if (lane == 0) sm[g] = x.m, sl[g] = x.l;
     }
     __syncthreads();
     if (warp > 0) return;
@@ -723,11 +723,11 @@ bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::s
   cudaError_t e = p.in_f16 ? launch_dim<1>(p, dev.num_sms, stream) : launch_dim<0>(p, dev.num_sms, stream);
   if (e == cudaSuccess && p.max_splits > 1) {
     const int64_t rows = (int64_t)p.B * p.Hq;
-    constexpr int kT = 32 * kJoinGroups;
+    constexpr int kT = 32 * kJoinWarps;
     if (rows < kFewRows) {
       paged_join_kernel<1, true><<<(unsigned)(rows * (p.D / 64)), kT, 0, stream>>>(p);
     } else {
-      const unsigned grid = (unsigned)((rows + kJoinGroups - 1) / kJoinGroups);
+      const unsigned grid = (unsigned)((rows + kJoinWarps - 1) / kJoinWarps);
       if (p.D == 64)
         paged_join_kernel<1, false><<<grid, kT, 0, stream>>>(p);
       else if (p.D == 128)

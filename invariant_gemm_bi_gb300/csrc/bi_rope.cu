@@ -295,7 +295,7 @@ cudaError_t launch_vec(const RopeParams& p, int num_sms, cudaStream_t stream) {
   // All heads a block, six a warp requested ahead, once that fills the GPU
   // twice; below, a head a warp (a latency-bound call wants every load in
   // flight at once).
-  if (blocks * z >= 4 * (int64_t)num_sms) {
+  if (blocks * z >= 4 * (int64_t)num_sms || heads > 8 * 65535) {
     constexpr size_t kRing = 6 * kSlot;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&rope_vec_kernel<QK, QO, KV, CK, 6>),
                                   (int)(kRing + sizeof(float2) * kMaxTokens * BI_ROPE_MAX_PAIRS), 56 + QK + 1);

@@ -496,7 +496,9 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   PagedAttnParams p;
   memset(&p, 0, sizeof(p));
   p.q = q->ptr, p.q_b = stride_or(q, 0, 0), p.q_h = stride_or(q, 1, 0);
-  p.k = k_cache->ptr, p.v = v_cache->ptr;
+  // (an empty cache may have no address: its keys are all absent, and a copy of
+  // no bytes is given some address that is one)
+  p.k = P * ps > 0 ? k_cache->ptr : q->ptr, p.v = P * ps > 0 ? v_cache->ptr : q->ptr;
   p.k_page = stride_or(k_cache, 0, 0), p.k_row = stride_or(k_cache, 1, 0), p.k_head = stride_or(k_cache, 2, 0);
   p.v_page = stride_or(v_cache, 0, 0), p.v_row = stride_or(v_cache, 1, 0), p.v_head = stride_or(v_cache, 2, 0);
   p.table = static_cast<const int32_t*>(page_table->ptr);
@@ -568,7 +570,7 @@ extern "C" bi_status bi_token_logprobs(const bi_tensor* logits, const bi_tensor*
   p.entropy = entropy ? static_cast<float*>(entropy->ptr) : nullptr;
   p.top_lp = K ? static_cast<float*>(top_logprobs->ptr) : nullptr;
   p.top_ids = K ? static_cast<int32_t*>(top_ids->ptr) : nullptr;
-  p.R = R, p.N = N, p.ld_x = R > 1 ? logits->stride[0] : N;
+  p.R = R, p.N = N, p.ld_x = R > 1 ? logits->stride[0] : 0;
   p.K = (int32_t)K, p.tok64 = tokens->dtype == BI_I64, p.x_kind = kind_of(logits->dtype);
   c.st = launch_logprobs(p, (cudaStream_t)stream, &c.why);
   return abi_finish(c.st, c.why);

@@ -240,6 +240,19 @@ def test_store_views_of_pages_and_heads():
     assert bits_equal(kc[slots // page, slots % page], k) and bits_equal(vc[slots // page, slots % page], v)
 
 
+def test_rope_and_store_with_nothing_to_do():
+    cfg = bi.bi_rope_config(64)
+    x = torch.empty(0, 4, 64, dtype=BF16, device="cuda")
+    assert bi.bi_rope(x, _i32([]), cfg).shape == (0, 4, 64)
+    y = torch.empty(3, 0, 64, dtype=BF16, device="cuda")
+    assert bi.bi_rope(y, _i32([1, 2, 3]), cfg).shape == (3, 0, 64)
+    none = torch.empty(0, 16, 2, 64, dtype=BF16, device="cuda")
+    k = _normal((2, 2, 64), BF16, 20)
+    bi.bi_paged_store(k, k.clone(), torch.tensor([-1, -1], device="cuda"), none, none.clone())
+    bi.bi_paged_store(k, k.clone(), torch.tensor([0, -1], device="cuda"), none, none.clone())
+    _bad_index()
+
+
 def test_store_slot_past_the_cache_is_reported_and_skipped():
     T, P, page, H, D = 4, 2, 16, 2, 64
     k, v = _normal((T, H, D), BF16, 18), _normal((T, H, D), BF16, 19)
@@ -397,6 +410,48 @@ def test_attention_extreme_scores():
     assert np.array_equal(ref.f64(o[0, 0]), ref.f64(vc[row][0]))
     kc[row] = float("nan")
     assert bi.bi_paged_attention(q, kc, vc, table, ln, 1.0).isnan().all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_attention_zero_and_negative_scale(scale):
+    kc, vc, table, ln = _cache([300, 3], 16, 2, 64, BF16, 85)
+    q = _normal((2, 4, 64), BF16, 88)
+    o = bi.bi_paged_attention(q, kc, vc, table, ln, scale)
+    want, bound = ref.attention(q, kc, vc, table, ln, scale, F32)
+    ref.assert_within(o, want, bound)
+
+
+def test_attention_empty_cache_and_empty_tables():
+    q = _normal((2, 4, 64), BF16, 89)
+    none = torch.empty(0, 16, 2, 64, dtype=BF16, device="cuda")
+    t = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    assert not bi.bi_paged_attention(q, none, none, t, _i32([0, 0]), 0.1).any()
+    assert not bi.bi_paged_attention(q, none, none, t, _i32([5, 40]), 0.1).any()
+    _bad_index()  # pages of a cache that has none
+    kc = _normal((2, 16, 2, 64), BF16, 90)
+    assert not bi.bi_paged_attention(q, kc, kc, t[:, :0], _i32([0, 7]), 0.1).any()
+    _bad_index()  # a length past an empty table
+
+
+def test_attention_a_nan_head_stays_alone():
+    kc, vc, table, ln = _cache([700], 16, 1, 128, F16, 91)
+    q = _normal((1, 12, 128), F16, 94)
+    o = bi.bi_paged_attention(q, kc, vc, table, ln, 0.09)
+    q[0, 5] = float("nan")
+    p = bi.bi_paged_attention(q, kc, vc, table, ln, 0.09)
+    assert p[0, 5].isnan().all()
+    keep = [h for h in range(12) if h != 5]
+    assert bits_equal(p[:, keep], o[:, keep])
+
+
+def test_attention_many_requests():
+    # more requests than a block has threads: pieces are found by a walk
+    lens = [(i * 37) % 300 for i in range(700)]
+    kc, vc, table, ln = _cache(lens, 32, 1, 64, BF16, 95)
+    q = _normal((700, 2, 64), BF16, 98)
+    o = bi.bi_paged_attention(q, kc, vc, table, ln, 0.125)
+    want, bound = ref.attention(q, kc, vc, table, ln, 0.125, F32)
+    ref.assert_within(o, want, bound)
 
 
 def test_attention_graph_replay_follows_lengths_and_tables():
