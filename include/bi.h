@@ -523,9 +523,8 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  * a key-value head, at D = 128); p = 2^(t - m), t = RN(score * RN(scale
  * log2 e)).  Warp w + W/2 is joined into warp w, then warps 1, 2, ... into
  * warp 0, groups of 16 pieces in piece order, then the groups in order, all in
- * fp32.  Sums are of the unrounded p; the product with v takes p rounded to the
- * cache's type, or for an fp32 o as the sum of two (fp16) or three (bf16) such
- * numbers.
+ * fp32.  Sums are of the unrounded p; the product with v takes p as the
+ * sum of two numbers of the cache's type, or of three bf16 for an fp32 o.
  *
  * workspace: caller-owned, 16-byte aligned, at least
  * bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes -- 0 when

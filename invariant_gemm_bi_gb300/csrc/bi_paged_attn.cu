@@ -20,7 +20,7 @@
 // mma.sync m16n8k16 with the long side on M: S^T = K Q^T (16 keys x 8 heads)
 // and O^T += V^T P^T (16 dimensions x 8 heads).  With one token a head there
 // are at most G rows to a product, which a 128-row tcgen05 tile would waste
-// 15/16 of, and the tensor pipe is 7 % busy as it is.
+// 15/16 of, and the tensor pipe is an eighth busy as it is.
 //
 // Feeding it.  Each warp owns a ring of three shared-memory slots, keys and
 // values of a tile taking one each, filled by 16-byte asynchronous copies: two
@@ -45,13 +45,11 @@
 // Arithmetic, per query head: t = RN(s c) with c = RN(scale log2 e); a running
 // maximum m per warp over its tiles; p = 2^(t - m) (the SFU's approximation);
 // l sums the unrounded p in fp32; the value product takes p in the cache's
-// 16-bit type, the tensor core's operand type: for a 16-bit result one
-// rounding of p (the weights are positive, so the result is off by at most
-// half a step of the averaged |v|, like its own rounding), for an fp32 result
-// p as a sum of such numbers, two of fp16 or three of bf16: 22 or 24 bits (the
-// products run in a third of the time the values take to come, three or not).
-// O in fp32.  Warps are
-// joined in a fixed tree, pieces in fixed groups in piece order.
+// 16-bit type, the tensor core's operand type, as a sum of two such numbers (22
+// bits of fp16, 16 of bf16; three bf16, 24 bits, for an fp32 result): one
+// alone, rounded, would be off as much as the 16-bit result's own rounding, and
+// the second costs 0.2 % (161.1 us and 161.3 for the batch above).  O in fp32.
+// Warps are joined in a fixed tree, pieces in fixed groups in piece order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -193,8 +191,8 @@ __device__ __forceinline__ void barrier_arrive(uint32_t id, uint32_t count) {
 // The join's barriers: upper warps' results written; the rest's written; all read.
 constexpr uint32_t kBarUpper = 1, kBarLower = 2, kBarRead = 3;
 
-// PS: 16-bit pieces of p in the value product: for an fp32 result 2 of fp16 or
-// 3 of bf16.
+// PS: 16-bit pieces of p in the value product: 2 of fp16, or of bf16 2 for a
+// 16-bit result and 3 for an fp32 one.
 template <int F16, int D, int NT, int PS>
 __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) paged_attn_kernel(const PagedAttnParams p) {
   using Sh = Shape<D, NT>;
@@ -679,9 +677,8 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
   using Sh = Shape<D, NT>;
   constexpr int kBytes = sizeof(typename Sh::Shared);
   static_assert(kBytes <= 227 * 1024 && Sh::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-  // one slot per instance: 20 of them, from 24 on
-  constexpr int kOut = PS > 1;
-  constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + kOut : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + kOut);
+  // one slot per instance, from 24 on
+  constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + PS - 2 : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + PS - 2);
   static_assert(kSlot < 48, "set_smem_once's table");
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS>), kBytes, kSlot);
   if (e != cudaSuccess) return e;
@@ -694,8 +691,10 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
 
 template <int F16, int D, int NT>
 cudaError_t launch_out(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
-  constexpr int kPieces = F16 ? 2 : 3;
-  return p.out_kind == 2 ? launch<F16, D, NT, kPieces>(p, num_sms, stream) : launch<F16, D, NT, 1>(p, num_sms, stream);
+  if constexpr (F16)
+    return launch<F16, D, NT, 2>(p, num_sms, stream);
+  else
+    return p.out_kind == 2 ? launch<F16, D, NT, 3>(p, num_sms, stream) : launch<F16, D, NT, 2>(p, num_sms, stream);
 }
 
 template <int F16>

@@ -114,7 +114,7 @@ def attention(q, kc, vc, table, lens, scale, out_dtype):
     table, lens = table.cpu().numpy(), lens.cpu().numpy()
     q64 = f64(q)
     ref, bound = np.zeros((B, Hq, D)), np.zeros((B, Hq, D))
-    u = HALF_STEP[q.dtype] if out_dtype != torch.float32 else HALF_STEP[q.dtype] ** (3 if q.dtype == torch.bfloat16 else 2)
+    u = HALF_STEP[q.dtype] ** (3 if q.dtype == torch.bfloat16 and out_dtype == torch.float32 else 2)
     for b in range(B):
         n = max(0, min(int(lens[b]), table.shape[1] * page))
         j = np.arange(n)
@@ -138,7 +138,7 @@ def attention(q, kc, vc, table, lens, scale, out_dtype):
             # A (products exact, sums truncated), the scaled score two roundings: under
             # 2^-17 A; t - m and m's own rescaling add 2^-22 A: 2^-16 A in the exponent.
             # 2^x is good to 2^-21.  Both count in p and in the sum it is divided by.
-            # p is rounded to the cache's type (3 bf16 or 2 fp16 pieces for an fp32 result): u.
+            # p is carried in two pieces of the cache's type, three bf16 for an fp32 result: u.
             # The sums over n keys: n 2^-23.  The division, two roundings: 2^-22.
             rel = u + 2 * (2.0 ** -16 * A + 2.0 ** -21) + n * 2.0 ** -23 + 2.0 ** -22
             err = rel * (p @ np.abs(vh))
