@@ -9,10 +9,12 @@
 // them into 2^-d S and 2^-d (H - d S).  Then, with M the row's maximum,
 //   log-sum = ln S + ln 2 (M' - M L)        (what RN(M L) left out, one fma)
 //   lp      = (x_tok - M) - log-sum,   entropy = ln S - ln 2 H / S.
-// Two passes with expf over differences, which would give the log-softmax
-// entry's own bits, cost 21 instructions an element instead of 8 and took 229 us for
-// 2048 rows of 128256 bf16 logits (525 MB) in the best of three layouts (row
-// in the registers of a cluster, 334 us; streamed twice, 229 us).
+// 2048 rows of 128256 bf16 logits (525 MB, 77 us at the copy rate) take 99 us,
+// 11 instructions an element, the ALU pipe 60 % busy.  Two passes with expf
+// over differences, which would give the log-softmax entry's own bits, cost 21
+// and took 229 us in the best of three layouts (a row in the registers of a
+// cluster 334 us, streamed twice 229 us).  8 fp32 rows with 20 alternatives
+// take 7.3 us.
 //
 // Order.  256 threads; a thread's chunk of a slice is four 16-byte units, 256
 // units apart (32 elements of 16 bits or 16 of fp32; a slice is 16 KB), reduced
@@ -34,8 +36,10 @@
 // bound of the K-th largest logit (K distinct elements reach it) and a close
 // one: K of 2 K groups are reached by about 1.4 K elements.  The chunks whose
 // maximum reaches tau are read again (out of L2), all at once, and the elements
-// that do are ranked by counting.  Rows with more than 512 such
-// elements (ties) and rows with NaNs extract one element a round instead.
+// that do are ranked by counting.  (A thread reading its own chunks again, one
+// latency after the other: 19 us in place of 7 for the 8 rows.)  Rows with more
+// than 512 such elements (ties) and rows with NaNs extract one element a round
+// instead.
 #include "bi_rows.cuh"
 #include "bi_serve.h"
 

@@ -31,10 +31,10 @@ struct Check {
     st = bad;
     why = name ? std::string(name) + ": " + reason : std::string(reason);
   }
-  static int64_t numel(const bi_tensor* t) {
-    int64_t n = 1;
-    for (int i = 0; i < t->ndim; ++i) n *= t->shape[i] > 0 ? t->shape[i] : 0;
-    return n;
+  static bool empty(const bi_tensor* t) {
+    for (int i = 0; i < t->ndim; ++i)
+      if (t->shape[i] <= 0) return true;
+    return false;
   }
   // rank, type class, extents, strides, element alignment
   void tensor(const bi_tensor* t, const char* name, int ndim, bool index) {
@@ -54,7 +54,10 @@ struct Check {
            "a stride is negative or out of range", name);
     }
     if (!ok()) return;
-    if (numel(t) > 0) {
+    if (!empty(t)) {
+      double span = 1.0;
+      for (int i = 0; i < ndim; ++i) span += (double)(t->shape[i] - 1) * (double)t->stride[i];
+      that(span < 1125899906842624.0 /* 2^50 */, BI_ERR_UNSUPPORTED_LAYOUT, "spans more memory than there is", name);
       that(t->ptr != nullptr, BI_ERR_INVALID_ARG, "null data pointer", name);
       that(on(t->ptr, bytes_of(t->dtype)), BI_ERR_UNSUPPORTED_LAYOUT, "not aligned to its element size", name);
     }
@@ -74,7 +77,7 @@ struct Check {
   }
   // every element of an output has an address of its own
   void distinct(const bi_tensor* t, const char* name) {
-    if (!ok() || numel(t) == 0) return;
+    if (!ok() || empty(t)) return;
     // dimensions in the order of their strides: each must clear what the smaller ones span
     int order[4] = {0, 1, 2, 3};
     for (int i = 0; i < t->ndim; ++i)
@@ -96,7 +99,7 @@ struct Check {
     *e = *b + (uintptr_t)((last + 1) * bytes_of(t->dtype));
   }
   void apart(const bi_tensor* out, const bi_tensor* in, const char* what) {
-    if (!ok() || !out || !in || numel(out) == 0 || numel(in) == 0) return;
+    if (!ok() || !out || !in || empty(out) || empty(in)) return;
     uintptr_t a0, a1, b0, b1;
     range(out, &a0, &a1);
     range(in, &b0, &b1);
@@ -235,7 +238,7 @@ void config_into(RopeParams* p, const bi_rope_config* cfg) {
 bool units_fit(const RopeParams& p) { return p.half % 8 == 0 && (p.D - 2 * p.half) % 16 == 0; }
 
 bi_status run_rope(RopeParams& p, int64_t T, bi_stream stream, std::string* why) {
-  if (T * p.D / 2 * std::max(1, p.hq + 2 * p.hkv) > (int64_t)INT32_MAX * 128) {
+  if ((double)T * p.D * std::max(1, p.hq + 2 * p.hkv) > 5e11) {  // grids stay below 2^31 blocks
     *why = "too many elements";
     return BI_ERR_INVALID_ARG;
   }
@@ -436,7 +439,9 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
 extern "C" int64_t bi_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len) {
   if (B <= 0 || Hq <= 0 || max_len <= 0 || B > INT32_MAX || Hq > INT32_MAX || !attention_head_dim_ok(D)) return 0;
   const int64_t n = paged_max_splits(max_len);
-  return n <= 1 ? 0 : B * Hq * n * (D + 2) * 4;
+  if (n <= 1) return 0;
+  const int64_t rows = B * Hq;  // below 2^62
+  return rows > INT64_MAX / (n * (D + 2) * 4) ? INT64_MAX : rows * n * (D + 2) * 4;
 }
 
 extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const bi_tensor* v_cache,
@@ -472,7 +477,7 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   if (!c.ok()) return abi_finish(c.st, c.why);
   const bi_tensor* ts[4] = {q, k_cache, v_cache, o};
   for (int i = 0; i < 4; ++i)
-    c.that(Check::numel(ts[i]) == 0 || rows_on_16(ts[i]), BI_ERR_UNSUPPORTED_LAYOUT,
+    c.that(Check::empty(ts[i]) || rows_on_16(ts[i]), BI_ERR_UNSUPPORTED_LAYOUT,
            "base pointers and strides of q, the caches and o must be multiples of 16 bytes");
   const bi_tensor* in[5] = {q, k_cache, v_cache, page_table, seq_lens};
   c.distinct(o, "o");

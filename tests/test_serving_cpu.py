@@ -284,6 +284,20 @@ def test_binding_refuses_what_it_cannot_describe(lib):
         binding.bi_paged_attention(None, None, None, None, None, 1.0)
 
 
+def test_descriptors_of_absurd_extent_are_refused(lib):
+    big = (1 << 31) - 1
+    assert _attend(lib, q=lambda a, o: a.t([3, 8, 128], BF16, [1 << 44, 1 << 44, 1]),
+                   kc=lambda a, o: a.t([big, big, 2, 128], BF16, [1 << 43, 1 << 43, 128, 1])) == LAYOUT
+    assert lib.bi_paged_attention_workspace_bytes(big, big, 256, 1 << 30) == (1 << 63) - 1
+    cfg = binding.bi_rope_config(128)
+    assert _store(lib, cfg, slots=lambda a, o: a.t([big], I64), pos=lambda a, o: a.t([big], I64), q=None, q_out=None,
+                  k=lambda a, o: a.t([big, big, 128], BF16, [0, 0, 1]),
+                  v=lambda a, o: a.t([big, big, 128], BF16, [0, 0, 1]),
+                  kc=lambda a, o: a.t([1, 1, big, 128], BF16), vc=lambda a, o: a.t([1, 1, big, 128], BF16)) == INVALID
+    assert _attend(lib, q=lambda a, o: a.t([big, 8, 128], BF16), table=lambda a, o: a.t([big, 40], I32),
+                   lens=lambda a, o: a.t([big], I32), o=lambda a, o: a.t([big, 8, 128], F32)) == INVALID
+
+
 def test_integer_types_stay_refused_elsewhere(lib):
     a = Arena()
     assert lib.bi_mm(_r(a.t([4, 64], I32)), _r(a.t([64, 32], I32)), _r(a.t([4, 32], F32)), None) == DTYPE
