@@ -383,7 +383,7 @@ bi_status bi_addmm_packed(const bi_tensor* bias, const bi_tensor* a, const bi_pa
  * row j % page_size; its "slot" is page * page_size + row.  One decode step is
  * bi_paged_plan (once), then per layer bi_paged_store and bi_paged_attention,
  * then bi_token_logprobs on the logits.  Each is one launch (the attention two
- * when a request's keys may be split), allocates nothing and reads lengths and
+ * for caches that are long or many), allocates nothing and reads lengths and
  * tables on the device, so a step can be captured into a CUDA graph and
  * replayed as the batch grows within the captured extents; graphs whose
  * replays may overlap need workspaces of their own.

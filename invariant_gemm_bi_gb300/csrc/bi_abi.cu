@@ -42,7 +42,7 @@ struct DevState {
   std::string why;
   int num_sms = 0;
   unsigned int* status_word = nullptr;
-  bool smem_set[64] = {};
+  bool smem_set[96] = {};
   int pairs[24] = {};  // resident 2-CTA clusters per kernel slot (0: not yet asked)
   void* scratch = nullptr;  // device address of g_bi_noalloc_scratch (0: not yet asked)
 };

@@ -62,7 +62,7 @@ namespace {
 
 // A piece has at least 256 keys: 512 would save the join's traffic (159 us
 // against 163 for the batch above) but leave a short cache to few SMs (one
-// request of 1021 keys 12.3 us against 9.9).  At most 128 pieces: 256 made
+// request of 1021 keys, joined by a second launch, 12.3 us against 9.9).  At most 128 pieces: 256 made
 // 131071 keys at D = 256 wait longer for the join than the evener split saved
 // (97.7 us against 97.1).
 constexpr int kMinSplit = 256;
@@ -192,8 +192,9 @@ __device__ __forceinline__ void barrier_arrive(uint32_t id, uint32_t count) {
 constexpr uint32_t kBarUpper = 1, kBarLower = 2, kBarRead = 3;
 
 // PS: 16-bit pieces of p in the value product: 2 of fp16, or of bf16 2 for a
-// 16-bit result and 3 for an fp32 one.
-template <int F16, int D, int NT, int PS>
+// 16-bit result and 3 for an fp32 one.  ONE: a cluster has one (request, head
+// tile), a CTA each of its pieces, and joins them itself.
+template <int F16, int D, int NT, int PS, bool ONE>
 __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) paged_attn_kernel(const PagedAttnParams p) {
   using Sh = Shape<D, NT>;
   extern __shared__ __align__(1024) unsigned char dyn[];
@@ -201,9 +202,11 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
   constexpr int W = Sh::W, H = W / 2, kThreads = 32 * W, KT = Sh::KT, KJ = Sh::KJ, MT = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 
-  // pieces before each thread's requests
+  const int inner = p.Hkv * p.head_tiles;
   const int per = (p.B + kThreads - 1) / kThreads;
-  {
+  int64_t all = 0, units = 1;  // units of the grid and of this CTA
+  if constexpr (!ONE) {
+    // pieces before each thread's requests
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int n = 0;
     for (int b = b0; b < b1; ++b) n += split_count(request_len(p, b));
@@ -219,15 +222,23 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
     sm.start[threadIdx.x] = sum - n;
     if (threadIdx.x == kThreads - 1) sm.start[kThreads] = sum;
     __syncthreads();
+    all = (int64_t)sm.start[kThreads] * inner;
+    // this CTA's: blockIdx.x, blockIdx.x + gridDim.x, ...
+    units = all > blockIdx.x ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    if (units == 0) return;
   }
-  const int inner = p.Hkv * p.head_tiles;
-  const int64_t all = (int64_t)sm.start[kThreads] * inner;
-  // units of this CTA: blockIdx.x, blockIdx.x + gridDim.x, ...
-  const int64_t units = all > blockIdx.x ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-  if (units == 0) return;
 
   // The CTA's i-th unit; `w` is refilled, a unit a lane, when i leaves it.
   auto unit_at = [&](int64_t i, Window& w) {
+    Unit u;
+    if constexpr (ONE) {
+      const int id = (int)blockIdx.x / p.max_splits;
+      u.b = id / inner, u.hk = id - u.b * inner, u.piece = (int)blockIdx.x % p.max_splits;
+      u.len = request_len(p, u.b);
+      const int n = paged_split_len(u.len);
+      u.k0 = u.piece * n, u.k1 = min(u.len, u.k0 + n);  // below k0 for a piece that the request has not
+      return u;
+    }
     if (i >= w.base + 32) {
       w.base = i;
       const int64_t id = blockIdx.x + (i + lane) * gridDim.x;
@@ -252,7 +263,6 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
       __syncwarp();
     }
     const int src = (int)(i - w.base);
-    Unit u;
     u.b = __shfl_sync(0xffffffffu, w.b, src);
     u.hk = __shfl_sync(0xffffffffu, w.hk, src);
     u.piece = __shfl_sync(0xffffffffu, w.piece, src);
@@ -526,6 +536,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
         for (int w = 1; w < H; ++w) take_over(w);
         if (ui + 1 < units) barrier_arrive(kBarRead, 32 * (H + 1));
+        if constexpr (ONE) {
+          hand_over(0);  // for the cluster's first CTA, where this warp alone has read
+          continue;
+        }
         const int pieces = split_count(u.len);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -538,8 +552,9 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
               const int64_t at = u.b * p.o_b + (head + hh) * p.o_h + g;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
-                store_one(p.o, p.out_kind, at + 16 * i, __fmul_rn(o[i][n][h], inv));
-                store_one(p.o, p.out_kind, at + 16 * i + 8, __fmul_rn(o[i][n][2 + h], inv));
+                // + 0: a negative zero becomes the positive one that a join makes of it
+                store_one(p.o, p.out_kind, at + 16 * i, __fmul_rn(__fadd_rn(o[i][n][h], 0.0f), inv));
+                store_one(p.o, p.out_kind, at + 16 * i + 8, __fmul_rn(__fadd_rn(o[i][n][2 + h], 0.0f), inv));
               }
             } else {
               const int64_t part = ((int64_t)u.b * p.max_splits + u.piece) * p.Hq + head + hh;
@@ -556,6 +571,46 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
     u = next;
   }
   copies_wait<0>();
+  if constexpr (ONE) {
+    // The first CTA joins the cluster's pieces as paged_join_kernel does a
+    // group of them (a piece that the request has not adds zeros).
+    cluster_sync_all();
+    if (cluster_ctarank() == 0) {
+      const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
+      const int head = kvh * p.group + h0, heads = min(8 * NT, p.group - h0);
+      for (int e = threadIdx.x; e < heads * (D / 4); e += kThreads) {
+        const int h = e / (D / 4), d = (e % (D / 4)) * 4;
+        const uint32_t am = smem_u32(&sm.m[0][h]), al = smem_u32(&sm.l[0][h]), ao = smem_u32(&sm.o[0][h][d]);
+        float m[8], l[8], o[8][4];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= p.max_splits) break;
+          m[r] = ld_shared_cluster_f32(cluster_map_shared(am, (uint32_t)r));
+          l[r] = ld_shared_cluster_f32(cluster_map_shared(al, (uint32_t)r));
+          const uint32_t x = cluster_map_shared(ao, (uint32_t)r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[r][i] = ld_shared_cluster_f32(x + 4 * i);
+          mx = fmaxf(mx, m[r]);
+        }
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        float sum = 0.0f, a[4] = {};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= p.max_splits) break;
+          const float f = ex2_approx(m[r] - ref);
+          sum = fmaf(f, l[r], sum);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = fmaf(f, o[r][i], a[i]);
+        }
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);  // no key: zeros
+        const int64_t at = u.b * p.o_b + (head + h) * p.o_h + d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_one(p.o, p.out_kind, at + i, __fmul_rn(a[i], inv));
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while the first may read its results
+  }
 }
 
 // Joins the pieces of each (request, query head): groups of 16 pieces, each
@@ -672,39 +727,61 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   }
 }
 
+// *joined: whether the launch leaves nothing to join.
 template <int F16, int D, int NT, int PS>
-cudaError_t launch(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
   using Sh = Shape<D, NT>;
   constexpr int kBytes = sizeof(typename Sh::Shared);
   static_assert(kBytes <= 227 * 1024 && Sh::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-  // one slot per instance, from 24 on
+  // one slot per instance, from 24 on (ONE: from 64 on)
   constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + PS - 2 : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + PS - 2);
-  static_assert(kSlot < 48, "set_smem_once's table");
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS>), kBytes, kSlot);
-  if (e != cudaSuccess) return e;
   p.head_tiles = (p.group + 8 * NT - 1) / (8 * NT);
   const int64_t most = (int64_t)p.B * p.max_splits * p.Hkv * p.head_tiles;
+  // Short caches whose units all run at once: a CTA a unit and a cluster a
+  // request's head tile, joined in place -- one launch, and no search for the
+  // units (one request of 1021 keys: 6.9 us, 10.0 the other way).  The bits are
+  // the same.
+  *joined = p.max_splits == 1 || (p.max_splits <= 8 && most <= (int64_t)num_sms * Sh::kCtas);
+  if (p.max_splits <= 8 && most <= (int64_t)num_sms * Sh::kCtas) {
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS, true>), kBytes, kSlot + 40);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)most);
+    cfg.blockDim = dim3(32 * Sh::W);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.max_splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<F16, D, NT, PS, true>, p);
+  }
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS, false>), kBytes, kSlot);
+  if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms * Sh::kCtas);
-  paged_attn_kernel<F16, D, NT, PS><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
+  paged_attn_kernel<F16, D, NT, PS, false><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int F16, int D, int NT>
-cudaError_t launch_out(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_out(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
   if constexpr (F16)
-    return launch<F16, D, NT, 2>(p, num_sms, stream);
+    return launch<F16, D, NT, 2>(p, num_sms, joined, stream);
   else
-    return p.out_kind == 2 ? launch<F16, D, NT, 3>(p, num_sms, stream) : launch<F16, D, NT, 2>(p, num_sms, stream);
+    return p.out_kind == 2 ? launch<F16, D, NT, 3>(p, num_sms, joined, stream) : launch<F16, D, NT, 2>(p, num_sms, joined, stream);
 }
 
 template <int F16>
-cudaError_t launch_dim(PagedAttnParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
   // more than eight query heads a key-value head: 16 a unit, except at
   // D = 256, where two tiles' accumulators would not fit the registers
   const bool wide = p.group > 8;
-  if (p.D == 64) return wide ? launch_out<F16, 64, 2>(p, num_sms, stream) : launch_out<F16, 64, 1>(p, num_sms, stream);
-  if (p.D == 128) return wide ? launch_out<F16, 128, 2>(p, num_sms, stream) : launch_out<F16, 128, 1>(p, num_sms, stream);
-  return launch_out<F16, 256, 1>(p, num_sms, stream);
+  if (p.D == 64) return wide ? launch_out<F16, 64, 2>(p, num_sms, joined, stream) : launch_out<F16, 64, 1>(p, num_sms, joined, stream);
+  if (p.D == 128) return wide ? launch_out<F16, 128, 2>(p, num_sms, joined, stream) : launch_out<F16, 128, 1>(p, num_sms, joined, stream);
+  return launch_out<F16, 256, 1>(p, num_sms, joined, stream);
 }
 
 }  // namespace
@@ -719,8 +796,9 @@ bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::s
   const bi_status st = current_device_info(&dev, why);
   if (st != BI_OK) return st;
   p.status_word = dev.status_word;
-  cudaError_t e = p.in_f16 ? launch_dim<1>(p, dev.num_sms, stream) : launch_dim<0>(p, dev.num_sms, stream);
-  if (e == cudaSuccess && p.max_splits > 1) {
+  bool joined = false;
+  cudaError_t e = p.in_f16 ? launch_dim<1>(p, dev.num_sms, &joined, stream) : launch_dim<0>(p, dev.num_sms, &joined, stream);
+  if (e == cudaSuccess && !joined) {
     const int64_t rows = (int64_t)p.B * p.Hq;
     constexpr int kT = 32 * kJoinWarps;
     if (rows < kFewRows) {

@@ -340,6 +340,22 @@ def test_attention_rows_do_not_depend_on_batch_pages_or_workspace(D, Hq, Hkv):
                           o[b:b + 1, :g])
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (128, 32, 2), (256, 8, 2)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_attention_bits_do_not_depend_on_the_table_width(D, Hq, Hkv, out):
+    # a narrow table (its pieces joined by a cluster in one launch) and a wide one
+    for lens in ([1], [256], [257, 0], [700, 40, 2048], [1500] * 3):
+        kc, vc, table, ln = _cache(lens, 16, Hkv, D, BF16, 46)
+        q = _normal((len(lens), Hq, D), BF16, 49)
+        o = bi.bi_paged_attention(q, kc, vc, table, ln, 0.1, out_dtype=out)
+        for width in (129, 300, 1000):
+            wide = torch.zeros(len(lens), width, dtype=torch.int32, device="cuda")
+            wide[:, :table.shape[1]] = table
+            assert bits_equal(bi.bi_paged_attention(q, kc, vc, wide, ln, 0.1, out_dtype=out), o), (lens, width)
+        want, bound = ref.attention(q, kc, vc, table, ln, 0.1, out)
+        ref.assert_within(o, want, bound)
+
+
 def test_attention_strided_operands():
     lens, page, Hkv, D, Hq = [300, 33], 16, 2, 64, 4
     kc, vc, table, ln = _cache(lens, page, Hkv, D, F16, 50)
