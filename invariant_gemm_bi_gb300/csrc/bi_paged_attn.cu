@@ -786,7 +786,6 @@ cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream
 
 }  // namespace
 
-int32_t paged_splits(int64_t len) { return split_count(len); }
 int32_t paged_max_splits(int64_t cap) {
   return cap >= (int64_t)kManySplits * kMinSplit ? kManySplits : split_count(cap);
 }

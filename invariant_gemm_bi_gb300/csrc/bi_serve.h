@@ -90,8 +90,7 @@ struct PagedAttnParams {
   float score_log2;      // scale * log2(e), rounded once to fp32
   unsigned int* status_word;
 };
-// Splits of a key range of len keys, and the most over all lengths up to cap.
-int32_t paged_splits(int64_t len);
+// The most pieces of a key range, over all lengths up to cap.
 int32_t paged_max_splits(int64_t cap);
 bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::string* why);
 
