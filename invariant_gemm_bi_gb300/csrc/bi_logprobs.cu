@@ -340,6 +340,7 @@ __device__ __forceinline__ void sums_by_definition(Shared& sm, const char* x, in
   __syncthreads();
   S = sm.warp[0].S, H = sm.warp[0].H;
   for (int w = 1; w < kWarps; ++w) S = __fadd_rn(S, sm.warp[w].S), H = __fadd_rn(H, sm.warp[w].H);
+  __syncthreads();  // read before the next row's states are written there
 }
 
 // A row's results from the threads' states, by the whole CTA; thread 0 brings

@@ -607,6 +607,24 @@ def test_logprobs_many_rows():
     _check_logprobs(x, tokens, 3)
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_logprobs_rows_of_lowest_numbers_without_alternatives(dt):
+    # many rows a CTA, all summed by the definition, nothing asked for but the
+    # token's own: each row is as it is alone
+    x = _normal((4000, 300), dt, 126)
+    x[::2] = torch.finfo(dt).min
+    x[::2, ::3] = float("-inf")
+    x[::2, 5] = 0.75 * torch.finfo(dt).min
+    x[6::8] = torch.finfo(dt).min
+    tokens = torch.randint(0, 300, (4000,), generator=_gen(127), device="cuda")
+    r = bi.bi_token_logprobs(x, tokens)
+    few = _check_logprobs(x[:16], tokens[:16], 0)
+    assert bits_equal(r.logprobs[:16], few.logprobs) and bits_equal(r.entropy[:16], few.entropy)
+    # every eighth row holds one number: each of its 300 tokens has 1/300
+    assert torch.equal(r.logprobs[6::8], r.logprobs[6:7].expand(500)) and torch.equal(r.entropy[6::8], r.entropy[6:7].expand(500))
+    ref.assert_same_nonfinite(r.logprobs[6:7], *(np.full(1, v) for v in (-np.log(300.0), 2.0 ** -20)), "uniform")
+
+
 # -- streams and the whole step -------------------------------------------------------------------------
 
 def test_calls_on_another_stream():
