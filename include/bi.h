@@ -401,7 +401,7 @@ bi_status bi_addmm_packed(const bi_tensor* bias, const bi_tensor* a, const bi_pa
 /*
  * Block tables and slot maps from request lengths.
  *   context_lens [B], new_lens [B] int32: tokens already cached, tokens to add
- *     (negative ones count as 0);
+ *     (negative ones count as 0); B <= 2^22;
  *   page_table [B, W] int32, unit stride on W, updated: the first
  *     ceil(context / page_size) entries of a row are its pages;
  *   free_pages [F] int32: pages handed out in this order.
@@ -493,8 +493,8 @@ bi_status bi_rope(const bi_rope_config* config, const bi_tensor* x, const bi_ten
  *   types (may be q itself, as in bi_rope); k_cache, v_cache
  *   [P,page_size,Hkv,D] of one type, bf16, fp16 or fp32; unit strides on D;
  *   P * page_size < 2^31.
- * Slots must be distinct: which of two tokens with one slot is kept is not
- * specified.  Cache rows that no token names are left as they were.
+ * Slots must be distinct: a row that two tokens name holds parts of either, and
+ * which is not specified.  Cache rows that no token names are left as they were.
  */
 bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* positions,
                          const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
@@ -508,7 +508,7 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  *   q [B,Hq,D] bf16 or fp16; k_cache, v_cache [P,page_size,Hkv,D] of q's type;
  *   o [B,Hq,D] fp32, bf16 or fp16;  Hkv divides Hq;  D = 64, 128 or 256;
  *   page_table [B,W] int32, unit stride on W; seq_lens [B] int32; any
- *   page_size >= 1 with P * page_size < 2^31 and W * page_size <= 2^30.
+ *   page_size >= 1 with P * page_size < 2^31 and W * page_size <= 2^30; B <= 2^22.
  *   q, caches and o: unit stride on D, 16-byte aligned, other strides
  *   multiples of 16 bytes.  scale finite.
  * A request of length <= 0 gives zeros (the new token itself is normally in

@@ -136,6 +136,9 @@ struct Check {
   }
 };
 
+constexpr int64_t kMaxRequests = 1 << 22;  // of a plan and an attention call
+constexpr int64_t kMaxHeads = 1 << 30;     // head numbers of a token, and steps past them, fit 32 bits
+
 int64_t stride_or(const bi_tensor* t, int d, int64_t alone) { return t->shape[d] > 1 ? t->stride[d] : alone; }
 
 }  // namespace
@@ -160,7 +163,7 @@ extern "C" bi_status bi_paged_plan(const bi_tensor* context_lens, const bi_tenso
   c.tensor(positions, "positions", 1, true);
   if (!c.ok()) return abi_finish(c.st, c.why);
   const int64_t B = page_table->shape[0], T = positions->shape[0];
-  c.that(B < INT32_MAX, BI_ERR_INVALID_ARG, "too many requests");
+  c.that(B <= kMaxRequests, BI_ERR_INVALID_ARG, "too many requests");
   c.vec(context_lens, "context_lens", B, BI_I32);
   c.vec(new_lens, "new_lens", B, BI_I32);
   c.vec(seq_lens, "seq_lens", B, BI_I32);
@@ -336,6 +339,7 @@ extern "C" bi_status bi_rope(const bi_rope_config* config, const bi_tensor* x, c
   c.that(D >= config->rotary_dim && D <= 1024, BI_ERR_INVALID_ARG, "the head dimension must be within [rotary_dim, 1024]");
   if (!c.ok()) return abi_finish(c.st, c.why);
   c.distinct(y, "y");
+  c.that(H <= kMaxHeads, BI_ERR_INVALID_ARG, "too many heads");
   if (!same_view(x, y)) c.apart(y, x, "bi_rope");
   c.apart(y, positions, "bi_rope");
   if (!c.ok() || T == 0 || H == 0) return abi_finish(c.st, c.why);
@@ -406,7 +410,7 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
     for (int j = 0; j < i; ++j) c.apart(out[i], out[j], "bi_paged_store");
   }
   const int64_t Hq = q ? q->shape[1] : 0;
-  c.that(Hq + 2 * H <= INT32_MAX, BI_ERR_INVALID_ARG, "too many heads");
+  c.that(Hq + 2 * H <= kMaxHeads, BI_ERR_INVALID_ARG, "too many heads");
   if (!c.ok() || T == 0 || Hq + H == 0) return abi_finish(c.st, c.why);
   RopeParams p;
   memset(&p, 0, sizeof(p));
@@ -484,7 +488,7 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   for (int i = 0; i < 5; ++i) c.apart(o, in[i], "bi_paged_attention");
   if (!c.ok() || B == 0 || Hq == 0) return abi_finish(c.st, c.why);
   const int64_t cap = W * ps, need = bi_paged_attention_workspace_bytes(B, Hq, D, cap);
-  c.that(B * Hq * (D / 64) <= INT32_MAX && B <= (1 << 22), BI_ERR_INVALID_ARG, "too many requests");
+  c.that(B * Hq * (D / 64) <= INT32_MAX && B <= kMaxRequests, BI_ERR_INVALID_ARG, "too many requests");
   c.that(!workspace || on(workspace, 16), BI_ERR_UNSUPPORTED_LAYOUT, "the workspace must be 16-byte aligned");
   if (!c.ok()) return abi_finish(c.st, c.why);
   if (need > 0 && (!workspace || workspace_bytes < need))

@@ -298,6 +298,21 @@ def test_descriptors_of_absurd_extent_are_refused(lib):
                    lens=lambda a, o: a.t([big], I32), o=lambda a, o: a.t([big, 8, 128], F32)) == INVALID
 
 
+def test_numbers_that_steps_would_carry_past_32_bits_are_refused(lib):
+    big = (1 << 31) - 1
+    cfg = binding.bi_rope_config(16)
+    assert _rope(lib, cfg, x=lambda a, o: a.t([1, big, 16], BF16), pos=lambda a, o: a.t([1], I32),
+                 y=lambda a, o: a.t([1, big, 16], BF16)) == INVALID
+    assert _store(lib, cfg, slots=lambda a, o: a.t([1], I64), pos=lambda a, o: a.t([1], I64),
+                  q=lambda a, o: a.t([1, big - 4, 16], BF16), q_out=lambda a, o: a.t([1, big - 4, 16], BF16),
+                  k=lambda a, o: a.t([1, 2, 16], BF16), v=lambda a, o: a.t([1, 2, 16], BF16),
+                  kc=lambda a, o: a.t([4, 16, 2, 16], BF16), vc=lambda a, o: a.t([4, 16, 2, 16], BF16)) == INVALID
+    n = big - 1
+    assert _plan(lib, ctx=lambda a, o: a.t([n], I32), new=lambda a, o: a.t([n], I32),
+                 table=lambda a, o: a.t([n, 8], I32), lens=lambda a, o: a.t([n], I32),
+                 offs=lambda a, o: a.t([n + 1], I32)) == INVALID
+
+
 def test_integer_types_stay_refused_elsewhere(lib):
     a = Arena()
     assert lib.bi_mm(_r(a.t([4, 64], I32)), _r(a.t([64, 32], I32)), _r(a.t([4, 32], F32)), None) == DTYPE
