@@ -51,7 +51,8 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& b, int64_t* sh) 
 }
 
 // Last index i in [0, n) with at[i] <= v (at ascending, at[0] == 0).
-__device__ __forceinline__ int find_last(const int32_t* at, int n, int32_t v) {
+template <typename I>
+__device__ __forceinline__ int find_last(const I* at, int n, I v) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -69,7 +70,8 @@ __device__ __forceinline__ int find_last(const int32_t* at, int n, int32_t v) {
 template <int NT>
 __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
   __shared__ int64_t sh[2 * NT / 32];
-  __shared__ int32_t tok_at[NT], page_at[NT];
+  __shared__ int32_t tok_at[NT];
+  __shared__ int64_t page_at[NT];
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
   int64_t tok = 0, pages = 0;
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
   const int64_t own_tok = tok, own_pages = pages;
   block_scan<NT>(tok, pages, sh);
   tok_at[threadIdx.x] = sat32(tok - own_tok);
-  page_at[threadIdx.x] = sat32(pages - own_pages);
+  page_at[threadIdx.x] = pages - own_pages;
   int64_t all_tok = 0, all_pages = 0;
   for (int i = 0; i < NT / 32; ++i) all_tok += sh[i], all_pages += sh[NT / 32 + i];
   __syncthreads();
@@ -100,16 +102,19 @@ __global__ void __launch_bounds__(NT) plan_kernel(const PlanParams p) {
   }
   const int used = (p.B + per - 1) / max(per, 1);  // threads that own requests
   const int32_t first = (int32_t)(blockIdx.x * NT + threadIdx.x), step = (int32_t)(gridDim.x * NT);
-  // new pages
-  const int32_t n_pages = sat32(all_pages);
-  for (int64_t e = first; e < n_pages; e += step) {
-    const int i = find_last(page_at, used, (int32_t)e);
+  // new pages; those past a row's last column (lengths that no table can hold)
+  // are stepped over a request at a time
+  for (int64_t e = first; e < all_pages; e += step) {
+    const int i = find_last(page_at, used, e);
     int64_t at = page_at[i];
     int b = i * per;
     Req r = load_req(p, b);
     while (e >= at + r.take) at += r.take, r = load_req(p, ++b);
     const int64_t col = r.held + (e - at);
-    if (col < p.W) p.table[b * p.ld_table + col] = e < p.F ? __ldg(p.pool + e) : -1;
+    if (col < p.W)
+      p.table[b * p.ld_table + col] = e < p.F ? __ldg(p.pool + e) : -1;
+    else
+      e += (at + r.take - 1 - e) / step * step;
   }
   // tokens
   for (int64_t t = first; t < p.T; t += step) {

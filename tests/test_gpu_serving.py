@@ -95,6 +95,19 @@ def test_plan_saturates_and_empty_batch():
     assert e.token_offsets.tolist() == [0] and e.slots.tolist() == [-1] * 3 and e.totals.tolist() == [0, 0]
 
 
+def test_plan_lengths_that_no_table_can_hold():
+    # 2^31 - 1 pages for each of 300 requests, three columns a row: every row's own
+    # columns are written, the first ones from the pool
+    B, most = 300, 2 ** 31 - 1
+    table = torch.full((B, 3), 7, dtype=torch.int32, device="cuda")
+    p = bi.bi_paged_plan(_i32([1] + [0] * (B - 1)), _i32([most] * B), table, _i32([5, 6]), 1, 4)
+    want = torch.full((B, 3), -1, dtype=torch.int32)
+    want[0] = torch.tensor([7, 5, 6])
+    assert torch.equal(table.cpu(), want)
+    assert p.totals.tolist() == [most, most] and p.slots.tolist() == [5, 6, -1, -1]
+    assert p.positions.tolist() == [1, 2, 3, 4] and p.seq_lens.tolist() == [most] * B
+
+
 # -- rotary positions ------------------------------------------------------------------------
 
 ROPES = [  # heads, D, rotary, interleaved
