@@ -115,10 +115,13 @@ struct SharedCluster {
   float4 state[kGroups][kThreads];
 };
 
-// Whether a row's maximum is where references neither overflow nor come near
-// kFloor, below which -inf counts: then the sums above are the definition.
-constexpr float kFloor = -8.507059173023462e37f;  // -2^126
-__device__ __forceinline__ bool usual(float m) { return m > -1e37f && m < 1e36f; }
+// A reference is a rounded product, so the largest t of a chunk is what the
+// rounding left out: up to 2^-24 |m'|, no longer a small number when m' is not.
+// Hence references are held above a floor, whose chunks (of masked entries)
+// weigh nothing in a usual row; rows whose maximum is not clear of the floor,
+// or as large, are summed by the definition.
+constexpr float kFloor = -2097152.0f;  // -2^21
+__device__ __forceinline__ bool usual(float m) { return fabsf(m) < 1048576.0f; }
 // Larger of two 16-bit pairs, a NaN giving way to a number.
 template <int X>
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
@@ -323,7 +326,7 @@ __device__ __forceinline__ void extract_top(Shared& sm, const char* x, int N, in
 }
 
 // The same sums from the definition, for rows whose maximum is out of the
-// ordinary (all entries at the type's lowest numbers, or enormous ones): expf
+// ordinary (all entries masked by low numbers, or enormous ones): expf
 // over differences, thread t over elements t, t + 256, ..., warps in order.
 template <int X>
 __device__ __forceinline__ void sums_by_definition(Shared& sm, const char* x, int N, float M, float& S, float& H) {

@@ -638,6 +638,32 @@ def test_logprobs_rows_of_lowest_numbers_without_alternatives(dt):
     ref.assert_same_nonfinite(r.logprobs[6:7], *(np.full(1, v) for v in (-np.log(300.0), 2.0 ** -20)), "uniform")
 
 
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("N", [40, 9001, 40000])
+def test_logprobs_logits_masked_by_low_numbers(dt, N):
+    # rows whose maximum, or most of whose entries, are low numbers of any size up
+    # to the type's lowest, with -inf, the lowest number and a NaN among the entries
+    low = torch.finfo(dt).min
+    tops = [low, 0.98 * low, 0.9 * low, 0.25 * low, 1e-3 * low, -3e30, -1e20, -1e12, -1e10, -1.1e9, -4e6, -2.2e6, -1.5e6,
+            -1e6, -6e4, -5e3, -3.0, 8.0]
+    tops = [t for t in tops if t >= low]
+    x = torch.full((5 * len(tops), N), low, dtype=torch.float64)
+    for i, t in enumerate(tops):
+        x[5 * i:5 * i + 4, 2::5] = t
+        x[5 * i + 1, ::3] = float("-inf")
+        x[5 * i + 2] = float("-inf")
+        x[5 * i + 2, [1, N - 2]] = t
+        x[5 * i + 2, 7] = low
+        x[5 * i + 3, N // 2] = float("nan")
+        x[5 * i + 4] = t  # whole chunks of it in a row of others
+        x[5 * i + 4, :min(N, 8192):3] = torch.linspace(-4, 4, len(range(0, min(N, 8192), 3)), dtype=torch.float64)
+    tokens = torch.randint(0, N, (x.shape[0],), generator=_gen(128), device="cuda")
+    _check_logprobs(x.to(dt).cuda(), tokens, 11)
+    few = slice(-10, None)  # a cluster a row and a CTA a row: the same bits
+    a, b = (bi.bi_token_logprobs(y.to(dt).cuda(), tokens[few].repeat(k)) for y, k in ((x[few], 1), (x[few].repeat(40, 1), 40)))
+    assert bits_equal(a.logprobs, b.logprobs[:10]) and bits_equal(a.entropy, b.entropy[:10])
+
+
 # -- streams and the whole step -------------------------------------------------------------------------
 
 def test_calls_on_another_stream():
