@@ -9,12 +9,12 @@
 // them into 2^-d S and 2^-d (H - d S).  Then, with M the row's maximum,
 //   log-sum = ln S + ln 2 (M' - M L)        (what RN(M L) left out, one fma)
 //   lp      = (x_tok - M) - log-sum,   entropy = ln S - ln 2 H / S.
-// 2048 rows of 128256 bf16 logits (525 MB, 77 us at the copy rate) take 99 us,
-// 11 instructions an element, the ALU pipe 60 % busy.  Two passes with expf
+// 2048 rows of 128256 bf16 logits (525 MB, 77 us at the copy rate) take 87 us,
+// 9.6 instructions an element.  Two passes with expf
 // over differences, which would give the log-softmax entry's own bits, cost 21
 // and took 229 us in the best of three layouts (a row in the registers of a
 // cluster 334 us, streamed twice 229 us).  8 fp32 rows with 20 alternatives
-// take 7.3 us.
+// take 6.9 us.
 //
 // Order.  256 threads; a thread's chunk of a slice is four 16-byte units, 256
 // units apart (32 elements of 16 bits or 16 of fp32; a slice is 16 KB), reduced
@@ -29,7 +29,11 @@
 // Loads.  Every thread copies its own chunks into a shared-memory ring of its
 // own, half a slice a stage, by 16-byte asynchronous copies, and the ring runs
 // on from row to row: no barrier and no producer, 128 KB an SM in flight.  Rows
-// that are not on 16-byte boundaries are read a word at a time into registers.
+// that are not on 16-byte boundaries are copied from the boundary before, and a
+// thread puts its units together from its own and the next lane's, by a shift
+// that is the row's (N = 128257 110 us, 128258 107; words loaded straight into
+// registers 177 and 113; rows of less than a slice are slower for it, 20000 of
+// 1001 123 us against 113).
 //
 // Alternatives.  The selection is exact, so it is free to use any order.  The
 // K-th largest, tau, of the maxima of 2 K or more groups of threads is a lower
@@ -97,7 +101,7 @@ __device__ __forceinline__ State shuffle_down(const State& s, int x) {
 }
 
 struct Shared {
-  unsigned char ring[kStages][kThreads * kHalf * 16];
+  unsigned char ring[kStages][(kThreads + kWarps) * kHalf * 16];
   float best[kGroups][kThreads];  // the threads' maxima in each group of slices
   __align__(16) float group[kMaxima];
   Cand cand[kBuffer];
@@ -119,9 +123,15 @@ struct SharedCluster {
 // rounding left out: up to 2^-24 |m'|, no longer a small number when m' is not.
 // Hence references are held above a floor, whose chunks (of masked entries)
 // weigh nothing in a usual row; rows whose maximum is not clear of the floor,
-// or as large, are summed by the definition.
-constexpr float kFloor = -2097152.0f;  // -2^21
-__device__ __forceinline__ bool usual(float m) { return fabsf(m) < 1048576.0f; }
+// or as large, are summed by the definition.  16-bit entries are held above it
+// themselves, so that -inf has a finite t: within a usual row e is 0 there, and
+// e t with it.
+template <int X>
+struct Floor {  // -2^21; fp16's lowest number
+  static constexpr float v = X == 1 ? -65504.0f : -2097152.0f;
+};
+template <int X>
+__device__ __forceinline__ bool usual(float m) { return m > (X == 1 ? -6e4f : -1048576.0f) && m < 1048576.0f; }
 // Larger of two 16-bit pairs, a NaN giving way to a number.
 template <int X>
 __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
@@ -130,6 +140,16 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The same, a NaN staying one.
+template <int X>
+__device__ __forceinline__ uint32_t max16x2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (X == 1)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -151,8 +171,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// A thread's chunk of 16 words: its state and its maximum.  t is held above
-// -200 in H alone, so that an entry at -inf (e = 0) adds 0.
+// A thread's chunk of 16 words: its state and its maximum.  Entries at -inf
+// (e = 0) add 0 to H: those of 16 bits by their floor, half an instruction an
+// element (an instruction to hold t itself: 3 us more); an fp32 t is held above
+// -200 there.
 template <int X>
 __device__ __forceinline__ State reduce_chunk(const uint32_t (&w)[4 * kUnits], float& best) {
   constexpr int NW = 4 * kUnits;
@@ -168,18 +190,24 @@ __device__ __forceinline__ State reduce_chunk(const uint32_t (&w)[4 * kUnits], f
     m = fmaxf(half_bits_to_float(m2 & 0xffffu, X), half_bits_to_float(m2 >> 16, X));
   }
   best = m;
-  const float r = __fmul_rn(fmaxf(m, kFloor), kL);
+  const float r = __fmul_rn(fmaxf(m, Floor<X>::v), kL);
   const uint64_t l2 = pack2(kL, kL), r2 = pack2(-r, -r);
   uint64_t S2 = pack2(0.0f, 0.0f), H2 = S2;
 #pragma unroll
   for (int i = 0; i < NW; i += X == 2 ? 2 : 1) {
-    const uint64_t v = X == 2 ? pack2(__uint_as_float(w[i]), __uint_as_float(w[i + (X == 2)]))
-                              : pack2(half_bits_to_float(w[i] & 0xffffu, X), half_bits_to_float(w[i] >> 16, X));
+    uint64_t v;
+    if constexpr (X == 2) {
+      v = pack2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+    } else {
+      const uint32_t f = max16x2_nan<X>(w[i], X == 1 ? 0xfbfffbffu : 0xca00ca00u);  // the floor, twice
+      v = pack2(half_bits_to_float(f & 0xffffu, X), half_bits_to_float(f >> 16, X));
+    }
+    const uint64_t t = fma2(v, l2, r2);
     float t0, t1;
-    unpack2(fma2(v, l2, r2), t0, t1);
+    unpack2(t, t0, t1);
     const uint64_t e = pack2(ex2_approx(t0), ex2_approx(t1));
     S2 = add2(S2, e);
-    H2 = fma2(e, pack2(fmaxf(t0, -200.0f), fmaxf(t1, -200.0f)), H2);
+    H2 = fma2(e, X == 2 ? pack2(fmaxf(t0, -200.0f), fmaxf(t1, -200.0f)) : t, H2);
   }
   float s0, s1, h0, h1;
   unpack2(S2, s0, s1);
@@ -254,7 +282,7 @@ __device__ __forceinline__ void add_candidate(Shared& sm, float y, int j) {
 // thread in a group of slices) whose maximum does are listed, then their units
 // are read again, a unit a thread, so that one load's latency covers them all.
 template <int X>
-__device__ __forceinline__ void collect(Shared& sm, const char* x, int N, const Cut& cut, bool ring) {
+__device__ __forceinline__ void collect(Shared& sm, const char* x, int N, const Cut& cut, bool aligned) {
   constexpr int E = Slice<X>::E;
   const int tid = threadIdx.x;
   const float tau = sm.tau;
@@ -279,7 +307,7 @@ __device__ __forceinline__ void collect(Shared& sm, const char* x, int N, const 
     const int j0 = s * Slice<X>::kSlice + ((r % kUnits) * kThreads + who % kThreads) * E;
     if (j0 >= N) continue;
     uint32_t w[4];
-    if (ring && j0 + E <= N) {
+    if (aligned && j0 + E <= N) {
       const uint4 q = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)j0 * Elem<X>::kBytes));
       w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
     } else {
@@ -351,7 +379,7 @@ __device__ __forceinline__ void sums_by_definition(Shared& sm, const char* x, in
 // protects is not protected again.
 template <int X>
 __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, int64_t row, const char* x, int N,
-                                           const Cut& cut, State st, float best, int64_t tok, float xt, bool ring) {
+                                           const Cut& cut, State st, float best, int64_t tok, float xt, bool aligned) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
 #pragma unroll
   for (int y = 16; y > 0; y >>= 1) st = join(st, shuffle_down(st, y));
@@ -372,7 +400,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, i
 #pragma unroll
     for (int y = kWarps / 2; y > 0; y >>= 1) all = join(all, shuffle_down(all, y));
     if (lane == 0) {
-      const bool u = usual(M);
+      const bool u = usual<X>(M);
       const float ln_s = logf(all.S), lse = fmaf(kLn2, fmaf(-M, kL, all.m), ln_s);
       sm.M = M, sm.lse = lse;
       sm.count = 0, sm.hits = 0;
@@ -414,7 +442,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, i
     p.top_ids[row * K + r] = c.j;
     p.top_lp[row * K + r] = __fsub_rn(__fsub_rn(c.v, M), lse);
   };
-  if (kind != kNaN) collect<X>(sm, x, N, cut, ring);
+  if (kind != kNaN) collect<X>(sm, x, N, cut, aligned);
   __syncthreads();
   const int n = sm.count;
   if (kind != kNaN && n <= kBuffer) {
@@ -433,6 +461,10 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, Shared& sm, i
   }
 }
 
+__device__ __forceinline__ void copy_unit(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first `bytes` of a unit, then zeros.
 __device__ __forceinline__ void copy_unit(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -441,9 +473,40 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
                : "memory");
 }
 
+// A thread's half slice out of a stage whose units start 2 K bytes before the
+// row's: each is the end of the thread's and the start of the next one's.
+template <int K, int kPitch>
+__device__ __forceinline__ void read_shifted(uint32_t src, uint32_t* w) {
+#pragma unroll
+  for (int u = 0; u < kHalf; ++u, src += kPitch, w += 4) {
+    const uint4 a = ld_shared_v4(src), b = K ? ld_shared_v4(src + 16) : a;
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = K & 1 ? __byte_perm(v[i + K / 2], v[(i + K / 2 + 1) & 7], 0x5432) : v[i + K / 2];
+  }
+}
+template <int X, int kPitch>
+__device__ __forceinline__ void read_half(uint32_t src, int k, uint32_t* w) {
+  switch (k) {
+    case 0: return read_shifted<0, kPitch>(src, w);
+    case 2: return read_shifted<2, kPitch>(src, w);
+    case 4: return read_shifted<4, kPitch>(src, w);
+    case 6: return read_shifted<6, kPitch>(src, w);
+  }
+  if constexpr (X != 2) {
+    switch (k) {
+      case 1: return read_shifted<1, kPitch>(src, w);
+      case 3: return read_shifted<3, kPitch>(src, w);
+      case 5: return read_shifted<5, kPitch>(src, w);
+      case 7: return read_shifted<7, kPitch>(src, w);
+    }
+  }
+}
+
 // CL: rows are spread over clusters of p.cl CTAs, a row each; otherwise a
-// persistent grid takes a row a CTA.  RING: rows on 16-byte boundaries.
-template <int X, bool RING, bool CL>
+// persistent grid takes a row a CTA.  ALIGNED: rows on 16-byte boundaries.
+template <int X, bool ALIGNED, bool CL>
 __global__ void __launch_bounds__(kThreads, CL ? 2 : 4) logprobs_kernel(const LogprobParams p) {
   constexpr int E = Slice<X>::E, kSlice = Slice<X>::kSlice;
   extern __shared__ __align__(128) unsigned char dyn[];
@@ -459,34 +522,59 @@ __global__ void __launch_bounds__(kThreads, CL ? 2 : 4) logprobs_kernel(const Lo
   const char* base = static_cast<const char*>(p.x);
   const int64_t ld = p.ld_x * Elem<X>::kBytes;
 
-  // the thread's place in a stage, and the half slice to request next
-  const uint32_t mine = smem_u32(sm.ring[0]) + tid * 16;
-  constexpr uint32_t kStage = kThreads * kHalf * 16;
+  // the thread's place in a stage, and the half slice to request next.  Rows off
+  // 16-byte boundaries are copied from the boundary before: `off` bytes earlier,
+  // a warp's 33rd unit by its last lane, and a first unit that would start
+  // before the row not at all.
+  constexpr int kPitch = (ALIGNED ? kThreads : kThreads + kWarps) * 16;  // of a unit in a stage
+  constexpr uint32_t kStage = kHalf * kPitch;
   constexpr int kHalfBytes = kThreads * kHalf * 16;  // of the row, a half slice
+  constexpr int kFull = (kHalf - 1) * kThreads * 16 + (ALIGNED ? 16 : 32);
+  const uint32_t mine = smem_u32(sm.ring[0]) + (ALIGNED ? tid : tid + (tid >> 5)) * 16;
   const int halves = 2 * (s_end - s_beg);
+  const bool last = !ALIGNED && (tid & 31) == 31;
+  bool head = false;  // the thread's next unit starts before the row
   int64_t prow = first;
-  const char* pa = base + first * ld + (int64_t)s_beg * kSlice * Elem<X>::kBytes + tid * 16;
-  int phalf = 0, stage = 0;
-  int left = (N - s_beg * kSlice) * Elem<X>::kBytes - tid * 16;  // bytes from pa to the row's end; below 2^27
+  int phalf = 0, stage = 0, left;
+  const char* pa;
+  auto start_row = [&]() {
+    const char* x = base + prow * ld;
+    const int off = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(x) & 15);
+    pa = x - off + (int64_t)s_beg * kSlice * Elem<X>::kBytes + tid * 16;
+    left = (N - s_beg * kSlice) * Elem<X>::kBytes - tid * 16 + off;  // bytes from pa to the row's end; below 2^27
+    if (!ALIGNED) head = tid == 0 && s_beg == 0 && off != 0;
+  };
+  start_row();
   uint32_t pdst = mine;
   auto request = [&]() {
-    if constexpr (RING) {
-      if (prow < p.R && halves > 0) {
+    if (prow < p.R && halves > 0) {
+      if (left >= kFull && !head) {
+#pragma unroll
+        for (int u = 0; u < kHalf; ++u) {
+          copy_unit(pdst + u * kPitch, pa + u * (kThreads * 16));
+          if (last) copy_unit(pdst + u * kPitch + 16, pa + u * (kThreads * 16) + 16);
+        }
+      } else {
+        // (what is not copied is past the row's end, and replaced)
 #pragma unroll
         for (int u = 0; u < kHalf; ++u) {
           const int have = left - u * (kThreads * 16);
-          copy_unit(pdst + u * (kThreads * 16), have > 0 ? pa + u * (kThreads * 16) : base, min(16, max(0, have)));
+          if (have > 0 && !(u == 0 && head)) copy_unit(pdst + u * kPitch, pa + u * (kThreads * 16), min(16, have));
+          if (last && have > 16) copy_unit(pdst + u * kPitch + 16, pa + u * (kThreads * 16) + 16, min(16, have - 16));
         }
-        pa += kHalfBytes, left -= kHalfBytes;
-        if (++phalf == halves) {
-          phalf = 0;
-          prow += step;
-          pa += step * ld - (int64_t)halves * kHalfBytes, left += halves * kHalfBytes;
-        }
+        head = false;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      pdst = pdst == mine + (kStages - 1) * kStage ? mine : pdst + kStage;
+      pa += kHalfBytes, left -= kHalfBytes;
+      if (++phalf == halves) {
+        phalf = 0, prow += step;
+        if constexpr (ALIGNED)
+          pa += step * ld - (int64_t)halves * kHalfBytes, left += halves * kHalfBytes;
+        else
+          start_row();
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    pdst = pdst == mine + (kStages - 1) * kStage ? mine : pdst + kStage;
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) request();
@@ -494,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, CL ? 2 : 4) logprobs_kernel(const Lo
 
   for (int64_t row = first; row < p.R; row += step) {
     const char* x = base + row * ld;
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) & 15);
     int64_t tok = -1;  // its logit, requested early
     float xt = 0.0f;
     if (tid == 0 && rank == 0) {
@@ -509,23 +598,24 @@ __global__ void __launch_bounds__(kThreads, CL ? 2 : 4) logprobs_kernel(const Lo
       for (int s = g * cut.per_group; s < min(cut.slices, (g + 1) * cut.per_group); ++s) {
         const int j0 = s * kSlice + tid * E;
         uint32_t w[4 * kUnits];
-        if constexpr (RING) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        for (int half = 0; half < 2; ++half) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+          if constexpr (ALIGNED) {
 #pragma unroll
             for (int u = 0; u < kHalf; ++u) {
-              const uint4 q = ld_shared_v4(mine + stage * kStage + u * (kThreads * 16));
+              const uint4 q = ld_shared_v4(mine + stage * kStage + u * kPitch);
               const int i = 4 * (half * kHalf + u);
               w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
             }
-            stage = stage + 1 == kStages ? 0 : stage + 1;
-            request();  // into the stage read before this one
+          } else {
+            __syncwarp();  // the next lane's units are here, and the stage before this one is read
+            read_half<X, kPitch>(mine + stage * kStage, off >> 1, w + 4 * kHalf * half);
           }
-        } else {
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) load_unit_any<X>(x, j0 + u * kThreads * E, N, w + 4 * u);
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+          request();  // into the stage read before this one
         }
+        if (!ALIGNED && j0 == 0 && off != 0) load_unit_any<X>(x, 0, N, w);
         if ((s + 1) * kSlice > N) {
           if (j0 >= N) continue;  // nothing of this slice is this thread's
 #pragma unroll
@@ -554,22 +644,22 @@ __global__ void __launch_bounds__(kThreads, CL ? 2 : 4) logprobs_kernel(const Lo
         best = fmaxf(best, q.w);
       }
     }
-    finish_row<X>(p, sm, row, x, N, cut, total, best, tok, xt, RING);
+    finish_row<X>(p, sm, row, x, N, cut, total, best, tok, xt, ALIGNED);
   }
-  if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int X, bool RING>
+template <int X, bool ALIGNED>
 cudaError_t launch(const LogprobParams& p_in, int num_sms, cudaStream_t stream) {
   LogprobParams p = p_in;
   const Cut cut = cut_row(p.N, Slice<X>::kSlice);
   // Clusters while their CTAs fit the SMs, two each.
   p.cl = 1;
   while (2 * p.cl <= cut.groups && p.R * 2 * p.cl <= 2 * num_sms) p.cl *= 2;
-  constexpr int kSlot = 44 + (RING ? 0 : 6) + 2 * X;
+  constexpr int kSlot = 44 + (ALIGNED ? 0 : 6) + 2 * X;
   const bool clusters = p.cl > 1;
-  const void* fn = clusters ? reinterpret_cast<const void*>(&logprobs_kernel<X, RING, true>)
-                            : reinterpret_cast<const void*>(&logprobs_kernel<X, RING, false>);
+  const void* fn = clusters ? reinterpret_cast<const void*>(&logprobs_kernel<X, ALIGNED, true>)
+                            : reinterpret_cast<const void*>(&logprobs_kernel<X, ALIGNED, false>);
   const int bytes = clusters ? (int)sizeof(SharedCluster) : (int)sizeof(Shared);
   static_assert(2 * (sizeof(SharedCluster) + 1024) <= 228 * 1024 && 4 * (sizeof(Shared) + 1024) <= 228 * 1024,
                 "shared memory of an SM");
@@ -577,7 +667,7 @@ cudaError_t launch(const LogprobParams& p_in, int num_sms, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   if (!clusters) {
     const unsigned grid = (unsigned)std::min<int64_t>(p.R, 4 * (int64_t)num_sms);
-    logprobs_kernel<X, RING, false><<<grid, kThreads, bytes, stream>>>(p);
+    logprobs_kernel<X, ALIGNED, false><<<grid, kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -592,7 +682,7 @@ cudaError_t launch(const LogprobParams& p_in, int num_sms, cudaStream_t stream) 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<X, RING, true>, p);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<X, ALIGNED, true>, p);
 }
 
 }  // namespace
@@ -602,14 +692,14 @@ bi_status launch_logprobs(const LogprobParams& p, cudaStream_t stream, std::stri
   const bi_status st = current_device_info(&dev, why);
   if (st != BI_OK) return st;
   const int esz = p.x_kind == 2 ? 4 : 2;
-  const bool ring = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ld_x * esz % 16 == 0;
+  const bool aligned = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ld_x * esz % 16 == 0;
   cudaError_t e;
   if (p.x_kind == 2)
-    e = ring ? launch<2, true>(p, dev.num_sms, stream) : launch<2, false>(p, dev.num_sms, stream);
+    e = aligned ? launch<2, true>(p, dev.num_sms, stream) : launch<2, false>(p, dev.num_sms, stream);
   else if (p.x_kind == 1)
-    e = ring ? launch<1, true>(p, dev.num_sms, stream) : launch<1, false>(p, dev.num_sms, stream);
+    e = aligned ? launch<1, true>(p, dev.num_sms, stream) : launch<1, false>(p, dev.num_sms, stream);
   else
-    e = ring ? launch<0, true>(p, dev.num_sms, stream) : launch<0, false>(p, dev.num_sms, stream);
+    e = aligned ? launch<0, true>(p, dev.num_sms, stream) : launch<0, false>(p, dev.num_sms, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     *why = std::string("token log probabilities launch: ") + cudaGetErrorString(e);
