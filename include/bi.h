@@ -516,8 +516,9 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  * keys on a page outside [0, P) as absent; both are reported.  Rows past a
  * request's length are never read.
  *
- * Order: a request of n keys is cut into pieces of s = 256 * 2^k keys, k the
- * least with n <= 128 s -- a rule on its own length.  In a piece, warp w of W
+ * Order: a request of n keys is cut into pieces of s keys, s = 256 up to n =
+ * 2048, beyond that 512 * 2^k, k the least with n <= 128 s -- a rule on its own
+ * length.  In a piece, warp w of W
  * takes the tiles w, w + W, ... in order with a running maximum (tiles of 32
  * keys, 16 at D = 256; W = 4, or 8 at D = 256 and, for more than 8 query heads
  * a key-value head, at D = 128); p = 2^(t - m), t = RN(score * RN(scale
@@ -528,8 +529,9 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  *
  * workspace: caller-owned, 16-byte aligned, at least
  * bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes -- 0 when
- * W * page_size <= 256, else B * Hq * min(ceil(W * page_size / 256), 128) *
- * (D + 2) * 4.  Scratch, as in bi_attention_ws.
+ * W * page_size <= 256, else B * Hq * n * (D + 2) * 4, n the most pieces of a
+ * request: with L = W * page_size, ceil(L / 256) up to L = 2048, beyond that
+ * ceil(L / 512), but at least 8 and at most 128.  Scratch, as in bi_attention_ws.
  */
 int64_t bi_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len);
 bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const bi_tensor* v_cache,

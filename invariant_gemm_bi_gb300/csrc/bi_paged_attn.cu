@@ -39,8 +39,8 @@
 // (956 MB; 141 us at the copy rate of 6.79 TB/s): fragments loaded straight
 // into registers, 16 warps an SM, 250 us (each unit's first loads exposed);
 // shared-memory rings across units, 16-key tiles, 204 us (bound by issue, 512
-// instructions a tile and warp); 32-key tiles with transposing reads 163 us,
-// 5.87 TB/s, now near the memory's rate.
+// instructions a tile and warp); 32-key tiles with transposing reads 164 us,
+// longer pieces 160 us, 5.97 TB/s, now near the memory's rate.
 //
 // Arithmetic, per query head: t = RN(s c) with c = RN(scale log2 e); a running
 // maximum m per warp over its tiles; p = 2^(t - m) (the SFU's approximation);
@@ -60,16 +60,20 @@
 namespace bi {
 namespace {
 
-// A piece has at least 256 keys: 512 would save the join's traffic (159 us
-// against 163 for the batch above) but leave a short cache to few SMs (one
-// request of 1021 keys, joined by a second launch, 12.3 us against 9.9).  At most 128 pieces: 256 made
-// 131071 keys at D = 256 wait longer for the join than the evener split saved
-// (97.7 us against 97.1).
+// A piece has 256 keys up to 2048, a cluster's worth of them: 512 would leave a
+// short cache to few SMs (one request of 1021 keys, then joined by a second
+// launch, 12.3 us against 9.9).  Longer requests have at least 512: fewer
+// results to hand over and to join (the batch above 160 us against 164, 32 x
+// 4096 keys of 16 ungrouped heads 96 against 98, one request of 4096 keys, all
+// in a cluster then, 10.5 against 11.4; one of 8192 is left to fewer SMs, 14.0
+// against 12.8).  At most 128 pieces: 256 made 131071 keys at D = 256 wait
+// longer for the join than the evener split saved (97.7 us against 97.1).
 constexpr int kMinSplit = 256;
+constexpr int kMaxCluster = 8;
 constexpr int kManySplits = 128;
 
 __host__ __device__ inline int32_t paged_split_len(int64_t len) {
-  int64_t s = kMinSplit;
+  int64_t s = len <= kMaxCluster * kMinSplit ? kMinSplit : 2 * kMinSplit;
   while (len > kManySplits * s) s *= 2;
   return (int32_t)s;
 }
@@ -581,10 +585,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
       for (int e = threadIdx.x; e < heads * (D / 4); e += kThreads) {
         const int h = e / (D / 4), d = (e % (D / 4)) * 4;
         const uint32_t am = smem_u32(&sm.m[0][h]), al = smem_u32(&sm.l[0][h]), ao = smem_u32(&sm.o[0][h][d]);
-        float m[8], l[8], o[8][4];
+        float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster][4];
         float mx = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kMaxCluster; ++r) {
           if (r >= p.max_splits) break;
           m[r] = ld_shared_cluster_f32(cluster_map_shared(am, (uint32_t)r));
           l[r] = ld_shared_cluster_f32(cluster_map_shared(al, (uint32_t)r));
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
         const float ref = mx == -INFINITY ? 0.0f : mx;
         float sum = 0.0f, a[4] = {};
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kMaxCluster; ++r) {
           if (r >= p.max_splits) break;
           const float f = ex2_approx(m[r] - ref);
           sum = fmaf(f, l[r], sum);
@@ -741,8 +745,9 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
   // request's head tile, joined in place -- one launch, and no search for the
   // units (one request of 1021 keys: 6.9 us, 10.0 the other way).  The bits are
   // the same.
-  *joined = p.max_splits == 1 || (p.max_splits <= 8 && most <= (int64_t)num_sms * Sh::kCtas);
-  if (p.max_splits <= 8 && most <= (int64_t)num_sms * Sh::kCtas) {
+  const bool one = p.max_splits <= kMaxCluster && most <= (int64_t)num_sms * Sh::kCtas;
+  *joined = p.max_splits == 1 || one;
+  if (one) {
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS, true>), kBytes, kSlot + 40);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -787,7 +792,9 @@ cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream
 }  // namespace
 
 int32_t paged_max_splits(int64_t cap) {
-  return cap >= (int64_t)kManySplits * kMinSplit ? kManySplits : split_count(cap);
+  if (cap <= kMaxCluster * kMinSplit) return split_count(cap);
+  if (cap >= (int64_t)kManySplits * 2 * kMinSplit) return kManySplits;
+  return std::max(split_count(cap), (int32_t)kMaxCluster);  // or a request of 2048 keys
 }
 
 bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::string* why) {

@@ -369,6 +369,21 @@ def test_attention_bits_do_not_depend_on_the_table_width(D, Hq, Hkv, out):
         ref.assert_within(o, want, bound)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (128, 8, 2), (256, 4, 1)])
+def test_attention_bits_where_pieces_grow(D, Hq, Hkv):
+    # 256 keys a piece up to 2048, 512 from there on: alone in narrow tables and
+    # together in wide ones
+    lens = [2047, 2048, 2049, 2560, 4095, 4096, 4097, 1, 65536, 65537]
+    kc, vc, table, ln = _cache(lens, 16, Hkv, D, BF16, 47)
+    q = _normal((len(lens), Hq, D), BF16, 48)
+    o = bi.bi_paged_attention(q, kc, vc, table, ln, 0.1, out_dtype=F32)
+    for i, n in enumerate(lens):
+        own = table[i:i + 1, :(n + 15) // 16].contiguous()
+        assert bits_equal(bi.bi_paged_attention(q[i:i + 1], kc, vc, own, ln[i:i + 1], 0.1, out_dtype=F32), o[i:i + 1]), n
+    want, bound = ref.attention(q, kc, vc, table, ln, 0.1, F32)
+    ref.assert_within(o, want, bound)
+
+
 def test_attention_strided_operands():
     lens, page, Hkv, D, Hq = [300, 33], 16, 2, 64, 4
     kc, vc, table, ln = _cache(lens, page, Hkv, D, F16, 50)

@@ -241,7 +241,8 @@ def test_attention_workspace_rule(lib):
     row = 2 * 4 * 66 * 4
     assert n(0) == n(1) == n(256) == 0
     assert n(257) == 2 * row and n(513) == 3 * row
-    assert n(128 * 256) == n(128 * 256 + 1) == n(1 << 30) == 128 * row  # never more than 128 pieces
+    assert n(2048) == n(2049) == n(4096) == 8 * row and n(4097) == 9 * row  # longer requests have longer pieces
+    assert n(128 * 512) == n(128 * 512 + 1) == n(1 << 30) == 128 * row  # never more than 128 pieces
     assert n(1000, D=96) == 0 and n(1000, B=0) == 0
 
 
