@@ -600,6 +600,24 @@ def test_logprobs_rows_do_not_depend_on_batch_or_layout(N):
     assert bits_equal(only.logprobs, r.logprobs)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("R,N", [(3, 5), (3, 4099), (5, 20003), (400, 9001), (700, 37)])
+def test_logprobs_rows_at_any_offset(dt, R, N):
+    # rows of every alignment, among NaNs: the bits of rows on boundaries
+    x = _normal((R, N), dt, 129, std=2.0)
+    x[1, ::3] = float("-inf")
+    tokens = torch.randint(0, N, (R,), generator=_gen(130), device="cuda")
+    even = torch.full((R, (N + 15) // 8 * 8), float("nan"), dtype=dt, device="cuda")
+    even[:, :N] = x
+    r = bi.bi_token_logprobs(even[:, :N], tokens, top=min(N, 6))
+    for at in range(8):
+        for pad in (9, 16 - N % 8):  # another alignment every row, the same for all
+            wide = torch.full((R, N + pad), float("nan"), dtype=dt, device="cuda")
+            wide[:, at:at + N] = x
+            s = bi.bi_token_logprobs(wide[:, at:at + N], tokens, top=min(N, 6))
+            assert all(bits_equal(a, b) for a, b in zip(r, s)), (at, pad)
+
+
 @pytest.mark.parametrize("dt,N,R", [(BF16, 128256, 330), (F32, 40001, 320), (F16, 16385, 310), (BF16, 70004, 310),
                                     (F32, 128256, 310), (F32, 9000, 310)])
 def test_logprobs_many_long_rows(dt, N, R):
