@@ -510,7 +510,7 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  *   page_table [B,W] int32, unit stride on W; seq_lens [B] int32; any
  *   page_size >= 1 with P * page_size < 2^31 and W * page_size <= 2^30; B <= 2^22.
  *   q, caches and o: unit stride on D, 16-byte aligned, other strides
- *   multiples of 16 bytes.  scale finite.
+ *   multiples of 16 bytes.  scale and scale * log2(e) finite.
  * A request of length <= 0 gives zeros (the new token itself is normally in
  * the cache by then).  A length past W * page_size counts as W * page_size,
  * keys on a page outside [0, P) as absent; both are reported.  Rows past a

@@ -472,7 +472,8 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   c.that(k_cache->dtype == q->dtype && v_cache->dtype == q->dtype, BI_ERR_UNSUPPORTED_DTYPE,
          "the caches must have q's type");
   c.that(attention_head_dim_ok(D), BI_ERR_INVALID_ARG, "head dimension must be 64, 128 or 256");
-  c.that(std::isfinite(scale), BI_ERR_INVALID_ARG, "scale must be finite");
+  const float score_log2 = (float)((double)scale * 1.4426950408889634);
+  c.that(std::isfinite(score_log2), BI_ERR_INVALID_ARG, "scale and scale * log2(e) must be finite");
   c.that(ps >= 1, BI_ERR_INVALID_ARG, "page_size must be positive");
   c.that(Hkv >= 1 ? Hq % Hkv == 0 : Hq == 0, BI_ERR_SHAPE_MISMATCH, "Hkv must divide Hq");
   c.that(P * ps <= INT32_MAX, BI_ERR_INVALID_ARG, "P * page_size must be below 2^31");
@@ -523,7 +524,7 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   p.ps_shift = (ps & (ps - 1)) == 0 ? __builtin_ctzll((unsigned long long)ps) : -1;
   p.in_f16 = q->dtype == BI_F16;
   p.out_kind = kind_of(o->dtype);
-  p.score_log2 = (float)((double)scale * 1.4426950408889634);
+  p.score_log2 = score_log2;
   c.st = launch_paged_attention(p, (cudaStream_t)stream, &c.why);
   return abi_finish(c.st, c.why);
 }

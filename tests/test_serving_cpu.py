@@ -314,6 +314,10 @@ def test_numbers_that_steps_would_carry_past_32_bits_are_refused(lib):
                  offs=lambda a, o: a.t([n + 1], I32)) == INVALID
 
 
+def test_scales_whose_base_2_form_overflows_are_refused(lib):
+    assert _attend(lib, scale=3e38) == INVALID and _attend(lib, scale=-3e38) == INVALID
+
+
 def test_integer_types_stay_refused_elsewhere(lib):
     a = Arena()
     assert lib.bi_mm(_r(a.t([4, 64], I32)), _r(a.t([64, 32], I32)), _r(a.t([4, 32], F32)), None) == DTYPE
