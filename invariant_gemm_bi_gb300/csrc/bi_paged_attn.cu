@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
       named_barrier(kBarUpper, kThreads);
       take_over(warp);
       if (warp > 0) {
+        __syncwarp();     // every lane has read the maxima and sums that some lanes replace now
         hand_over(warp);  // where this warp alone has just read
         barrier_arrive(kBarLower, 32 * H);
       } else {
