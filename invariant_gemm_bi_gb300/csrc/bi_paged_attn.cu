@@ -45,10 +45,13 @@
 // Arithmetic, per query head: t = RN(s c) with c = RN(scale log2 e); a running
 // maximum m per warp over its tiles; p = 2^(t - m) (the SFU's approximation);
 // l sums the unrounded p in fp32; the value product takes p in the cache's
-// 16-bit type, the tensor core's operand type, as a sum of two such numbers (22
-// bits of fp16, 16 of bf16; three bf16, 24 bits, for an fp32 result): one
-// alone, rounded, would be off as much as the 16-bit result's own rounding, and
-// the second costs 0.2 % (161.1 us and 161.3 for the batch above).  O in fp32.
+// 16-bit type, the tensor core's operand type, as a sum of such numbers: three
+// of bf16 (24 bits) or two of fp16 (22 bits).  One alone, rounded, would be off
+// as much as a 16-bit result's own rounding; two of bf16 turn the rounding of
+// one result in 500 (against an fp32 evaluation; three: one in 2000).  A piece
+// more costs 0.2 % (160.1 us and 160.5 for the batch above; the request of 1021
+// keys 6.9 us and 7.1).  A result of 16 bits is the fp32 result rounded once.
+// O in fp32.
 // Warps are joined in a fixed tree, pieces in fixed groups in piece order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -195,15 +198,15 @@ __device__ __forceinline__ void barrier_arrive(uint32_t id, uint32_t count) {
 // The join's barriers: upper warps' results written; the rest's written; all read.
 constexpr uint32_t kBarUpper = 1, kBarLower = 2, kBarRead = 3;
 
-// PS: 16-bit pieces of p in the value product: 2 of fp16, or of bf16 2 for a
-// 16-bit result and 3 for an fp32 one.  ONE: a cluster has one (request, head
-// tile), a CTA each of its pieces, and joins them itself.
-template <int F16, int D, int NT, int PS, bool ONE>
+// ONE: a cluster has one (request, head tile), a CTA each of its pieces, and
+// joins them itself.
+template <int F16, int D, int NT, bool ONE>
 __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) paged_attn_kernel(const PagedAttnParams p) {
   using Sh = Shape<D, NT>;
   extern __shared__ __align__(1024) unsigned char dyn[];
   typename Sh::Shared& sm = *reinterpret_cast<typename Sh::Shared*>(dyn);
   constexpr int W = Sh::W, H = W / 2, kThreads = 32 * W, KT = Sh::KT, KJ = Sh::KJ, MT = D / 16;
+  constexpr int PS = F16 ? 2 : 3;  // 16-bit pieces of p in the value product
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 
   const int inner = p.Hkv * p.head_tiles;
@@ -733,13 +736,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
 }
 
 // *joined: whether the launch leaves nothing to join.
-template <int F16, int D, int NT, int PS>
+template <int F16, int D, int NT>
 cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
   using Sh = Shape<D, NT>;
   constexpr int kBytes = sizeof(typename Sh::Shared);
   static_assert(kBytes <= 227 * 1024 && Sh::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
   // one slot per instance, from 24 on (ONE: from 64 on)
-  constexpr int kSlot = 24 + (D == 256 ? 16 + 2 * F16 + PS - 2 : (D == 128 ? 8 : 0) + 4 * F16 + 2 * (NT - 1) + PS - 2);
+  constexpr int kSlot = 24 + (D == 256 ? 8 + F16 : (D == 128 ? 4 : 0) + 2 * F16 + NT - 1);
   p.head_tiles = (p.group + 8 * NT - 1) / (8 * NT);
   const int64_t most = (int64_t)p.B * p.max_splits * p.Hkv * p.head_tiles;
   // Short caches whose units all run at once: a CTA a unit and a cluster a
@@ -749,7 +752,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
   const bool one = p.max_splits <= kMaxCluster && most <= (int64_t)num_sms * Sh::kCtas;
   *joined = p.max_splits == 1 || one;
   if (one) {
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS, true>), kBytes, kSlot + 40);
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, true>), kBytes, kSlot + 40);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)most);
@@ -763,21 +766,13 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<F16, D, NT, PS, true>, p);
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<F16, D, NT, true>, p);
   }
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, PS, false>), kBytes, kSlot);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, false>), kBytes, kSlot);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms * Sh::kCtas);
-  paged_attn_kernel<F16, D, NT, PS, false><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
+  paged_attn_kernel<F16, D, NT, false><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
   return cudaGetLastError();
-}
-
-template <int F16, int D, int NT>
-cudaError_t launch_out(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
-  if constexpr (F16)
-    return launch<F16, D, NT, 2>(p, num_sms, joined, stream);
-  else
-    return p.out_kind == 2 ? launch<F16, D, NT, 3>(p, num_sms, joined, stream) : launch<F16, D, NT, 2>(p, num_sms, joined, stream);
 }
 
 template <int F16>
@@ -785,9 +780,9 @@ cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream
   // more than eight query heads a key-value head: 16 a unit, except at
   // D = 256, where two tiles' accumulators would not fit the registers
   const bool wide = p.group > 8;
-  if (p.D == 64) return wide ? launch_out<F16, 64, 2>(p, num_sms, joined, stream) : launch_out<F16, 64, 1>(p, num_sms, joined, stream);
-  if (p.D == 128) return wide ? launch_out<F16, 128, 2>(p, num_sms, joined, stream) : launch_out<F16, 128, 1>(p, num_sms, joined, stream);
-  return launch_out<F16, 256, 1>(p, num_sms, joined, stream);
+  if (p.D == 64) return wide ? launch<F16, 64, 2>(p, num_sms, joined, stream) : launch<F16, 64, 1>(p, num_sms, joined, stream);
+  if (p.D == 128) return wide ? launch<F16, 128, 2>(p, num_sms, joined, stream) : launch<F16, 128, 1>(p, num_sms, joined, stream);
+  return launch<F16, 256, 1>(p, num_sms, joined, stream);
 }
 
 }  // namespace

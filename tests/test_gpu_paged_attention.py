@@ -63,3 +63,15 @@ def test_repeated_calls_give_the_same_bits(D, Hq, Hkv, lens, width):
             again = bi.bi_paged_attention(q, kc, vc, table, ln, D ** -0.5, out_dtype=out)
             differ += (again != first).sum()
         assert differ.item() == 0 and bits_equal(again, first)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 32, 8), (64, 3, 1), (128, 24, 2), (256, 5, 1), (64, 32, 2)])
+@pytest.mark.parametrize("lens,width", [([1021], 0), ([255, 3, 0, 2048], 400), ([9000, 250, 4097], 0)])
+def test_results_of_16_bits_are_those_of_32_rounded(dt, D, Hq, Hkv, lens, width):
+    P, table = _tables(lens, 16, 5, width)
+    kc, vc = _normal((P, 16, Hkv, D), dt, 6), _normal((P, 16, Hkv, D), dt, 7)
+    q, ln = _normal((len(lens), Hq, D), dt, 8), _i32(lens)
+    o = bi.bi_paged_attention(q, kc, vc, table, ln, D ** -0.5)
+    for out in (BF16, F16):
+        assert bits_equal(bi.bi_paged_attention(q, kc, vc, table, ln, D ** -0.5, out_dtype=out), o.to(out))
