@@ -525,7 +525,8 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  * log2 e)).  Warp w + W/2 is joined into warp w, then warps 1, 2, ... into
  * warp 0, groups of 16 pieces in piece order, then the groups in order, all in
  * fp32.  Sums are of the unrounded p; the product with v takes p as the
- * sum of three bf16 or of two fp16.  A 16-bit o is the fp32 o rounded once.
+ * sum of three bf16 or of two fp16 (of 2^15 p: what is below 2^-40 of a warp's
+ * largest p is not in o).  A 16-bit o is the fp32 o rounded once.
  *
  * workspace: caller-owned, 16-byte aligned, at least
  * bi_paged_attention_workspace_bytes(B, Hq, D, W * page_size) bytes -- 0 when

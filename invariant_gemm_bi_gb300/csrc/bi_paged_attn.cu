@@ -51,7 +51,10 @@
 // one result in 500 (against an fp32 evaluation; three: one in 2000).  A piece
 // more costs 0.2 % (160.1 us and 160.5 for the batch above; the request of 1021
 // keys 6.9 us and 7.1).  A result of 16 bits is the fp32 result rounded once.
-// O in fp32.
+// fp16 ends at 2^-24, so there p is carried times 2^15 (and the final division
+// takes it off): a weight is then cut at 2^-40 of the largest beside it and not
+// at 2^-25, where a long cache's many small ones would be missing in O and yet
+// counted in l.  O in fp32: n 2^15 times the largest value at most, 2^61.
 // Warps are joined in a fixed tree, pieces in fixed groups in piece order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -99,6 +102,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// What p is multiplied by before it is cut into 16-bit numbers, and its reciprocal.
+template <int F16>
+struct Up {
+  static constexpr float v = F16 ? 32768.0f : 1.0f, back = 1.0f / v;
+};
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -453,6 +461,10 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
           for (int x = 0; x < PS; ++x) {
             float(&e)[4] = s[t][n];
+            if (F16 && x == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] *= Up<F16>::v;
+            }
             const uint32_t lo = pack16<F16>(e[0], e[1]), hi = pack16<F16>(e[2], e[3]);
             pf[t][n][x][0] = transpose8x8(lo);
             pf[t][n][x][1] = transpose8x8(hi);
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
             const int hh = 8 * n + 2 * c + h;
             if (hh >= heads) continue;
             if (pieces == 1) {
-              const float inv = l[n][h] == 0.0f ? 0.0f : __frcp_rn(l[n][h]);  // no key: zeros
+              const float inv = l[n][h] == 0.0f ? 0.0f : __frcp_rn(l[n][h]) * Up<F16>::back;  // no key: zeros
               const int64_t at = u.b * p.o_b + (head + hh) * p.o_h + g;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
@@ -611,7 +623,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = fmaf(f, o[r][i], a[i]);
         }
-        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);  // no key: zeros
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum) * Up<F16>::back;  // no key: zeros
         const int64_t at = u.b * p.o_b + (head + h) * p.o_h + d;
 #pragma unroll
         for (int i = 0; i < 4; ++i) store_one(p.o, p.out_kind, at + i, __fmul_rn(a[i], inv));
@@ -722,7 +734,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
       join_into<V>(r, x.m, x.l, x.o);
     }
   }
-  const float inv = r.l == 0.0f ? 0.0f : __frcp_rn(r.l);
+  const float inv = r.l == 0.0f ? 0.0f : __frcp_rn(r.l) * (p.in_f16 ? Up<1>::back : Up<0>::back);
   const int64_t at = b * p.o_b + h * p.o_h + d0 + 2 * lane;
 #pragma unroll
   for (int v = 0; v < V; ++v) {

@@ -1,0 +1,71 @@
+"""Plain 64-bit forms of the serving operations with bounds that count the
+roundings of the kernels' own order, for tests of what a looser bound would hide."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+from tests.serving_reference import HALF_STEP, SUBNORMAL, f64
+
+
+# -- attention ---------------------------------------------------------------------
+
+def split_len(n):
+    """Keys of a piece of a request of n keys."""
+    s = 256 if n <= 2048 else 512
+    while n > 128 * s:
+        s *= 2
+    return s
+
+
+def attention_rel(n, D, group, dtype, A):
+    """Relative error of a result, of sum p |v|, from the order that the header states.
+
+    A: the largest scale * sum |q_d k_d|.  A score takes D / 16 tensor-core steps, each
+    off by at most 2^-22 of A, and two roundings: eps_t in base 2 and, after t - m (at most
+    2 A log2 e apart, 2^-24), in the exponent.  2^x is good to 2^-21; a key's weight goes
+    through one for itself, one for every later tile of its warp that raises the maximum, and
+    one in each join (two of warps for each of the H, one of pieces, one of groups).
+    The weights count in the sum of v and in the sum that it is divided by.
+    Sums of p v: a tensor-core step for each 16 keys of a warp and piece of p, 2^-22 each;
+    a product with a raised maximum's factor a tile, and two roundings a join, 2^-24 each:
+    H of warps, 16 of pieces, 8 of groups.  Sums of p: 2 KT adds of a tile and lane and one
+    to the running sum, 3 of lanes, and the joins.  Pieces of p: 2^-24 (three bf16) or
+    2^-22 (two fp16).  The division, two roundings."""
+    W = 8 if D == 256 or (D == 128 and group > 8) else 4
+    KT = 1 if D == 256 else 2
+    H = W // 2
+    own = -(-min(split_len(n), n) // (W * 16 * KT)) * 16 * KT  # keys of a warp
+    tiles = own // (16 * KT)
+    pieces, u = (2, 2.0 ** -22) if dtype == torch.float16 else (3, 2.0 ** -24)
+    eps_t = A * math.log2(math.e) * (D / 16 * 2.0 ** -22 + 2.0 ** -23 + 2.0 ** -23)
+    weight = math.log(2) * eps_t + (1 + tiles + H + 2) * 2.0 ** -21
+    joins = 2 * (H + 16 + 8) * 2.0 ** -24
+    sums = own / 16 * pieces * 2.0 ** -22 + tiles * 2.0 ** -24 + joins
+    total = (tiles * (2 * KT + 2) + 3) * 2.0 ** -24 + joins
+    return u + 2 * weight + sums + total + 2.0 ** -22
+
+
+def attention(q, k, v, scale, dtype, out_dtype):
+    """(result, bound) of one request: q [Hq, D] over its keys and values [n, Hkv, D] in order."""
+    q, k, v = (f64(x) if isinstance(x, torch.Tensor) else x for x in (q, k, v))
+    (Hq, D), (n, Hkv, _) = q.shape, k.shape
+    G = Hq // Hkv
+    ref, bound = np.zeros((Hq, D)), np.zeros((Hq, D))
+    for g in range(Hkv):
+        kh, vh, qh = k[:, g], v[:, g], q[g * G:(g + 1) * G]
+        s = scale * (qh @ kh.T)
+        A = abs(scale) * (np.abs(qh) @ np.abs(kh).T).max()
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        o = p @ vh
+        err = attention_rel(n, D, G, dtype, A) * (p @ np.abs(vh))
+        if dtype == torch.float16:
+            # p is scaled by 2^15 before it is cut into fp16 numbers, whose subnormals are
+            # 2^-24 apart: 2^-40 of a warp's largest weight, which is at most the largest
+            err = err + 2.0 ** -40 * p.max(-1, keepdims=True) * np.abs(vh).sum(0)
+        ref[g * G:(g + 1) * G] = o
+        bound[g * G:(g + 1) * G] = err + (np.abs(o) + err) * HALF_STEP[out_dtype] + SUBNORMAL[out_dtype]
+    return ref, bound

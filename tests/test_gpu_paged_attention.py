@@ -2,10 +2,13 @@
 mass of every piece of a long cache, and results of 16 bits beside those of 32."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 from invariant_gemm_bi_gb300 import binding as bi
+from tests import serving_reference as ref
+from tests import serving_tight as tight
 from tests.gpu_helpers import bits_equal
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +78,27 @@ def test_results_of_16_bits_are_those_of_32_rounded(dt, D, Hq, Hkv, lens, width)
     o = bi.bi_paged_attention(q, kc, vc, table, ln, D ** -0.5)
     for out in (BF16, F16):
         assert bits_equal(bi.bi_paged_attention(q, kc, vc, table, ln, D ** -0.5, out_dtype=out), o.to(out))
+
+
+# Every sixteenth key, so some of every warp, stands above all others by x bits and has
+# no value: the result is the others' weights alone, which are small beside those they
+# are computed next to.
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("D,Hq", [(64, 4), (64, 12), (128, 4), (128, 12), (256, 3)])
+@pytest.mark.parametrize("n", [256, 700, 5000])
+@pytest.mark.parametrize("x", [12.0, 20.5, 25.5, 28.3, 33.0])
+def test_small_weights_beside_large_ones_keep_their_share(dt, D, Hq, n, x):
+    P, table = _tables([n], 16, 9)
+    j = torch.arange(n, device="cuda")
+    k, v = torch.zeros(n, 1, D, device="cuda"), torch.full((n, 1, D), 1024.0, device="cuda")
+    k[::16, 0, 0], v[::16] = x * 0.6931471805599453, 0.0
+    k, v = k.to(dt), v.to(dt)
+    kc, vc = torch.zeros(P, 16, 1, D, dtype=dt, device="cuda"), torch.zeros(P, 16, 1, D, dtype=dt, device="cuda")
+    page = table[0, j // 16].long()
+    kc[page, j % 16], vc[page, j % 16] = k, v
+    q = torch.zeros(1, Hq, D, dtype=dt, device="cuda")
+    q[..., 0] = 1.0
+    o = bi.bi_paged_attention(q, kc, vc, table, _i32([n]), 1.0)
+    want, bound = tight.attention(q[0], k, v, 1.0, dt, F32)
+    assert np.all(want > 0) and np.all(bound < 0.02 * want)  # a bound that a lost weight would break
+    ref.assert_within(o[0], want, bound)
