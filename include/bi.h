@@ -431,8 +431,9 @@ bi_status bi_paged_plan(const bi_tensor* context_lens, const bi_tensor* new_lens
  * with (x1, x2) the elements (i, i + rotary_dim/2) of the head, or (2i, 2i+1)
  * when interleaved; elements from rotary_dim on are copied.  a = magnitude.
  * A configuration is host memory that a program fills once; calls copy it.
- * Angles are exact to the fp32 rounding of the reduced angle at any position
- * (the product n * f_i is taken modulo one turn in 64-bit integers).
+ * Frequencies are doubles.  n * f_i is taken modulo one turn in 64-bit
+ * integers, f_i / (2 pi) rounded to 2^-64 once: the reduced angle is off by |n|
+ * 2^-65 turns at most (1.9e-7 radians times |n| / 2^40) and its rounding to fp32.
  */
 #define BI_ROPE_MAX_PAIRS 128
 
@@ -466,7 +467,7 @@ typedef struct {
 /* Fills *out; scaling may be NULL (plain).  base > 1; magnitude finite.  Host only. */
 bi_status bi_rope_init(bi_rope_config* out, int32_t rotary_dim, int32_t interleaved, double base,
                        const bi_rope_scaling* scaling, double magnitude);
-/* The same with the rotary_dim / 2 angular frequencies given (finite). */
+/* The same with the rotary_dim / 2 angular frequencies given (below 2^53 in magnitude). */
 bi_status bi_rope_init_frequencies(bi_rope_config* out, int32_t rotary_dim, int32_t interleaved,
                                    const double* frequencies, double magnitude);
 

@@ -204,6 +204,60 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
+constexpr double kMaxFrequency = 9007199254740992.0;  // 2^53
+
+// A number of 256 bits, the last one 2^-192; w[3] is the whole part.
+struct Fixed {
+  uint64_t w[4];
+};
+bool at_least(const Fixed& a, const Fixed& b) {
+  for (int i = 3; i >= 0; --i)
+    if (a.w[i] != b.w[i]) return a.w[i] > b.w[i];
+  return true;
+}
+void subtract(Fixed& a, const Fixed& b) {
+  uint64_t borrow = 0;
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = a.w[i] - b.w[i], y = x - borrow;
+    borrow = (a.w[i] < b.w[i]) | (x < borrow);
+    a.w[i] = y;
+  }
+}
+Fixed shifted(const Fixed& a, int n) {  // left, by 0 .. 255
+  Fixed r = {};
+  for (int i = 3; i >= n / 64; --i) {
+    const int k = i - n / 64;
+    r.w[i] = a.w[k] << n % 64;
+    if (n % 64 && k > 0) r.w[i] |= a.w[k - 1] >> (64 - n % 64);
+  }
+  return r;
+}
+
+// 2^64 * (f / (2 pi) mod 1), rounded to nearest, 0 <= f < 2^53: binary long
+// division by 2 pi, since a quotient in doubles would be off by up to 2^-56 of
+// a turn for f near 1 -- 2^8 of the phase's units, and a millionth of a radian
+// at positions around 2^33.  (2 pi's bits past 2^-192 move the quotient by
+// 2^-139 at most.)
+uint64_t turns_of(double f) {
+  if (f < 1.0842021724855044e-19 /* 2^-63 */) return 0;  // below 2^-65 of a turn
+  const Fixed turn = {{0x48127044533e63a0ull, 0x2633145c06e0e689ull, 0x487ed5110b4611a6ull, 6}};  // 2 pi
+  int e;
+  const double m = std::frexp(f, &e);  // f = m 2^e, -62 <= e <= 53
+  Fixed rest = shifted({{(uint64_t)std::ldexp(m, 53), 0, 0, 0}}, 192 + e - 53);
+  for (int k = 51; k >= 0; --k) {  // whole turns
+    const Fixed d = shifted(turn, k);
+    if (at_least(rest, d)) subtract(rest, d);
+  }
+  uint64_t q = 0;
+  for (int k = 0; k <= 64; ++k) {  // 64 bits of the fraction, and the one that rounds them
+    rest = shifted(rest, 1);
+    const bool bit = at_least(rest, turn);
+    if (bit) subtract(rest, turn);
+    q = k < 64 ? q << 1 | bit : q + bit;
+  }
+  return q;
+}
+
 bi_status rope_config_ok(const bi_rope_config* cfg, std::string* why) {
   if (cfg->rotary_dim < 2 || cfg->rotary_dim > 2 * BI_ROPE_MAX_PAIRS || cfg->rotary_dim % 2 != 0 ||
       (cfg->interleaved != 0 && cfg->interleaved != 1) || !std::isfinite(cfg->magnitude)) {
@@ -264,15 +318,10 @@ extern "C" bi_status bi_rope_init_frequencies(bi_rope_config* out, int32_t rotar
   if (st != BI_OK)
     return abi_finish(st, "rotary_dim must be even and within [2, 256], the magnitude finite");
   for (int i = 0; i < rotary_dim / 2; ++i) {
-    if (!std::isfinite(frequencies[i])) return abi_finish(BI_ERR_INVALID_ARG, "a frequency is not finite");
-    double turns = frequencies[i] / kTwoPi;
-    turns -= std::floor(turns);
-    if (turns >= 1.0) turns = 0.0;  // a tiny negative frequency rounds up to a whole turn
-    // Two 32-bit halves, the low one rounded: 2^-65 of a turn at most is lost
-    // (bits of a frequency below 2^-11 that lie past the 64-bit fraction).
-    const double hi = std::floor(std::ldexp(turns, 32));
-    const double lo = std::nearbyint(std::ldexp(turns, 64) - std::ldexp(hi, 32));
-    cfg.phase[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+    if (!(std::fabs(frequencies[i]) < kMaxFrequency))
+      return abi_finish(BI_ERR_INVALID_ARG, "a frequency is not finite, or 2^53 or more");
+    const uint64_t turns = turns_of(std::fabs(frequencies[i]));
+    cfg.phase[i] = frequencies[i] < 0.0 ? 0 - turns : turns;
   }
   *out = cfg;
   return abi_finish(BI_OK, "");

@@ -69,3 +69,43 @@ def attention(q, k, v, scale, dtype, out_dtype):
         ref[g * G:(g + 1) * G] = o
         bound[g * G:(g + 1) * G] = err + (np.abs(o) + err) * HALF_STEP[out_dtype] + SUBNORMAL[out_dtype]
     return ref, bound
+
+
+# -- rotary positions -----------------------------------------------------------------
+
+PI_BITS = 1400
+
+
+def _pi():
+    """pi * 2^PI_BITS, by 16 arctan(1/5) - 4 arctan(1/239)."""
+    one = 1 << (PI_BITS + 32)
+
+    def arctan_inverse(x):
+        term = total = one // x
+        k, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // k)
+            k, sign = k + 2, -sign
+        return total
+    return (16 * arctan_inverse(5) - 4 * arctan_inverse(239)) >> 32
+
+
+PI = _pi()
+
+
+def turns(f, n, bits):
+    """n f / (2 pi) modulo one turn, in units of 2^-bits turns, rounded down (a double f, an integer n)."""
+    num, den = float(f).as_integer_ratio()
+    # num n / den / (2 pi) = num n 2^PI_BITS / (2 PI den)
+    return ((num * int(n)) << (PI_BITS + bits)) // (2 * PI * den) % (1 << bits)
+
+
+def angles(freq, pos):
+    """The reduced angles in (-pi, pi], [positions, pairs], to the precision of a double."""
+    out = np.zeros((len(pos), len(freq)))
+    for i, n in enumerate(pos):
+        for j, f in enumerate(freq):
+            t = turns(f, n, 128)
+            out[i, j] = (t - (1 << 128) if t > 1 << 127 else t) / 2.0 ** 127 * math.pi
+    return out

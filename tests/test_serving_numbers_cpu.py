@@ -1,0 +1,57 @@
+"""Numbers of the serving operations that the host computes, against big integers; and
+that the bounds of tests/serving_tight.py reject what they are meant to."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from invariant_gemm_bi_gb300 import binding, build
+from tests import serving_tight as tight
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.load()
+
+
+def test_pi():
+    assert tight.PI >> (tight.PI_BITS - 60) == 3622009729038561421  # 3.14159265358979323846... 2^60
+    assert abs(tight.PI / 2 ** tight.PI_BITS - math.pi) <= 2.0 ** -52
+
+
+def _phases(f):
+    cfg = binding.bi_rope_config(2 * len(f), frequencies=f)
+    return [int(p) for p in cfg.desc.phase[:len(f)]]
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1e6])
+@pytest.mark.parametrize("rotary", [64, 128, 256])
+def test_phases_are_the_nearest_of_64_bits(base, rotary):
+    f = [base ** (-2.0 * i / rotary) for i in range(rotary // 2)]
+    for x, p in zip(f, _phases(f)):
+        # 2^64 of a turn, off by half of one and 2^-10 for the division's own truncation
+        exact = tight.turns(x, 1, 80)
+        assert abs((p << 16) - exact) <= (1 << 15) + (1 << 6), x
+
+
+def test_phases_of_any_frequency():
+    rng = np.random.default_rng(7)
+    f = [1.0, 0.75, 2 * math.pi, math.pi, 3.0, 1e-3, 1e-12, 2.0 ** -62, 2.0 ** -63, 2.0 ** -64, 1e-300, 5e-324, 0.0,
+         1e9, 2.0 ** 40 + 1.0, 2.0 ** 52 + 1.0, 2.0 ** 53 - 1.0]
+    f += [float(x) for x in np.exp(rng.uniform(math.log(2.0 ** -66), math.log(2.0 ** 53), 100))]
+    got, mirrored = _phases(f), _phases([-x for x in f])
+    for x, p, q in zip(f, got, mirrored):
+        d = ((p << 16) - tight.turns(x, 1, 80)) % (1 << 80)
+        assert min(d, (1 << 80) - d) <= (1 << 15) + (1 << 6), x
+        assert (p + q) % (1 << 64) == 0, x  # a negative frequency is its complement of a turn
+    assert got[12] == 0
+
+
+@pytest.mark.parametrize("f", [2.0 ** 53, -2.0 ** 53, 1e300, float("inf"), float("nan")])
+def test_frequencies_without_a_fraction_of_a_turn_are_refused(f):
+    with pytest.raises(binding.BiError) as e:
+        binding.bi_rope_config(4, frequencies=[1.0, f])
+    assert e.value.status == binding.BI_ERR_INVALID_ARG
