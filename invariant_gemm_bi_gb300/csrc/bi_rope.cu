@@ -7,9 +7,11 @@
 // n = 10^6 it is off by up to 0.03 rad), and fp64 is slow on this chip.  The
 // frequency is held as a 64-bit binary fraction of a turn, so the integer
 // product phase * n mod 2^64 is the angle modulo one turn, off by at most
-// n 2^-65 turns; its top 32 bits, signed, scale to half turns in [-1, 1) and
-// sincospif needs no further reduction.  What remains is that number's
-// rounding to fp32: under 1.2e-7 rad.
+// n 2^-65 turns; signed, it is rounded to fp32 once and scales to half turns in
+// [-1, 1], so sincospif needs no further reduction.  That rounding is relative:
+// 2^-24 of the reduced angle, under 1.0e-7 rad, and a slow pair's small angle
+// keeps all its digits (the top 32 bits alone would be off by 1.5e-9 rad, to
+// one side, 7e-4 of an angle of 2e-6).  Positions n and -n are mirror images.
 //
 // Work.  A block takes a few tokens and all heads (a part of the heads when
 // there are few tokens).  Its threads compute each sine and cosine of its
@@ -91,7 +93,7 @@ __device__ __forceinline__ void store_one(void* p, int kind, float v) {
 // a cos and a sin of position n's angle for pair i.
 __device__ __forceinline__ void turn(const RopeParams& p, int64_t n, int i, float& c, float& s) {
   const uint64_t t = p.phase[i] * (uint64_t)n;
-  sincospif(__fmul_rn((float)(int32_t)(t >> 32), 4.656612873077393e-10f /* 2^-31 */), &s, &c);
+  sincospif(__fmul_rn(__ll2float_rn((long long)t), 1.0842021724855044e-19f /* 2^-63 */), &s, &c);
   c = __fmul_rn(c, p.magnitude);
   s = __fmul_rn(p.transpose ? -s : s, p.magnitude);
 }
