@@ -491,6 +491,14 @@ def _stream_ptr(stream, device: int) -> int:
     return stream.cuda_stream
 
 
+def _int32(v, name: str) -> int:
+    """v as an int that the library takes whole: ctypes would cut it to its last 32 bits."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name}: {v} is outside the 32-bit integers")
+    return v
+
+
 def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """An output or workspace on like's device, allocated for the stream that the call runs on."""
     if stream is None:
@@ -532,7 +540,8 @@ def bi_paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, page_table
             out = bi_paged_plan_buffers(page_table.shape[0], int(num_tokens), page_table.device)
     _check(lib, "bi_paged_plan", lib.bi_paged_plan(
         _packed(context_lens, "context_lens", dev, _INDEX_DTYPES), _packed(new_lens, "new_lens", dev, _INDEX_DTYPES),
-        _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(free_pages, "free_pages", dev, _INDEX_DTYPES), int(page_size),
+        _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(free_pages, "free_pages", dev, _INDEX_DTYPES),
+        _int32(page_size, "page_size"),
         _packed(out.seq_lens, "seq_lens", dev, _INDEX_DTYPES), _packed(out.token_offsets, "token_offsets", dev, _INDEX_DTYPES),
         _packed(out.positions, "positions", dev, _INDEX_DTYPES), _packed(out.slots, "slots", dev, _INDEX_DTYPES),
         _packed(out.totals, "totals", dev, _INDEX_DTYPES), _stream_ptr(stream, dev)))
@@ -574,16 +583,17 @@ def bi_rope_config(rotary_dim: int, base: float = 10000.0, interleaved: bool = F
     base^(-2i / rotary_dim), scaled by `scaling`, or the rotary_dim / 2 angular
     `frequencies` given (a sequence of floats; base and scaling are not used then)."""
     lib = load()
+    rotary_dim = _int32(rotary_dim, "rotary_dim")
     desc = BiRopeConfig()
     if frequencies is not None:
         f = [float(x) for x in frequencies]
-        if len(f) != int(rotary_dim) // 2:
-            raise ValueError(f"bi_rope_config: expected {int(rotary_dim) // 2} frequencies, got {len(f)}")
+        if len(f) != rotary_dim // 2:
+            raise ValueError(f"bi_rope_config: expected {rotary_dim // 2} frequencies, got {len(f)}")
         arr = (ctypes.c_double * max(len(f), 1))(*f)
-        st = lib.bi_rope_init_frequencies(ctypes.byref(desc), int(rotary_dim), int(bool(interleaved)), arr,
+        st = lib.bi_rope_init_frequencies(ctypes.byref(desc), rotary_dim, int(bool(interleaved)), arr,
                                           float(magnitude))
     else:
-        st = lib.bi_rope_init(ctypes.byref(desc), int(rotary_dim), int(bool(interleaved)), float(base),
+        st = lib.bi_rope_init(ctypes.byref(desc), rotary_dim, int(bool(interleaved)), float(base),
                               ctypes.byref(scaling.desc) if scaling is not None else None, float(magnitude))
     _check(lib, "bi_rope_config", st)
     return RopeConfig(desc)

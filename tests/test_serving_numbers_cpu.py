@@ -6,6 +6,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from invariant_gemm_bi_gb300 import binding, build
 from tests import serving_tight as tight
@@ -55,3 +56,23 @@ def test_frequencies_without_a_fraction_of_a_turn_are_refused(f):
     with pytest.raises(binding.BiError) as e:
         binding.bi_rope_config(4, frequencies=[1.0, f])
     assert e.value.status == binding.BI_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("more", [1 << 32, -(1 << 32), 1 << 40])
+def test_numbers_past_32_bits_are_refused_and_not_cut(more):
+    with pytest.raises(ValueError, match="rotary_dim"):
+        binding.bi_rope_config(more + 64)
+
+    class OnDevice(torch.Tensor):  # passes for a tensor on the current device
+        def get_device(self):
+            return 0
+
+    t = torch.zeros(2, 4, dtype=torch.int32).as_subclass(OnDevice)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 0)
+        m.setattr(binding, "_stream_ptr", lambda stream, device: 0)
+        m.setattr(binding, "_lib", object())  # no entry point is reached
+        i32 = [torch.zeros(n, dtype=torch.int32).as_subclass(OnDevice) for n in (2, 2, 9, 2, 3, 4, 2)]
+        out = binding.PagedPlan(i32[3], i32[4], i32[5], torch.zeros(4, dtype=torch.int64).as_subclass(OnDevice), i32[6])
+        with pytest.raises(ValueError, match="page_size"):
+            binding.bi_paged_plan(i32[0], i32[1], t, i32[2], more + 16, out=out)
