@@ -3,6 +3,7 @@ that the bounds of tests/serving_tight.py reject what they are meant to."""
 from __future__ import annotations
 
 import math
+import types
 
 import numpy as np
 import pytest
@@ -71,7 +72,7 @@ def test_numbers_past_32_bits_are_refused_and_not_cut(more):
     with pytest.MonkeyPatch.context() as m:
         m.setattr(torch.cuda, "current_device", lambda: 0)
         m.setattr(binding, "_stream_ptr", lambda stream, device: 0)
-        m.setattr(binding, "_lib", object())  # no entry point is reached
+        m.setattr(binding, "_lib", types.SimpleNamespace(bi_paged_plan=None))  # no entry point is reached
         i32 = [torch.zeros(n, dtype=torch.int32).as_subclass(OnDevice) for n in (2, 2, 9, 2, 3, 4, 2)]
         out = binding.PagedPlan(i32[3], i32[4], i32[5], torch.zeros(4, dtype=torch.int64).as_subclass(OnDevice), i32[6])
         with pytest.raises(ValueError, match="page_size"):
