@@ -109,3 +109,15 @@ def angles(freq, pos):
             t = turns(f, n, 128)
             out[i, j] = (t - (1 << 128) if t > 1 << 127 else t) / 2.0 ** 127 * math.pi
     return out
+
+
+# -- values that show every key's share ---------------------------------------------------
+
+def marked_values(n, Hkv, D, every):
+    """Values [n, Hkv, D] that are one number in one dimension and 0 in the others: blocks of
+    `every` keys take the dimensions in turn, the number 1 in the first round, 1.5 in the
+    second and so on, so a result is the mass of few blocks and none averages out."""
+    block = np.arange(n) // every
+    v = np.zeros((n, Hkv, D))
+    v[np.arange(n), :, block % D] = (1 + 0.5 * (block // D))[:, None]
+    return v

@@ -102,3 +102,49 @@ def test_small_weights_beside_large_ones_keep_their_share(dt, D, Hq, n, x):
     want, bound = tight.attention(q[0], k, v, 1.0, dt, F32)
     assert np.all(want > 0) and np.all(bound < 0.02 * want)  # a bound that a lost weight would break
     ref.assert_within(o[0], want, bound)
+
+
+# Long caches whose values mark their keys (tests/serving_tight.py): a piece, a group of
+# pieces or a tile that is left out or taken twice moves some results by their own size.
+@pytest.mark.parametrize("D,Hq", [(64, 2), (64, 12), (128, 2), (128, 12), (256, 2)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("n,page", [(700, 16), (2048, 24), (2049, 16), (32769, 128), (65536, 16), (65537, 64), (70001, 24),
+                                    (131071, 64), (131072, 16), (200001, 128)])
+def test_every_key_of_a_long_cache_counts_once(D, Hq, dt, n, page):
+    P, table = _tables([n, 40], page, 10)
+    q = _normal((2, Hq, D), dt, 11)
+    k = _normal((n, 1, D), dt, 12)
+    j = torch.arange(n, device="cuda")
+    at = table[0, j // page].long(), j % page
+    kc = torch.full((P, page, 1, D), float("nan"), dtype=dt, device="cuda")
+    vc = kc.clone()
+    kc[at] = k
+    kc[table[1, :-(-40 // page)].long()] = 1.0
+    vc[table[1, :-(-40 // page)].long()] = 1.0
+    for every in (256, 16):
+        v = tight.marked_values(n, 1, D, every)
+        vc[at] = torch.from_numpy(v).to(dt).cuda()
+        o = bi.bi_paged_attention(q, kc, vc, table, _i32([n, 40]), D ** -0.5)
+        want, bound = tight.attention(q[0], k, v, D ** -0.5, dt, F32)
+        ref.assert_within(o[0], want, bound, f"every {every}")
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 2), (128, 8, 2), (256, 2, 1)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_ragged_batches_of_marked_values(D, Hq, Hkv, dt):
+    # units of many requests on few blocks: the pieces of all lengths at once
+    lens = [5, 9000, 0, 257, 2048, 2049, 40000, 1, 511, 6000, 12345]
+    P, table = _tables(lens, 32, 13)
+    q = _normal((len(lens), Hq, D), dt, 14)
+    kc, vc = _normal((P, 32, Hkv, D), dt, 15), torch.full((P, 32, Hkv, D), float("inf"), dtype=dt, device="cuda")
+    values = []
+    for b, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        values.append(tight.marked_values(n, Hkv, D, 64))
+        vc[table[b, j // 32].long(), j % 32] = torch.from_numpy(values[b]).to(dt).cuda()
+    o = bi.bi_paged_attention(q, kc, vc, table, _i32(lens), D ** -0.5)
+    for b, n in enumerate(lens):
+        if n:
+            j = torch.arange(n, device="cuda")
+            want, bound = tight.attention(q[b], kc[table[b, j // 32].long(), j % 32], values[b], D ** -0.5, dt, F32)
+            ref.assert_within(o[b], want, bound, f"request {b}")

@@ -77,3 +77,28 @@ def test_numbers_past_32_bits_are_refused_and_not_cut(more):
         out = binding.PagedPlan(i32[3], i32[4], i32[5], torch.zeros(4, dtype=torch.int64).as_subclass(OnDevice), i32[6])
         with pytest.raises(ValueError, match="page_size"):
             binding.bi_paged_plan(i32[0], i32[1], t, i32[2], more + 16, out=out)
+
+
+@pytest.mark.parametrize("D,group", [(64, 1), (128, 12), (256, 1)])
+@pytest.mark.parametrize("n", [2049, 65537, 131071])
+@pytest.mark.parametrize("dtype,every", [(torch.bfloat16, 256), (torch.float16, 256), (torch.bfloat16, 16)])
+def test_the_attention_bound_rejects_work_left_out_or_done_twice(D, group, n, dtype, every):
+    rng = np.random.default_rng(n + D)
+    q, k = rng.standard_normal((1, D)), rng.standard_normal((n, 1, D))
+    v = tight.marked_values(n, 1, D, every)
+    ref, bound = tight.attention(np.repeat(q, group, 0), k, v, D ** -0.5, dtype, torch.float32)
+    ref, bound = ref[0], bound[0]
+    s = D ** -0.5 * (k[:, 0] @ q[0])
+    p = np.exp(s - s.max())
+    piece = tight.split_len(n)
+    for at, size in ((0, piece), (n // piece // 2 * piece, piece), (n - n % piece, piece),  # first, middle and last piece
+                     (0, min(16, n // piece // 2) * piece), (piece, 16), (n // 32 * 16, 16)):  # a join's group; a tile
+        there = np.ones(n)
+        for weight in (0.0, 2.0):
+            there[at:at + size] = weight
+            w = p * there
+            for total in (w.sum(), p.sum()):  # left out of both sums, or of the values' alone
+                off = np.abs((w @ v[:, 0]) / total - ref) > bound
+                assert off.any(), (at, size, weight)
+                if size == piece and every == 256:  # every dimension that the keys are marked in
+                    assert off[np.unique(np.arange(at, min(n, at + size)) // every % D)].all(), (at, size, weight)
