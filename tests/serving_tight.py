@@ -121,3 +121,48 @@ def marked_values(n, Hkv, D, every):
     v = np.zeros((n, Hkv, D))
     v[np.arange(n), :, block % D] = (1 + 0.5 * (block // D))[:, None]
     return v
+
+
+# -- token log probabilities -----------------------------------------------------------------
+
+def logprobs_sum_error(N, dtype):
+    """Relative error of a row's sum of exponentials, from the order that the header states:
+    16 adds of a chunk and one of its halves (2^-24 each); a join of every slice of a group, of
+    every group, of 5 rounds of lanes and 3 of warps, two roundings and one factor 2^x (2^-22)
+    each; and 2^x of the element itself."""
+    slices = -(-N // (4096 if dtype == torch.float32 else 8192))
+    per_group = -(-slices // 8)
+    joins = per_group + -(-slices // per_group) + 8
+    return (17 + 2 * joins) * 2.0 ** -24 + (joins + 1) * 2.0 ** -22
+
+
+def logprobs_bounds(x, lp, dtype):
+    """Bounds of (log probabilities lp, entropies) of ordinary rows x [R, N] in 64 bits: the argument
+    of 2^x is one rounding of x log2 e - m', log2 e itself good to 2^-26: 2^-22 |z| in the exponential."""
+    z = x - x.max(-1, keepdims=True)
+    e = np.exp(z)
+    S = e.sum(-1)
+    with np.errstate(invalid="ignore"):
+        spread = np.where(e > 0, -e * z, 0.0).sum(-1) / S
+        square = np.where(e > 0, e * z * z, 0.0).sum(-1) / S
+    err = logprobs_sum_error(x.shape[1], dtype)
+    log_sum = err + 2.0 ** -22 * spread + 2.0 ** -22 * np.abs(np.log(S))
+    at = (...,) + (None,) * (lp.ndim - 1)
+    # the differences' and the result's roundings
+    lp_bound = log_sum[at] + 2.0 ** -23 * np.abs(np.where(np.isfinite(lp), lp, 0.0)) + 2.0 ** -23 * np.log(S)[at]
+    # H is a sum of terms of one sign: its own sum's error and S's, t's rounding, the division
+    entropy = log_sum + (2 * err + 2.0 ** -21) * spread + 2.0 ** -22 * square + 2.0 ** -23 * (spread + np.log(S))
+    return lp_bound, entropy
+
+
+def marked_rows(N, dtype):
+    """Index sets on whose elements a row may have all its weight: the last and first ones, and
+    those at and around the boundaries of units, warps, stages, slices and groups."""
+    E = 4 if dtype == torch.float32 else 8
+    slices = -(-N // (1024 * E))
+    sets = [range(N - k, N) for k in range(1, 17)] + [range(k) for k in (1, 2, 3, 5, 7, 8, 9, 16)]
+    for b in (E, 31 * E, 32 * E, 33 * E, 255 * E, 256 * E, 512 * E, 768 * E, 1024 * E, 1024 * E * -(-slices // 8),
+              1024 * E * (slices - 1), N // E * E, N // (256 * E) * 256 * E):
+        sets += [range(b - 1, b + 1), range(b, b + E), range(b - E, b), range(b - 3, b + 13)]
+    sets = [[j for j in s if 0 <= j < N] for s in sets]
+    return [s for s in sets if s]

@@ -102,3 +102,17 @@ def test_the_attention_bound_rejects_work_left_out_or_done_twice(D, group, n, dt
                 assert off.any(), (at, size, weight)
                 if size == piece and every == 256:  # every dimension that the keys are marked in
                     assert off[np.unique(np.arange(at, min(n, at + size)) // every % D)].all(), (at, size, weight)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [50257, 128256, 128257, 300001])
+def test_the_log_sum_bound_rejects_a_lost_unit(dtype, N):
+    # 16 elements of an ordinary row, a 16-byte unit of a row without spread
+    x = np.random.default_rng(N).standard_normal((4, N)) * np.array([[0.0], [0.1], [1.0], [3.0]])
+    lp = x[:, :1] - np.log(np.exp(x).sum(-1, keepdims=True))
+    bound = tight.logprobs_bounds(x, lp, dtype)[0][:, 0]
+    for gone in (slice(N - 16, N), slice(0, 16), slice(4096, 4112)):
+        rest = np.exp(x)
+        rest[:, gone] = 0.0
+        off = np.abs(np.log(rest.sum(-1)) - np.log(np.exp(x).sum(-1)))
+        assert (off > bound)[:3].all() and (off > 0.3 * bound).all(), (off, bound)
