@@ -43,7 +43,9 @@
 // that do are ranked by counting.  (A thread reading its own chunks again, one
 // latency after the other: 19 us in place of 7 for the 8 rows.)  Rows with more
 // than 512 such elements (ties) and rows with NaNs extract one element a round
-// instead.
+// instead.  Where fewer than K groups have an allowed token, tau is -inf and
+// the whole row is read again, an element a thread: right, and slow (10 tokens
+// allowed, K = 20: 8 bf16 rows 38 us in place of 7.5, 2048 rows 334 of 95).
 #include "bi_rows.cuh"
 #include "bi_serve.h"
 

@@ -20,7 +20,7 @@
 // mma.sync m16n8k16 with the long side on M: S^T = K Q^T (16 keys x 8 heads)
 // and O^T += V^T P^T (16 dimensions x 8 heads).  With one token a head there
 // are at most G rows to a product, which a 128-row tcgen05 tile would waste
-// 15/16 of, and the tensor pipe is an eighth busy as it is.
+// 15/16 of, and the tensor pipe is a sixth busy as it is.
 //
 // Feeding it.  Each warp owns a ring of three shared-memory slots, keys and
 // values of a tile taking one each, filled by 16-byte asynchronous copies: two
@@ -40,7 +40,8 @@
 // into registers, 16 warps an SM, 250 us (each unit's first loads exposed);
 // shared-memory rings across units, 16-key tiles, 204 us (bound by issue, 512
 // instructions a tile and warp); 32-key tiles with transposing reads 164 us,
-// longer pieces 160 us, 5.97 TB/s, now near the memory's rate.
+// longer pieces 160 us, 5.97 TB/s, near the memory's rate (161 with p in three
+// pieces, below).
 //
 // Arithmetic, per query head: t = RN(s c) with c = RN(scale log2 e); a running
 // maximum m per warp over its tiles; p = 2^(t - m) (the SFU's approximation);
@@ -757,10 +758,11 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
   constexpr int kSlot = 24 + (D == 256 ? 8 + F16 : (D == 128 ? 4 : 0) + 2 * F16 + NT - 1);
   p.head_tiles = (p.group + 8 * NT - 1) / (8 * NT);
   const int64_t most = (int64_t)p.B * p.max_splits * p.Hkv * p.head_tiles;
-  // Short caches whose units all run at once: a CTA a unit and a cluster a
-  // request's head tile, joined in place -- one launch, and no search for the
-  // units (one request of 1021 keys: 6.9 us, 10.0 the other way).  The bits are
-  // the same.
+  // Tables of at most 4096 keys whose units all run at once: a CTA a unit and a
+  // cluster a request's head tile, joined in place -- one launch, and no search
+  // for the units (one request of 1021 keys 7.6 us; with a table for 131072, and
+  // so the other way, 10.7).  The host knows the table's width and not the
+  // lengths.  The bits are the same.
   const bool one = p.max_splits <= kMaxCluster && most <= (int64_t)num_sms * Sh::kCtas;
   *joined = p.max_splits == 1 || one;
   if (one) {

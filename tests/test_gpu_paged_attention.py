@@ -148,3 +148,46 @@ def test_ragged_batches_of_marked_values(D, Hq, Hkv, dt):
             j = torch.arange(n, device="cuda")
             want, bound = tight.attention(q[b], kc[table[b, j // 32].long(), j % 32], values[b], D ** -0.5, dt, F32)
             ref.assert_within(o[b], want, bound, f"request {b}")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("D,n", [(64, 200), (128, 3000), (256, 700)])
+def test_infinities_in_live_rows(dt, D, n):
+    P, table = _tables([n], 16, 16)
+    kc, vc = _normal((P, 16, 2, D), dt, 17), _normal((P, 16, 2, D), dt, 18)
+    q = _normal((1, 6, D), dt, 19)
+    q[..., 7] = 1.0
+    j = torch.arange(n, device="cuda")
+    pages = table[0, j // 16].long(), j % 16
+
+    def call():
+        return bi.bi_paged_attention(q, kc, vc, table, _i32([n]), D ** -0.5)
+
+    whole = call()
+    # an infinite value: not finite in its dimension for the heads that read it, the rest as it
+    # was.  (Its weight is a sum of 16-bit numbers p = hi + lo ...: hi is rounded to nearest, so lo
+    # may be positive, which gives an infinity, or negative or zero, inf - inf and 0 inf.)
+    kept = vc.clone()
+    vc[table[0, n // 32].long(), 5, 1, 9] = float("inf")
+    o = call()
+    assert not o[0, 3:, 9].isfinite().any() and bits_equal(o[0, :3], whole[0, :3])
+    other = torch.arange(D, device="cuda") != 9
+    assert bits_equal(o[0, 3:][:, other].contiguous(), whole[0, 3:][:, other].contiguous())
+    vc[table[0, n // 32].long(), 5, 1, 9] = float("nan")
+    o = call()
+    assert o[0, 3:, 9].isnan().all() and bits_equal(o[0, 3:][:, other].contiguous(), whole[0, 3:][:, other].contiguous())
+    vc.copy_(kept)
+    # keys whose score is -inf weigh nothing
+    out = torch.zeros(n, dtype=torch.bool, device="cuda")
+    out[::3] = True
+    kc[pages[0][out], pages[1][out], :, 7] = float("-inf")
+    want, bound = tight.attention(q[0], kc[pages][~out], vc[pages][~out], D ** -0.5, dt, F32)
+    _, more = tight.attention(q[0], _normal((n, 2, D), dt, 17), vc[pages], D ** -0.5, dt, F32)  # n keys' roundings
+    ref.assert_within(call()[0], want, bound + more)
+    kc[pages[0], pages[1], :, 7] = float("-inf")
+    assert not call().any()  # all of them: as without keys
+    # a score of +inf: NaN for the head it belongs to
+    kc.copy_(_normal((P, 16, 2, D), dt, 17))
+    kc[table[0, 0].long(), 3, 0, 7] = float("inf")
+    o = call()
+    assert o[0, :3].isnan().all() and bits_equal(o[0, 3:], whole[0, 3:])
