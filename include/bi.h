@@ -522,10 +522,9 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  *
  * Order: a request of n keys is cut into pieces of s keys, s = 256 up to n =
  * 2048, beyond that 512 * 2^k, k the least with n <= 128 s -- a rule on its own
- * length.  In a piece, warp w of W
- * takes the tiles w, w + W, ... in order with a running maximum (tiles of 32
- * keys, 16 at D = 256; W = 4, or 8 at D = 256 and, for more than 8 query heads
- * a key-value head, at D = 128); p = 2^(t - m), t = RN(score * RN(scale
+ * length.  In a piece, warp w of W takes the tiles w, w + W, ... in order with a
+ * running maximum (tiles of 32 keys, 16 at D = 256; W = 4, or 8 at D = 256 and,
+ * for more than 8 query heads a key-value head, at D = 128); p = 2^(t - m), t = RN(score * RN(scale
  * log2 e)).  Warp w + W/2 is joined into warp w, then warps 1, 2, ... into
  * warp 0, groups of 16 pieces in piece order, then the groups in order, all in
  * fp32.  Sums are of the unrounded p; the product with v takes p as the
@@ -538,8 +537,8 @@ bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* position
  * request: with L = W * page_size, ceil(L / 256) up to L = 2048, beyond that
  * ceil(L / 512), but at least 8 and at most 128.  Scratch, as in bi_attention_ws.
  * What the table can name decides this size and the form of the launch, not the
- * lengths, which the host does not know: one launch while L <= 4096 and the
- * B * n * Hkv * ceil(Hq / Hkv / 8 or 16) units run at once, else two.  A table kept for 131072 keys makes
+ * lengths, which the host does not know: one launch while L <= 4096 and all
+ * pieces of the batch run at once, else two.  A table kept for 131072 keys makes
  * one request of 1021 keys take 10.7 us in place of 7.6 on the device, and asks
  * for 2.1 MB of workspace for it (256 requests of 32 heads of 128: 545 MB).
  */
