@@ -66,7 +66,8 @@ typedef enum {
   BI_F16 = 1,
   BI_F32 = 2,
   BI_I32 = 3, /* index operands of the serving operations only */
-  BI_I64 = 4
+  BI_I64 = 4,
+  BI_E4M3 = 5 /* 8-bit operands (4 exponent, 3 mantissa bits) of the operations that say so */
 } bi_dtype;
 
 typedef enum {
@@ -578,11 +579,131 @@ bi_status bi_token_logprobs(const bi_tensor* logits, const bi_tensor* tokens,
                             const bi_tensor* top_logprobs, const bi_tensor* top_ids,
                             bi_stream stream);
 
+/* -------------------------------------------------------------------------
+ * 8-bit operands.  e4m3 numbers (4 exponent, 3 mantissa bits, at most 448, one
+ * NaN) with fp32 scales; a number stands for itself times its scale.  What is
+ * quantised here has scales 2^e, e the least integer from -126 on with
+ * 448 * 2^e >= the block's size (1 for a block of zeros), and numbers
+ * RN_e4m3(x / 2^e): scaling is exact, each element is rounded once, ties to
+ * even.  A block whose size is a NaN or infinite has a NaN for its scale and
+ * NaNs for its elements.  Operands with scales from elsewhere may have any fp32
+ * scales.
+ */
+
+/*
+ * Quantisation of x [M,K] (bf16, fp16 or fp32, unit stride on K) in blocks of
+ * block_rows x 128, block_rows 1 (activations) or 128 (weights); a block's size
+ * is its largest magnitude.  q [M,K] e4m3, unit stride on K; scales
+ * [ceil(M/block_rows), ceil(K/128)] fp32, any strides.  A row's blocks of 1 x
+ * 128 depend on that row alone.  Rows of x on 16 bytes and of q on 8 are read
+ * and written wide, others by element, with the same bits.
+ */
+bi_status bi_quantize_blocks(const bi_tensor* x, int32_t block_rows, const bi_tensor* q,
+                             const bi_tensor* scales, bi_stream stream);
+
+/*
+ * c[m,n] = sum_kb a_scales[m,kb] b_scales[kb,nb] sum_{k in block kb} a[m,k] b[k,n]  (+ bias[n]),
+ * kb = k / 128, nb = n / 128.
+ *   a [M,K] e4m3, unit stride on K; b [K,N] e4m3, unit stride on K (the weight
+ *   as [N,K], transposed); bases and the other strides multiples of 16 bytes.
+ *   a_scales [M, ceil(K/128)], b_scales [ceil(K/128), ceil(N/128)] fp32, any
+ *   strides (bi_quantize_blocks's of the weight, transposed).  bias [N] bf16,
+ *   fp16 or fp32, any stride, or NULL.  c [M,N] fp32, bf16 or fp16, unit stride
+ *   on N.  M, N, K <= 2^30.
+ *
+ * Order: D = the block's products, four tensor-core steps of 32 in ascending
+ * order; acc = fma(D, RN(a_scale b_scale), acc) in fp32, blocks in ascending
+ * order, from zero; then bias and one rounding, as bi_addmm.  Tiles are 64, 128
+ * or 256 columns wide by the number of tiles; an element's bits do not depend
+ * on it, so row m depends on row m of a and a_scales alone.
+ */
+bi_status bi_mm_blockscaled(const bi_tensor* a, const bi_tensor* a_scales, const bi_tensor* b,
+                            const bi_tensor* b_scales, const bi_tensor* bias, const bi_tensor* c,
+                            bi_stream stream);
+
+/*
+ * bi_paged_store into caches in 8 bits: k_cache, v_cache [P,page_size,Hkv,D]
+ * e4m3 (unit strides on D), k_scales, v_scales [P,page_size,Hkv] fp32 (any
+ * strides), one scale a token and head.  The size of a value head is its
+ * largest magnitude; of a key head the largest of RN(RN(|x1| + |x2|) |a|) over
+ * its rotated pairs, before they are turned, and of |x| over its other elements:
+ * turned elements do not exceed it, and a key's scale does not depend on its
+ * position.  (It is at most twice the largest element: one binade of the
+ * range's small end.)  Turned keys are rounded once, from fp32 to e4m3.  All
+ * else is as in bi_paged_store; rows of tokens that are not stored keep their
+ * scales too.
+ */
+bi_status bi_paged_store_quantized(const bi_rope_config* config, const bi_tensor* positions,
+                                   const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
+                                   const bi_tensor* k, const bi_tensor* v, const bi_tensor* k_cache,
+                                   const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                   const bi_tensor* v_scales, bi_stream stream);
+
+/*
+ * Rows of caches in 8 bits read back: k[t] = k_cache[slots[t]] * k_scales, v
+ * likewise, one rounding to the outputs' type; slots [T] int64 in any order,
+ * the same one as often as wanted; a negative slot gives a row of zeros, one
+ * past the cache too, and is reported.  k, v [T,Hkv,D] of one type, bf16, fp16
+ * or fp32, unit stride on D, D <= 1024.
+ */
+bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_tensor* k_cache,
+                                  const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                  const bi_tensor* v_scales, const bi_tensor* k, const bi_tensor* v,
+                                  bi_stream stream);
+
+/*
+ * bi_paged_attention over caches in 8 bits, their scales applied:
+ *   o[b,h,:] = sum_j softmax_j(scale * k_scale_j q[b,h,:] . k_j) v_scale_j v_j.
+ * q bf16 or fp16 whatever the caches; sizes, types of o, page tables, lengths,
+ * empty requests and the workspace are bi_paged_attention's.  A head of q that
+ * holds a NaN or an infinity gives NaNs.
+ *
+ * Order: as bi_paged_attention with W = 4; t = RN(RN(s k_scale) f), s the
+ * fp32 sum of products of fp16 numbers, q brought to fp16 by a power of two of
+ * its own for each head (exact down to 2^-27 of its largest element) and f =
+ * scale log2 e with that power taken off.  A key's weight in o is v_scale
+ * 2^(t - m'), m' the warp's largest t + log2 |v_scale| so far (whole part), and
+ * goes into the product as two fp16 of 2^14 times it; sums are of 2^(t - m).
+ */
+bi_status bi_paged_attention_quantized(const bi_tensor* q, const bi_tensor* k_cache,
+                                       const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                       const bi_tensor* v_scales, const bi_tensor* page_table,
+                                       const bi_tensor* seq_lens, float scale, const bi_tensor* o,
+                                       void* workspace, int64_t workspace_bytes, bi_stream stream);
+
+/*
+ * One token of each row of logits [R,N] (bf16, fp16 or fp32, unit stride on N,
+ * N <= 327680), drawn by uniforms[r] of [0, 1).  With z = x / temperature:
+ *   top_k   keeps the k largest logits, the lower index first among equals
+ *           (k <= 0, or k >= N: all);
+ *   top_p   of those the shortest prefix, largest first, whose sum of e^z is at
+ *           least top_p times all of it (the largest at least; top_p >= 1: all);
+ *   min_p   the tokens with e^(z - max z) >= min_p (<= 0: all; above 1 as 1).
+ * The token is the first in index order at which the running sum of the kept
+ * e^z exceeds uniforms[r] times their sum.  A temperature below 2^-20 (0 among
+ * them) takes the largest logit, the lowest index among equals, whatever the
+ * filters are.
+ *   temperature, top_p, min_p fp32 [R], top_k int32 [R], each row its own; NULL:
+ *   1, 1, 0, 0.  uniforms fp32 [R]; tokens int32 or int64 [R]; all contiguous.
+ * A row that holds a NaN or +inf, or nothing but -inf, gets token -1.  So does
+ * one whose uniform is outside [0, 1), whose temperature is outside [0, 2^20]
+ * or which has a NaN for a setting; that is reported.
+ *
+ * Sums are of 64-bit integers, e^(z - max z) to 2^-33 of itself in units of
+ * 2^-43 to 2^-46 of the largest by N (what is below half a unit has weight 0):
+ * exact, the same in any order, and on the side of a border that the real sums
+ * are on unless those are within about 2^-32 of it.  A row's token depends on
+ * that row and its settings alone.
+ */
+bi_status bi_sample_tokens(const bi_tensor* logits, const bi_tensor* uniforms, const bi_tensor* temperature,
+                           const bi_tensor* top_k, const bi_tensor* top_p, const bi_tensor* min_p,
+                           const bi_tensor* tokens, bi_stream stream);
+
 /*
  * Synchronises `stream`, then returns and clears the device-side status word
  * of the current device: BI_OK, BI_ERR_TIMEOUT when a kernel's bounded wait
  * ran out since the last call, or BI_ERR_INVALID_ARG when a serving operation
- * met a slot, page or length that does not exist (detail in
+ * met a slot, page or length that does not exist or a setting that is none (detail in
  * bi_last_error_message()).
  */
 bi_status bi_device_status(bi_stream stream);

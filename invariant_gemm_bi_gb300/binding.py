@@ -34,11 +34,14 @@ EXPORTED = ("bi_mm", "bi_addmm", "bi_bmm", "bi_conv2d_patch", "bi_softmax_lastdi
             "bi_conv_packed_weight_bytes", "bi_conv_pack_weight", "bi_conv2d_patch_packed",
             "bi_paged_plan", "bi_rope_init", "bi_rope_init_frequencies", "bi_rope", "bi_paged_store",
             "bi_paged_attention", "bi_paged_attention_workspace_bytes", "bi_token_logprobs",
+            "bi_quantize_blocks", "bi_mm_blockscaled", "bi_paged_store_quantized", "bi_paged_load_quantized",
+            "bi_paged_attention_quantized", "bi_sample_tokens",
             "bi_device_status", "bi_debug_expire_wait", "bi_status_string",
             "bi_last_error_message", "bi_abi_version")
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _INDEX_DTYPES = {torch.int32: 3, torch.int64: 4}  # index operands of the serving operations
+_E4M3_DTYPES = {torch.float8_e4m3fn: 5}  # 8-bit operands
 
 
 class BiTensor(ctypes.Structure):
@@ -155,6 +158,12 @@ def load(path: str | None = None):
                 "bi_paged_attention": ([vp] * 5 + [ctypes.c_float, vp, vp, ctypes.c_int64, vp], st),
                 "bi_paged_attention_workspace_bytes": ([ctypes.c_int64] * 4, ctypes.c_int64),
                 "bi_token_logprobs": ([vp] * 7, st),
+                "bi_quantize_blocks": ([vp, ctypes.c_int32, vp, vp, vp], st),
+                "bi_mm_blockscaled": ([vp] * 7, st),
+                "bi_paged_store_quantized": ([vp] * 12, st),
+                "bi_paged_load_quantized": ([vp] * 8, st),
+                "bi_paged_attention_quantized": ([vp] * 7 + [ctypes.c_float, vp, vp, ctypes.c_int64, vp], st),
+                "bi_sample_tokens": ([vp] * 8, st),
                 "bi_device_status": ([ctypes.c_void_p], st),
                 "bi_debug_expire_wait": ([ctypes.c_uint64, ctypes.c_void_p], st),
                 "bi_status_string": ([st], ctypes.c_char_p),
@@ -640,6 +649,22 @@ def bi_paged_attention_workspace_bytes(B: int, Hq: int, D: int, max_len: int) ->
     return int(load().bi_paged_attention_workspace_bytes(int(B), int(Hq), int(D), int(max_len)))
 
 
+def _attention_workspace(lib, q, k_cache, page_table, workspace, dev, stream):
+    """(address, bytes, tensor) of the workspace given, or of one allocated when it is needed."""
+    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and page_table.dim() == 2:
+        need = lib.bi_paged_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2],
+                                                      page_table.shape[1] * k_cache.shape[1])
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, q, stream)
+    if workspace is None:
+        return 0, 0, None
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace: expected a tensor on cuda:{dev}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def bi_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                        seq_lens: torch.Tensor, scale: float, out: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
@@ -653,19 +678,7 @@ def bi_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     dev = _call_device(q, "q")
     if out is None:
         out = _empty(q.shape, out_dtype, q, stream)
-    ws = 0
-    wbytes = 0
-    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and page_table.dim() == 2:
-        need = lib.bi_paged_attention_workspace_bytes(q.shape[0], q.shape[1], q.shape[2],
-                                                      page_table.shape[1] * k_cache.shape[1])
-        if need > 0:
-            workspace = _empty((need,), torch.uint8, q, stream)
-    if workspace is not None:
-        if workspace.get_device() != dev:
-            raise ValueError(f"workspace: expected a tensor on cuda:{dev}, got {workspace.device}")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous tensor")
-        ws, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws, wbytes, workspace = _attention_workspace(lib, q, k_cache, page_table, workspace, dev, stream)
     _check(lib, "bi_paged_attention", lib.bi_paged_attention(
         _packed(q, "q", dev), _packed(k_cache, "k_cache", dev), _packed(v_cache, "v_cache", dev),
         _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(seq_lens, "seq_lens", dev, _INDEX_DTYPES), float(scale),
@@ -701,6 +714,140 @@ def bi_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, 
         _packed(logits, "logits", dev), _packed(tokens, "tokens", dev, _INDEX_DTYPES), _packed(out.logprobs, "logprobs", dev),
         _packed(out.entropy, "entropy", dev), _packed(out.top_logprobs, "top_logprobs", dev),
         _packed(out.top_ids, "top_ids", dev, _INDEX_DTYPES), _stream_ptr(stream, dev)))
+    return out
+
+
+# -- 8-bit operands, and tokens drawn from logits ---------------------------------
+
+class QuantizedBlocks(NamedTuple):
+    """What bi_quantize_blocks gives: numbers and the scales of their blocks."""
+    values: torch.Tensor  # [M, K] float8_e4m3fn, rows on 16 bytes
+    scales: torch.Tensor  # [ceil(M / block_rows), ceil(K / 128)] fp32
+
+
+def bi_quantize_blocks(x: torch.Tensor, block_rows: int = 1, out: QuantizedBlocks | None = None,
+                       stream=None) -> QuantizedBlocks:
+    """x [M, K] in e4m3 with a scale for each block of block_rows x 128: block_rows 1 for
+    activations, 128 for a weight [N, K].  Without `out`, rows are laid out on 16
+    bytes, as bi_mm_blockscaled takes them, whatever K is."""
+    lib = _lib or load()
+    dev = _call_device(x, "x")
+    block_rows = _int32(block_rows, "block_rows")
+    if out is None:
+        if x.dim() != 2:
+            raise ValueError(f"x: expected rank 2, got {x.dim()}")
+        if block_rows < 1:
+            raise ValueError("block_rows: must be 1 or 128")
+        M, K = x.shape
+        out = QuantizedBlocks(_empty((M, (K + 15) // 16 * 16), torch.float8_e4m3fn, x, stream)[:, :K],
+                              _empty(((M + block_rows - 1) // block_rows, (K + 127) // 128), torch.float32, x, stream))
+    _check(lib, "bi_quantize_blocks", lib.bi_quantize_blocks(
+        _packed(x, "x", dev), block_rows, _packed(out.values, "values", dev, _E4M3_DTYPES),
+        _packed(out.scales, "scales", dev), _stream_ptr(stream, dev)))
+    return out
+
+
+def bi_mm_blockscaled(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                      bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """a [M, K] times b [K, N] (a weight [N, K], transposed), both e4m3 with scales of
+    blocks of 1 x 128 and 128 x 128: a_scales [M, ceil(K / 128)], b_scales
+    [ceil(K / 128), ceil(N / 128)] (the weight's, transposed); plus bias [N]."""
+    lib = _lib or load()
+    dev = _call_device(a, "a")
+    if out is None:
+        if a.dim() != 2 or b.dim() != 2:
+            raise ValueError("bi_mm_blockscaled: a and b must have rank 2")
+        out = _empty((a.shape[0], b.shape[1]), out_dtype, a, stream)
+    _check(lib, "bi_mm_blockscaled", lib.bi_mm_blockscaled(
+        _packed(a, "a", dev, _E4M3_DTYPES), _packed(a_scales, "a_scales", dev), _packed(b, "b", dev, _E4M3_DTYPES),
+        _packed(b_scales, "b_scales", dev), _packed(bias, "bias", dev), _packed(out, "out", dev),
+        _stream_ptr(stream, dev)))
+    return out
+
+
+def bi_paged_store_quantized(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                             k_scales: torch.Tensor, v_cache: torch.Tensor, v_scales: torch.Tensor,
+                             q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                             config: RopeConfig | None = None, q_out: torch.Tensor | None = None,
+                             q_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor | None:
+    """bi_paged_store into caches [P, page_size, Hkv, D] of float8_e4m3fn with scales
+    [P, page_size, Hkv], one a token and head.  q_out is allocated in q_dtype, or in
+    q's dtype, when not given."""
+    lib = _lib or load()
+    dev = _call_device(k, "k")
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, q_dtype or q.dtype, q, stream)
+    _check(lib, "bi_paged_store_quantized", lib.bi_paged_store_quantized(
+        config._ref if config is not None else None, _packed(positions, "positions", dev, _INDEX_DTYPES),
+        _packed(slots, "slots", dev, _INDEX_DTYPES), _packed(q, "q", dev), _packed(q_out, "q_out", dev),
+        _packed(k, "k", dev), _packed(v, "v", dev), _packed(k_cache, "k_cache", dev, _E4M3_DTYPES),
+        _packed(k_scales, "k_scales", dev), _packed(v_cache, "v_cache", dev, _E4M3_DTYPES),
+        _packed(v_scales, "v_scales", dev), _stream_ptr(stream, dev)))
+    return q_out
+
+
+class CacheRows(NamedTuple):
+    """What bi_paged_load_quantized gives, [T, Hkv, D] each."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+
+def bi_paged_load_quantized(slots: torch.Tensor, k_cache: torch.Tensor, k_scales: torch.Tensor,
+                            v_cache: torch.Tensor, v_scales: torch.Tensor, out: CacheRows | None = None,
+                            out_dtype: torch.dtype = torch.bfloat16, stream=None) -> CacheRows:
+    """The keys and values at slots [T] of caches in 8 bits as numbers (zeros for a
+    negative slot)."""
+    lib = _lib or load()
+    dev = _call_device(k_cache, "k_cache")
+    if out is None:
+        if slots.dim() != 1 or k_cache.dim() != 4:
+            raise ValueError("bi_paged_load_quantized: slots must have rank 1, the caches rank 4")
+        shape = (slots.shape[0], k_cache.shape[2], k_cache.shape[3])
+        out = CacheRows(_empty(shape, out_dtype, k_cache, stream), _empty(shape, out_dtype, k_cache, stream))
+    _check(lib, "bi_paged_load_quantized", lib.bi_paged_load_quantized(
+        _packed(slots, "slots", dev, _INDEX_DTYPES), _packed(k_cache, "k_cache", dev, _E4M3_DTYPES),
+        _packed(k_scales, "k_scales", dev), _packed(v_cache, "v_cache", dev, _E4M3_DTYPES),
+        _packed(v_scales, "v_scales", dev), _packed(out.k, "k", dev), _packed(out.v, "v", dev),
+        _stream_ptr(stream, dev)))
+    return out
+
+
+def bi_paged_attention_quantized(q: torch.Tensor, k_cache: torch.Tensor, k_scales: torch.Tensor,
+                                 v_cache: torch.Tensor, v_scales: torch.Tensor, page_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, scale: float, out: torch.Tensor | None = None,
+                                 out_dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+                                 stream=None) -> torch.Tensor:
+    """bi_paged_attention over caches [P, page_size, Hkv, D] of float8_e4m3fn with scales
+    [P, page_size, Hkv]; q [B, Hq, D] bf16 or fp16.  The workspace is
+    bi_paged_attention's."""
+    lib = _lib or load()
+    dev = _call_device(q, "q")
+    if out is None:
+        out = _empty(q.shape, out_dtype, q, stream)
+    ws, wbytes, workspace = _attention_workspace(lib, q, k_cache, page_table, workspace, dev, stream)
+    _check(lib, "bi_paged_attention_quantized", lib.bi_paged_attention_quantized(
+        _packed(q, "q", dev), _packed(k_cache, "k_cache", dev, _E4M3_DTYPES), _packed(k_scales, "k_scales", dev),
+        _packed(v_cache, "v_cache", dev, _E4M3_DTYPES), _packed(v_scales, "v_scales", dev),
+        _packed(page_table, "page_table", dev, _INDEX_DTYPES), _packed(seq_lens, "seq_lens", dev, _INDEX_DTYPES),
+        float(scale), _packed(out, "out", dev), ws or None, wbytes, _stream_ptr(stream, dev)))
+    return out
+
+
+def bi_sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, temperature: torch.Tensor | None = None,
+                     top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                     min_p: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One token of each row of logits [R, N], drawn by uniforms [R] of [0, 1): settings
+    [R] of each row (fp32, top_k int32), or None for temperature 1, all tokens, 1 and 0.
+    Returns [R] int64 (or out, int32 or int64); -1 where a row has no distribution."""
+    lib = _lib or load()
+    dev = _call_device(logits, "logits")
+    if out is None:
+        out = _empty((logits.shape[0],), torch.int64, logits, stream)
+    _check(lib, "bi_sample_tokens", lib.bi_sample_tokens(
+        _packed(logits, "logits", dev), _packed(uniforms, "uniforms", dev), _packed(temperature, "temperature", dev),
+        _packed(top_k, "top_k", dev, _INDEX_DTYPES), _packed(top_p, "top_p", dev), _packed(min_p, "min_p", dev),
+        _packed(out, "out", dev, _INDEX_DTYPES), _stream_ptr(stream, dev)))
     return out
 
 

@@ -21,7 +21,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompil
               "--expt-relaxed-constexpr"]
 SOURCES = ["bi_abi.cu", "bi_gemm.cu", "bi_conv.cu", "bi_patch.cu", "bi_softmax.cu", "bi_rows.cu", "bi_rows_rms.cu",
            "bi_rows_lsm.cu", "bi_attn.cu", "bi_plan.cu", "bi_rope.cu", "bi_paged_attn.cu", "bi_logprobs.cu",
-           "bi_serve_abi.cu"]
+           "bi_serve_abi.cu", "bi_quant.cu", "bi_mm8.cu", "bi_cache8.cu", "bi_sample.cu", "bi_quant_abi.cu"]
 
 
 def _nvcc() -> str:

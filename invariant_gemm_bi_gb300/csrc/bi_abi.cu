@@ -42,8 +42,8 @@ struct DevState {
   std::string why;
   int num_sms = 0;
   unsigned int* status_word = nullptr;
-  bool smem_set[96] = {};
-  int pairs[24] = {};  // resident 2-CTA clusters per kernel slot (0: not yet asked)
+  bool smem_set[160] = {};
+  int pairs[160] = {};  // resident 2-CTA clusters per kernel slot (0: not yet asked)
   void* scratch = nullptr;  // device address of g_bi_noalloc_scratch (0: not yet asked)
 };
 DevState g_dev[kMaxDevices];
@@ -1038,9 +1038,11 @@ extern "C" bi_status bi_device_status(bi_stream stream) {
                                  "draining in-flight work", "debug wait", "conv producer waiting for a free stage",
                                  "weight packer waiting for its tile", "attention softmax waiting",
                                  "a cache slot past the cache's end",
-                                 "a page outside the cache, or a length past the page table"};
+                                 "a page outside the cache, or a length past the page table",
+                                 "a given number or a row's setting to sample by"};
   const unsigned site = (v >> 8) & 0xFF;
   why = std::string(site == kSitePagedSlot || site == kSitePagedPage ? "bad index on the device: "
+                    : site == kSiteSample                            ? "bad value on the device: "
                                                                      : "device wait ran out: ") +
         (site < sizeof(kSites) / sizeof(kSites[0]) ? kSites[site] : "?");
   return finish((bi_status)(v & 0xFF), why);

@@ -41,6 +41,7 @@ enum : unsigned int {
   kSiteAttnSoftmax = 9,
   kSitePagedSlot = 10,  // a token's cache slot does not exist
   kSitePagedPage = 11,  // a page or a length that the table does not have
+  kSiteSample = 12,     // a setting of a sampled row that is none
 };
 __host__ __device__ constexpr unsigned int status_code(unsigned int bi_err, unsigned int site) {
   return bi_err | (site << 8);

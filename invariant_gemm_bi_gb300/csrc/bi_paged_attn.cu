@@ -60,6 +60,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "bi_e4m3.cuh"
 #include "bi_launch.h"
 #include "bi_ptx_ext.cuh"
 #include "bi_serve.h"
@@ -103,10 +104,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// What p is multiplied by before it is cut into 16-bit numbers, and its reciprocal.
-template <int F16>
+// Kinds of cache: bf16 and fp16 as q, or e4m3 with scales.
+constexpr int kCache16 = 1, kCache8 = 2;  // fp16, e4m3
+// What a weight is multiplied by before it is cut into 16-bit numbers, and what
+// takes it off the joined result (in 8 bits a unit's end does).
+template <int C>
 struct Up {
-  static constexpr float v = F16 ? 32768.0f : 1.0f, back = 1.0f / v;
+  static constexpr float v = C == kCache8 ? 16384.0f : C == kCache16 ? 32768.0f : 1.0f;
+  static constexpr float back = C == kCache8 ? 1.0f : 1.0f / v;
 };
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -158,16 +163,19 @@ struct Unit {
   int b, hk, piece, len, k0, k1;
 };
 
-template <int D, int NT>
+template <int C, int D, int NT>
 struct Shape {
-  static constexpr bool kBig = D == 256 || (D == 128 && NT == 2);
+  static constexpr bool kBig = C != kCache8 && (D == 256 || (D == 128 && NT == 2));
   static constexpr int W = kBig ? 8 : 4;                     // warps of a CTA
-  static constexpr int kCtas = kBig ? 1 : (D == 64 ? (NT == 1 ? 4 : 3) : 2);  // CTAs of an SM
+  static constexpr int kCtas = C == kCache8 ? (D == 64 && NT == 1 ? 4 : D == 128 && NT == 1 ? 3 : 2)
+                               : kBig       ? 1
+                                            : (D == 64 ? (NT == 1 ? 4 : 3) : 2);  // CTAs of an SM
+  static constexpr int E = C == kCache8 ? 1 : 2;             // bytes of an element
   static constexpr int KT = D == 256 ? 1 : 2;                // 16-key groups of a tile
   static constexpr int kTile = 16 * KT;                      // keys of a tile
   static constexpr int kStep = W * kTile;
-  static constexpr int KJ = D / 32;                          // 16-byte chunks of a lane in a key row
-  static constexpr int kSlotBytes = kTile * D * 2;           // a tile's keys, or its values
+  static constexpr int KJ = D * E / 64;                      // 16-byte chunks of a lane in a key row
+  static constexpr int kSlotBytes = kTile * D * E;           // a tile's keys, or its values
   static constexpr int kRow = D + 4;                         // padded row of the join: no bank conflicts
   struct Shared {
     unsigned char ring[W][3][kSlotBytes];
@@ -209,9 +217,12 @@ constexpr uint32_t kBarUpper = 1, kBarLower = 2, kBarRead = 3;
 
 // ONE: a cluster has one (request, head tile), a CTA each of its pieces, and
 // joins them itself.
-template <int F16, int D, int NT, bool ONE>
-__global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) paged_attn_kernel(const PagedAttnParams p) {
-  using Sh = Shape<D, NT>;
+template <int C, int D, int NT, bool ONE>
+__global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCtas)
+    paged_attn_kernel(const PagedAttnParams p) {
+  using Sh = Shape<C, D, NT>;
+  constexpr bool Q8 = C == kCache8;
+  constexpr int F16 = C != 0;  // the tensor cores' operand type
   extern __shared__ __align__(1024) unsigned char dyn[];
   typename Sh::Shared& sm = *reinterpret_cast<typename Sh::Shared*>(dyn);
   constexpr int W = Sh::W, H = W / 2, kThreads = 32 * W, KT = Sh::KT, KJ = Sh::KJ, MT = D / 16;
@@ -294,7 +305,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
   int64_t pi = -1;               // the unit of the tile to request next
   int pkey = 0, pend = 0;        // its first key, and the unit's last
   const int32_t* ptab = nullptr; // the request's page table row
-  const unsigned short *kb = nullptr, *vb = nullptr;  // the unit's head, at this lane's chunk
+  const unsigned char *kb = nullptr, *vb = nullptr;  // the unit's head, at this lane's chunk
+  const float *ksb = nullptr, *vsb = nullptr;        // and its scales
   int page = -1, row = 0;        // of key pkey + lane % kTile; page -1: none
   auto advance = [&]() {         // to the warp's next tile
     pkey += Sh::kStep;
@@ -304,8 +316,12 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
       const int kvh = u.hk / p.head_tiles;
       pkey = u.k0 + warp * Sh::kTile, pend = u.k1;
       ptab = p.table + u.b * p.ld_table;
-      kb = static_cast<const unsigned short*>(p.k) + kvh * p.k_head + 8 * c;
-      vb = static_cast<const unsigned short*>(p.v) + kvh * p.v_head + 8 * c;
+      kb = static_cast<const unsigned char*>(p.k) + kvh * p.k_head * Sh::E + 16 * c;
+      vb = static_cast<const unsigned char*>(p.v) + kvh * p.v_head * Sh::E + 16 * c;
+      if constexpr (Q8) {
+        ksb = static_cast<const float*>(p.ks.ptr) + kvh * p.ks.head;
+        vsb = static_cast<const float*>(p.vs.ptr) + kvh * p.vs.head;
+      }
     }
     page = -1;
     const int j = pkey + (lane & (Sh::kTile - 1));
@@ -318,22 +334,27 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
   };
   const uint32_t ring = smem_u32(sm.ring[warp][0]);
   uint32_t live_next = 0;  // mask of the requested tile's keys
-  int64_t vo = 0;          // element offset of the lane's key in the value cache
+  int64_t vo = 0;          // byte offset of the lane's key in the value cache
+  float ks_next = 0.0f, vs_next = 0.0f;  // scales of the lane's key in the requested tile
   // Keys: lane (g, c) takes chunks c, c + 4, ... of keys g, g + 8, ... to a place of its own.
   auto request_keys = [&](int slot) {
     const bool there = page >= 0 && page < p.P;
     if (!there && page != -1) record_failure(p.status_word, status_code(BI_ERR_INVALID_ARG, kSitePagedPage));
     live_next = __ballot_sync(0xffffffffu, there);
-    const int64_t ko = there ? page * p.k_page + row * p.k_row : 0;
-    vo = there ? page * p.v_page + row * p.v_row : 0;
+    const int64_t ko = there ? (page * p.k_page + row * p.k_row) * Sh::E : 0;
+    vo = there ? (page * p.v_page + row * p.v_row) * Sh::E : 0;
+    if constexpr (Q8) {
+      ks_next = there ? __ldg(ksb + page * p.ks.page + row * p.ks.row) : 0.0f;
+      vs_next = there ? __ldg(vsb + page * p.vs.page + row * p.vs.row) : 0.0f;
+    }
     if (pi < units) {
       uint32_t dst = ring + slot * Sh::kSlotBytes + lane * 16;
 #pragma unroll
       for (int r = 0; r < 2 * KT; ++r) {
-        const unsigned short* a = kb + __shfl_sync(0xffffffffu, ko, 8 * r + g);
+        const unsigned char* a = kb + __shfl_sync(0xffffffffu, ko, 8 * r + g);
         const bool ok = (live_next >> (8 * r + g)) & 1;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j, dst += 512) copy16(dst, a + 32 * j, ok);
+        for (int j = 0; j < KJ; ++j, dst += 512) copy16(dst, a + 64 * j, ok);
       }
     }
     copies_commit();
@@ -342,34 +363,88 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
   // that the transposing reads of eight keys meet no bank twice.
   auto request_values = [&](int slot) {
     if (pi < units) {
-      const uint32_t dst = ring + slot * Sh::kSlotBytes + g * (2 * D) + ((c ^ g) & 3) * 16 + (g >> 2) * 64;
+      // (rows of 64 bytes: two keys to a line of all banks, the chunk permuted by the pair)
+      const uint32_t swap = Q8 && D == 64 ? (g >> 1) & 3 : g;
+      const uint32_t dst = ring + slot * Sh::kSlotBytes + g * (D * Sh::E) + ((c ^ swap) & 3) * 16 + (swap >> 2) * 64;
 #pragma unroll
       for (int r = 0; r < 2 * KT; ++r) {
-        const unsigned short* a = vb + __shfl_sync(0xffffffffu, vo, 8 * r + g);
+        const unsigned char* a = vb + __shfl_sync(0xffffffffu, vo, 8 * r + g);
         const bool ok = (live_next >> (8 * r + g)) & 1;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) copy16((dst + r * 16 * D) ^ (j * 64), a + 32 * j, ok);
+        for (int j = 0; j < KJ; ++j) copy16((dst + r * 8 * D * Sh::E) ^ (j * 64), a + 64 * j, ok);
       }
     }
     copies_commit();
   };
-  // Q^T fragments: head g of tile n, dimensions 32 j + 8 c .. + 7
-  uint4 q[NT][KJ], qn[NT][KJ];
+  // Q^T fragments: head g of tile n, dimensions 32 j + 8 c .. + 7; with caches in
+  // 8 bits chunks of 16 dimensions, 64 (j / 2) + 16 c + 8 (j % 2) .. + 7
+  constexpr int QJ = D / 32;
+  uint4 q[NT][QJ], qn[NT][QJ];
+  float qs[NT][2];  // in 8 bits: a score's factor for heads 2c, 2c + 1
   auto load_queries = [&](const Unit& u) {
     const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
     const unsigned short* qb =
-        static_cast<const unsigned short*>(p.q) + u.b * p.q_b + (kvh * p.group + h0 + g) * p.q_h + 8 * c;
+        static_cast<const unsigned short*>(p.q) + u.b * p.q_b + (kvh * p.group + h0 + g) * p.q_h + (Q8 ? 16 : 8) * c;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        qn[n][j] = h0 + 8 * n + g < p.group ? __ldg(reinterpret_cast<const uint4*>(qb + 8 * n * p.q_h + 32 * j))
-                                            : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < QJ; ++j)
+        qn[n][j] = h0 + 8 * n + g < p.group
+                       ? __ldg(reinterpret_cast<const uint4*>(qb + 8 * n * p.q_h + (Q8 ? 64 * (j / 2) + 8 * (j % 2) : 32 * j)))
+                       : make_uint4(0, 0, 0, 0);
+  };
+  // With caches in 8 bits, whose numbers are fp16 to the tensor cores, so is q,
+  // brought to a largest element of 2^13 .. 2^14 a head by a power of two: exact
+  // but for elements below 2^-27 of the largest, which are off by 2^-39 of it at
+  // most.  A head that holds a NaN or an infinity gets a NaN for its factor.
+  auto take_queries = [&]() {
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < QJ; ++j) q[n][j] = qn[n][j];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t top = 0;
+        auto both = [&](uint32_t w, float& lo, float& hi) {
+          lo = p.in_f16 ? low16<1>(w) : low16<0>(w);
+          hi = p.in_f16 ? high16<1>(w) : high16<0>(w);
+        };
+        auto look = [&](uint32_t w) {
+          float lo, hi;
+          both(w, lo, hi);
+          top = max(top, max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu));
+        };
+#pragma unroll
+        for (int j = 0; j < QJ; ++j) look(qn[n][j].x), look(qn[n][j].y), look(qn[n][j].z), look(qn[n][j].w);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(min((int)(top >> 23) - 127, 127), -100) - 13;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+        auto scaled = [&](uint32_t w) {
+          float lo, hi;
+          both(w, lo, hi);
+          return pack16<1>(lo * down, hi * down);
+        };
+#pragma unroll
+        for (int j = 0; j < QJ; ++j)
+          q[n][j] = make_uint4(scaled(qn[n][j].x), scaled(qn[n][j].y), scaled(qn[n][j].z), scaled(qn[n][j].w));
+        float f = __fmul_rn(__uint_as_float((uint32_t)(127 + e) << 23), p.score_log2);
+        if (top >= 0x7f800000u) f = __uint_as_float(0x7fffffffu);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) qs[n][h] = __shfl_sync(0xffffffffu, f, (2 * c + h) * 4);
+      }
+    }
   };
   // where this lane's row of a transposing read starts: blocks (keys 0-7, dims
   // 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15); the chunk is permuted by the key
-  const uint32_t vrow = ((lane & 7) + ((lane >> 4) & 1) * 8) * (2 * D);
-  const uint32_t vchunk = (lane >> 3) & 1, vkey = lane & 7;
+  // (in 8 bits a transposed element is two dimensions of a key: blocks (keys 0-7,
+  // dims 0-15), (8-15, 0-15), (0-7, 16-31), (8-15, 16-31))
+  const uint32_t vrow = ((lane & 7) + ((lane >> (Q8 ? 3 : 4)) & 1) * 8) * (D * Sh::E);
+  const uint32_t vchunk = (lane >> (Q8 ? 4 : 3)) & 1, vkey = Q8 && D == 64 ? (lane >> 1) & 3 : lane & 7;
+  // the dimensions of the accumulators' rows g and g + 8 of 16-dimension block i
+  auto dim = [&](int i, int x) { return Q8 ? 16 * i + 2 * g + x : 16 * i + 8 * x + g; };
 
   Unit u = unit_at(0, cw);
   load_queries(u);
@@ -379,21 +454,37 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
   advance();
   int sk = 0;  // slot of the tile's keys; its values are in the slot after it
   for (int64_t ui = 0; ui < units; ++ui) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < KJ; ++j) q[n][j] = qn[n][j];
+    take_queries();
     const Unit next = unit_at(min(ui + 1, units - 1), cw);
     load_queries(next);
     float o[MT][NT][4] = {};
     float m[NT][2], l[NT][2];
+    float mo[NT][2];  // in 8 bits: the reference of o, the largest t + log2 of a value's scale
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+      if constexpr (Q8) mo[n][0] = mo[n][1] = -INFINITY;
+    }
     for (int key = u.k0 + warp * Sh::kTile; key < u.k1; key += Sh::kStep) {
       const int sv = sk == 2 ? 0 : sk + 1, sn = sk == 0 ? 2 : sk - 1;
       copies_wait<1>();  // this tile's keys are here
       __syncwarp();      // and every lane is done with the last tile's values
       const uint32_t live = live_next;
+      // in 8 bits: scales of keys 8 r + g, the values' as 2^vlog * vfrac
+      float ks[2 * KT], vlog[2 * KT], vfrac[2 * KT];
+      if constexpr (Q8) {
+        const uint32_t bits = __float_as_uint(vs_next), e = (bits >> 23) & 255u;
+        const bool plain = e != 0 && e != 255;
+        const float lg = plain ? (float)((int)e - 127) : e == 0 ? -127.0f : 0.0f;
+        const float fr = plain ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u)
+                               : vs_next * (e == 0 ? 1.7014118346046923e38f /* 2^127 */ : 1.0f);
+#pragma unroll
+        for (int r = 0; r < 2 * KT; ++r) {
+          ks[r] = __shfl_sync(0xffffffffu, ks_next, 8 * r + g);
+          vlog[r] = __shfl_sync(0xffffffffu, lg, 8 * r + g);
+          vfrac[r] = __shfl_sync(0xffffffffu, fr, 8 * r + g);
+        }
+      }
       request_keys(sn);
       // scores of keys g (elements 0, 1) and g + 8 (2, 3) for heads 2c, 2c + 1
       float s[KT][NT][4] = {};
@@ -404,10 +495,24 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
           for (int t = 0; t < KT; ++t) {
             const uint4 k0 = read_chunk(src + (2 * t * KJ + j) * 512), k1 = read_chunk(src + ((2 * t + 1) * KJ + j) * 512);
+            if constexpr (!Q8) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<F16>(s[t][n], k0.x, k1.x, k0.y, k1.y, q[n][j].x, q[n][j].y);
-              mma16816<F16>(s[t][n], k0.z, k1.z, k0.w, k1.w, q[n][j].z, q[n][j].w);
+              for (int n = 0; n < NT; ++n) {
+                mma16816<F16>(s[t][n], k0.x, k1.x, k0.y, k1.y, q[n][j].x, q[n][j].y);
+                mma16816<F16>(s[t][n], k0.z, k1.z, k0.w, k1.w, q[n][j].z, q[n][j].w);
+              }
+            } else {
+              auto step = [&](uint32_t w0, uint32_t w1, int h, bool upper) {  // four dimensions of a lane
+                const uint32_t a0 = e4m3x2_to_half2(w0 & 0xffffu), a2 = e4m3x2_to_half2(w0 >> 16);
+                const uint32_t a1 = e4m3x2_to_half2(w1 & 0xffffu), a3 = e4m3x2_to_half2(w1 >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  const uint4& b = q[n][2 * j + h];
+                  mma16816<F16>(s[t][n], a0, a1, a2, a3, upper ? b.z : b.x, upper ? b.w : b.y);
+                }
+              };
+              step(k0.x, k1.x, 0, false), step(k0.y, k1.y, 0, true);
+              step(k0.z, k1.z, 1, false), step(k0.w, k1.w, 1, true);
             }
           }
       }
@@ -417,7 +522,9 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][n][e] = __fmul_rn(s[t][n][e], p.score_log2);
+          for (int e = 0; e < 4; ++e)
+            s[t][n][e] = Q8 ? __fmul_rn(__fmul_rn(s[t][n][e], ks[2 * t + (e >> 1)]), qs[n][e & 1])
+                            : __fmul_rn(s[t][n][e], p.score_log2);
         if (live != (Sh::kTile == 32 ? 0xffffffffu : live | 0xffffu)) {
 #pragma unroll
           for (int t = 0; t < KT; ++t)
@@ -434,12 +541,29 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
         for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], x));
-        if (__any_sync(0xffffffffu, mx[0] != m[n][0] || mx[1] != m[n][1])) {
+        float mxo[2] = {0.0f, 0.0f};
+        if constexpr (Q8) {
+          mxo[0] = mo[n][0], mxo[1] = mo[n][1];
+#pragma unroll
+          for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mxo[e & 1] = fmaxf(mxo[e & 1], __fadd_rn(s[t][n][e], vlog[2 * t + (e >> 1)]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mxo[h] = fmaxf(mxo[h], __shfl_xor_sync(0xffffffffu, mxo[h], x));
+        }
+        const bool moved = mx[0] != m[n][0] || mx[1] != m[n][1] || (Q8 && (mxo[0] != mo[n][0] || mxo[1] != mo[n][1]));
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float alpha = mx[h] == -INFINITY ? 0.0f : ex2_approx(m[n][h] - mx[h]);
+            float alpha = mx[h] == -INFINITY ? 0.0f : ex2_approx(m[n][h] - mx[h]);
             m[n][h] = mx[h];
             l[n][h] = __fmul_rn(l[n][h], alpha);
+            if constexpr (Q8) {
+              alpha = mxo[h] == -INFINITY ? 0.0f : ex2_approx(mo[n][h] - mxo[h]);
+              mo[n][h] = mxo[h];
+            }
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][n][h] *= alpha, o[i][n][2 + h] *= alpha;
           }
@@ -452,8 +576,15 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
           for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int e = h; e < 4; e += 2) {
-              s[t][n][e] = ex2_approx(__fsub_rn(s[t][n][e], ref));
-              sum += s[t][n][e];
+              if constexpr (Q8) {
+                const float refo = mxo[h] == -INFINITY ? 0.0f : mxo[h];
+                const float weight = ex2_approx(__fsub_rn(__fadd_rn(s[t][n][e], vlog[2 * t + (e >> 1)]), refo));
+                sum += ex2_approx(__fsub_rn(s[t][n][e], ref));
+                s[t][n][e] = __fmul_rn(weight, vfrac[2 * t + (e >> 1)]);
+              } else {
+                s[t][n][e] = ex2_approx(__fsub_rn(s[t][n][e], ref));
+                sum += s[t][n][e];
+              }
             }
           l[n][h] += sum;
         }
@@ -464,7 +595,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
             float(&e)[4] = s[t][n];
             if (F16 && x == 0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] *= Up<F16>::v;
+              for (int i = 0; i < 4; ++i) e[i] *= Up<C>::v;
             }
             const uint32_t lo = pack16<F16>(e[0], e[1]), hi = pack16<F16>(e[2], e[3]);
             pf[t][n][x][0] = transpose8x8(lo);
@@ -483,7 +614,24 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; Q8 && i < MT; i += 2) {
+          // of a key two neighbouring dimensions: bytes (k, d) (k, d + 1) (k + 1, d) (k + 1, d + 1)
+          const uint4 a = read_transposed(src + t * (16 * D) + (((i + vchunk) ^ vkey) * 16));
+          auto step = [&](uint32_t k0, uint32_t k8, int i) {
+            k0 = __byte_perm(k0, 0, 0x3120), k8 = __byte_perm(k8, 0, 0x3120);
+            const uint32_t a0 = e4m3x2_to_half2(k0 & 0xffffu), a1 = e4m3x2_to_half2(k0 >> 16);
+            const uint32_t a2 = e4m3x2_to_half2(k8 & 0xffffu), a3 = e4m3x2_to_half2(k8 >> 16);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < PS; ++x) mma16816<F16>(o[i][n], a0, a1, a2, a3, pf[t][n][x][0], pf[t][n][x][1]);
+          };
+          step(a.x, a.y, i), step(a.z, a.w, i + 1);
+        }
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; !Q8 && i < MT; ++i) {
           // rows g: dimension 16 i + g; rows g + 8: 16 i + 8 + g
           const uint4 a = read_transposed(src + t * (32 * D) + (((2 * i + vchunk) ^ vkey) * 16));
 #pragma unroll
@@ -500,6 +648,16 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
     // next unit.
     const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
     const int head = kvh * p.group + h0, heads = min(8 * NT, p.group - h0);
+    if constexpr (Q8) {  // o relative to m, as l is
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = mo[n][h] == -INFINITY ? 0.0f : ex2_approx(mo[n][h] - m[n][h]) * (1.0f / Up<C>::v);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) o[i][n][h] *= f, o[i][n][2 + h] *= f;
+        }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -516,8 +674,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
           if (hh < heads) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-              sm.o[to][hh][16 * i + g] = o[i][n][h];
-              sm.o[to][hh][16 * i + 8 + g] = o[i][n][2 + h];
+              sm.o[to][hh][dim(i, 0)] = o[i][n][h];
+              sm.o[to][hh][dim(i, 1)] = o[i][n][2 + h];
             }
           }
         }
@@ -535,8 +693,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
           if (hh < heads) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-              o[i][n][h] = fmaf(f2, sm.o[from][hh][16 * i + g], __fmul_rn(f, o[i][n][h]));
-              o[i][n][2 + h] = fmaf(f2, sm.o[from][hh][16 * i + 8 + g], __fmul_rn(f, o[i][n][2 + h]));
+              o[i][n][h] = fmaf(f2, sm.o[from][hh][dim(i, 0)], __fmul_rn(f, o[i][n][h]));
+              o[i][n][2 + h] = fmaf(f2, sm.o[from][hh][dim(i, 1)], __fmul_rn(f, o[i][n][2 + h]));
             }
           }
         }
@@ -569,20 +727,20 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
             const int hh = 8 * n + 2 * c + h;
             if (hh >= heads) continue;
             if (pieces == 1) {
-              const float inv = l[n][h] == 0.0f ? 0.0f : __frcp_rn(l[n][h]) * Up<F16>::back;  // no key: zeros
-              const int64_t at = u.b * p.o_b + (head + hh) * p.o_h + g;
+              const float inv = l[n][h] == 0.0f ? 0.0f : __frcp_rn(l[n][h]) * Up<C>::back;  // no key: zeros
+              const int64_t at = u.b * p.o_b + (head + hh) * p.o_h;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 // + 0: a negative zero becomes the positive one that a join makes of it
-                store_one(p.o, p.out_kind, at + 16 * i, __fmul_rn(__fadd_rn(o[i][n][h], 0.0f), inv));
-                store_one(p.o, p.out_kind, at + 16 * i + 8, __fmul_rn(__fadd_rn(o[i][n][2 + h], 0.0f), inv));
+                store_one(p.o, p.out_kind, at + dim(i, 0), __fmul_rn(__fadd_rn(o[i][n][h], 0.0f), inv));
+                store_one(p.o, p.out_kind, at + dim(i, 1), __fmul_rn(__fadd_rn(o[i][n][2 + h], 0.0f), inv));
               }
             } else {
               const int64_t part = ((int64_t)u.b * p.max_splits + u.piece) * p.Hq + head + hh;
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
-                p.ws_o[part * D + 16 * i + g] = o[i][n][h];
-                p.ws_o[part * D + 16 * i + 8 + g] = o[i][n][2 + h];
+                p.ws_o[part * D + dim(i, 0)] = o[i][n][h];
+                p.ws_o[part * D + dim(i, 1)] = o[i][n][2 + h];
               }
               if (g == 0) p.ws_ml[2 * part] = m[n][h], p.ws_ml[2 * part + 1] = l[n][h];
             }
@@ -624,7 +782,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT>::W, Shape<D, NT>::kCtas) pag
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = fmaf(f, o[r][i], a[i]);
         }
-        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum) * Up<F16>::back;  // no key: zeros
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum) * Up<C>::back;  // no key: zeros
         const int64_t at = u.b * p.o_b + (head + h) * p.o_h + d;
 #pragma unroll
         for (int i = 0; i < 4; ++i) store_one(p.o, p.out_kind, at + i, __fmul_rn(a[i], inv));
@@ -735,7 +893,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
       join_into<V>(r, x.m, x.l, x.o);
     }
   }
-  const float inv = r.l == 0.0f ? 0.0f : __frcp_rn(r.l) * (p.in_f16 ? Up<1>::back : Up<0>::back);
+  const float inv = r.l == 0.0f ? 0.0f : __frcp_rn(r.l) * (p.e4m3 ? Up<kCache8>::back : p.in_f16 ? Up<kCache16>::back : Up<0>::back);
   const int64_t at = b * p.o_b + h * p.o_h + d0 + 2 * lane;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -749,13 +907,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
 }
 
 // *joined: whether the launch leaves nothing to join.
-template <int F16, int D, int NT>
+template <int C, int D, int NT>
 cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
-  using Sh = Shape<D, NT>;
+  using Sh = Shape<C, D, NT>;
   constexpr int kBytes = sizeof(typename Sh::Shared);
   static_assert(kBytes <= 227 * 1024 && Sh::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-  // one slot per instance, from 24 on (ONE: from 64 on)
-  constexpr int kSlot = 24 + (D == 256 ? 8 + F16 : (D == 128 ? 4 : 0) + 2 * F16 + NT - 1);
+  // one slot per instance, from 24 on (ONE: from 64 on), for caches in 8 bits from 115 on (120)
+  constexpr int kSlot = C == kCache8 ? 115 + (D == 256 ? 4 : (D == 128 ? 2 : 0) + NT - 1)
+                                     : 24 + (D == 256 ? 8 + C : (D == 128 ? 4 : 0) + 2 * C + NT - 1);
+  constexpr int kOneSlot = C == kCache8 ? kSlot + 5 : kSlot + 40;
   p.head_tiles = (p.group + 8 * NT - 1) / (8 * NT);
   const int64_t most = (int64_t)p.B * p.max_splits * p.Hkv * p.head_tiles;
   // Tables of at most 4096 keys whose units all run at once: a CTA a unit and a
@@ -766,7 +926,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
   const bool one = p.max_splits <= kMaxCluster && most <= (int64_t)num_sms * Sh::kCtas;
   *joined = p.max_splits == 1 || one;
   if (one) {
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, true>), kBytes, kSlot + 40);
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<C, D, NT, true>), kBytes, kOneSlot);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)most);
@@ -780,23 +940,23 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<F16, D, NT, true>, p);
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<C, D, NT, true>, p);
   }
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<F16, D, NT, false>), kBytes, kSlot);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&paged_attn_kernel<C, D, NT, false>), kBytes, kSlot);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms * Sh::kCtas);
-  paged_attn_kernel<F16, D, NT, false><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
+  paged_attn_kernel<C, D, NT, false><<<grid, 32 * Sh::W, kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int F16>
+template <int C>
 cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t stream) {
   // more than eight query heads a key-value head: 16 a unit, except at
   // D = 256, where two tiles' accumulators would not fit the registers
   const bool wide = p.group > 8;
-  if (p.D == 64) return wide ? launch<F16, 64, 2>(p, num_sms, joined, stream) : launch<F16, 64, 1>(p, num_sms, joined, stream);
-  if (p.D == 128) return wide ? launch<F16, 128, 2>(p, num_sms, joined, stream) : launch<F16, 128, 1>(p, num_sms, joined, stream);
-  return launch<F16, 256, 1>(p, num_sms, joined, stream);
+  if (p.D == 64) return wide ? launch<C, 64, 2>(p, num_sms, joined, stream) : launch<C, 64, 1>(p, num_sms, joined, stream);
+  if (p.D == 128) return wide ? launch<C, 128, 2>(p, num_sms, joined, stream) : launch<C, 128, 1>(p, num_sms, joined, stream);
+  return launch<C, 256, 1>(p, num_sms, joined, stream);
 }
 
 }  // namespace
@@ -813,7 +973,9 @@ bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::s
   if (st != BI_OK) return st;
   p.status_word = dev.status_word;
   bool joined = false;
-  cudaError_t e = p.in_f16 ? launch_dim<1>(p, dev.num_sms, &joined, stream) : launch_dim<0>(p, dev.num_sms, &joined, stream);
+  cudaError_t e = p.e4m3     ? launch_dim<kCache8>(p, dev.num_sms, &joined, stream)
+                  : p.in_f16 ? launch_dim<1>(p, dev.num_sms, &joined, stream)
+                             : launch_dim<0>(p, dev.num_sms, &joined, stream);
   if (e == cudaSuccess && !joined) {
     const int64_t rows = (int64_t)p.B * p.Hq;
     constexpr int kT = 32 * kJoinWarps;

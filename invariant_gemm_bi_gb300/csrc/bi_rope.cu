@@ -36,6 +36,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "bi_e4m3.cuh"
 #include "bi_launch.h"
 #include "bi_ptx_ext.cuh"
 #include "bi_serve.h"
@@ -44,6 +45,7 @@ namespace bi {
 namespace {
 
 constexpr int kAny = -1;  // element kind read from the parameters
+constexpr int kE4m3 = 3;  // a cache in 8 bits, with scales
 
 __device__ __forceinline__ float half_to_f(uint32_t h, int kind) {
   return kind == 1 ? __half2float(__ushort_as_half((unsigned short)h)) : __uint_as_float(h << 16);
@@ -61,7 +63,7 @@ __device__ __forceinline__ uint32_t f2_to_half2(float a, float b, int kind) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ int elem_bytes(int kind) { return kind == 2 ? 4 : 2; }
+__device__ __forceinline__ int elem_bytes(int kind) { return kind == 2 ? 4 : kind == kE4m3 ? 1 : 2; }
 
 // Eight consecutive elements from their raw words: 4 or 8 of them.
 __device__ __forceinline__ void unpack_oct(const uint4& lo, const uint4& hi, int kind, float (&f)[8]) {
@@ -94,10 +96,22 @@ __device__ __forceinline__ void store_one(void* p, int kind, float v) {
     *reinterpret_cast<unsigned short*>(p) = (unsigned short)f_to_half(v, kind);
 }
 
-// a cos and a sin of position n's angle for pair i.
+// a cos and a sin of position n's angle for pair i.  FINE (caches in 8 bits):
+// with what the angle's rounding to fp32 left out, as a small turn d more,
+// sin + d cos and cos - d sin.  An element next to a border of two e4m3 numbers
+// is put on one side or the other, a sixteenth of it apart, by errors of any
+// size; with the angle's 2^-24 there are 1.7 times as many on the wrong side.
+template <bool FINE = false>
 __device__ __forceinline__ void turn(const RopeParams& p, int64_t n, int i, float& c, float& s) {
   const uint64_t t = p.phase[i] * (uint64_t)n;
-  sincospif(__fmul_rn(__ll2float_rn((long long)t), 1.0842021724855044e-19f /* 2^-63 */), &s, &c);
+  const float a = __ll2float_rn((long long)t);
+  sincospif(__fmul_rn(a, 1.0842021724855044e-19f /* 2^-63 */), &s, &c);
+  if constexpr (FINE) {
+    const float d = __ll2float_rn((long long)t - __float2ll_rz(a)) * 3.4061215800865545e-19f;  // pi 2^-63
+    const float s0 = s;
+    s = __fmaf_rn(d, c, s);
+    c = __fmaf_rn(-d, s0, c);
+  }
   c = __fmul_rn(c, p.magnitude);
   s = __fmul_rn(p.transpose ? -s : s, p.magnitude);
 }
@@ -127,6 +141,7 @@ __device__ __forceinline__ int64_t token_position(const RopeParams& p, int64_t t
 struct TokenPlace {
   const char *q, *k, *v;
   char *qd, *kd, *vd;
+  float *ks, *vs;  // scales of a cache in 8 bits
 };
 __device__ __forceinline__ TokenPlace token_place(const RopeParams& p, int64_t t, int64_t slot) {
   TokenPlace a;
@@ -135,10 +150,15 @@ __device__ __forceinline__ TokenPlace token_place(const RopeParams& p, int64_t t
   a.k = static_cast<const char*>(p.k.ptr) + t * p.k.t_stride * elem_bytes(p.kv_kind);
   a.v = static_cast<const char*>(p.v.ptr) + t * p.v.t_stride * elem_bytes(p.kv_kind);
   a.kd = a.vd = nullptr;
+  a.ks = a.vs = nullptr;
   if (slot >= 0) {
     const uint32_t page = (uint32_t)slot / (uint32_t)p.ps, row = (uint32_t)slot - page * (uint32_t)p.ps;
     a.kd = static_cast<char*>(p.kc.ptr) + (page * p.kc.page + row * p.kc.row) * elem_bytes(p.c_kind);
     a.vd = static_cast<char*>(p.vc.ptr) + (page * p.vc.page + row * p.vc.row) * elem_bytes(p.c_kind);
+    if (p.ks.ptr) {
+      a.ks = static_cast<float*>(p.ks.ptr) + page * p.ks.page + row * p.ks.row;
+      a.vs = static_cast<float*>(p.vs.ptr) + page * p.vs.page + row * p.vs.row;
+    }
   }
   return a;
 }
@@ -155,6 +175,26 @@ __device__ __forceinline__ char* target(const RopeParams& p, const TokenPlace& a
   h -= p.hq;
   if (h < p.hkv) return a.kd ? a.kd + h * p.kc.head * elem_bytes(kc) : nullptr;
   return a.vd ? a.vd + (h - p.hkv) * p.vc.head * elem_bytes(kc) : nullptr;
+}
+
+// A cache in 8 bits.  The size of a head, from which its scale follows, is the
+// largest |a| (|x1| + |x2|) of its rotated pairs and |x| of its other elements:
+// no angle takes an element past it, so a key's scale does not depend on its
+// position, is known before the angles are, and is the same from one sum of two
+// numbers a pair whatever computes it (the largest rotated element, rounded one
+// way or the other next to 448 2^e, would decide a whole head's scale).  It is
+// up to twice the largest element: at most one binade at the small end.
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t pair_size(float x1, float x2, float magnitude) {
+  return size_bits(__fmul_rn(__fadd_rn(fabsf(x1), fabsf(x2)), magnitude));
+}
+__device__ __forceinline__ uint2 quantize_oct(const float (&x)[8], float inv) {
+  return make_uint2(to_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                    to_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+}
+__device__ __forceinline__ float* scale_target(const RopeParams& p, const TokenPlace& a, int h) {
+  h -= p.hq;
+  return h < p.hkv ? a.ks + h * p.ks.head : a.vs + (h - p.hkv) * p.vs.head;
 }
 
 // Aligned operands.  A head has half/8 units of pairs and (D - 2 half)/16 of
@@ -206,7 +246,7 @@ __global__ void __launch_bounds__(256, QK == kAny ? 2 : 4)
     const int n = (int)min((int64_t)tokens, p.T - t0) * p.half;
     for (int i = tid; i < n; i += 256) {
       const int k = i / p.half, pair = i - k * p.half;
-      turn(p, token_position(p, t0 + k), pair, turns[i].x, turns[i].y);
+      turn<CK == kE4m3>(p, token_position(p, t0 + k), pair, turns[i].x, turns[i].y);
     }
     __syncthreads();
     if (live && !tail) {
@@ -221,18 +261,35 @@ __global__ void __launch_bounds__(256, QK == kAny ? 2 : 4)
     }
   }
   if (live && p.hkv) at = token_place(p, t, token_slot(p, t));
+  const float mag = fabsf(p.magnitude);
   int slot = 0;
   for (; h < h_end; h += 8) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
     char* o = live ? target(p, at, h, ko, kc) : nullptr;
+    uint32_t size = 0;  // of the unit's part of a cached head
+    float x[8], y[8];
     if (o) {
       const int in = h < p.hq ? kq : kk, out = h < p.hq ? ko : kc;
       const uint32_t src = mine + slot * (kPieces * 256 * 16);
-      float x[8], y[8];
       const uint4 none = make_uint4(0, 0, 0, 0);
       const bool wide = kPieces == 4 && in == 2;
       unpack_oct(ld_shared_v4(src), wide ? ld_shared_v4(src + 2 * 256 * 16) : none, in, x);
       unpack_oct(ld_shared_v4(src + 256 * 16), wide ? ld_shared_v4(src + 3 * 256 * 16) : none, in, y);
+      if constexpr (CK == kE4m3) {
+        if (h >= p.hq) {
+          if (tail || h >= p.hq + p.hkv || !p.half) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) size = max(size, max(size_bits(x[i]), size_bits(y[i])));
+          } else if (p.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              size = max(size, max(pair_size(x[i], x[i + 1], mag), pair_size(y[i], y[i + 1], mag)));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) size = max(size, pair_size(x[i], y[i], mag));
+          }
+        }
+      }
       if (!tail && h < p.hq + p.hkv && p.half) {
         if (p.interleaved) {
 #pragma unroll
@@ -245,8 +302,21 @@ __global__ void __launch_bounds__(256, QK == kAny ? 2 : 4)
           for (int i = 0; i < 8; ++i) rotate(x[i], y[i], c[i], s[i]);
         }
       }
-      store_oct(o + e0 * elem_bytes(out), out, x);
-      store_oct(o + e1 * elem_bytes(out), out, y);
+      if (CK != kE4m3 || h < p.hq) {
+        store_oct(o + e0 * elem_bytes(out), out, x);
+        store_oct(o + e1 * elem_bytes(out), out, y);
+      }
+    }
+    if constexpr (CK == kE4m3) {
+      if (h >= p.hq) {  // the units of a head are neighbouring lanes, a power of two of them
+        for (int d = units >> 1; d > 0; d >>= 1) size = max(size, __shfl_xor_sync(0xffffffffu, size, d));
+        if (o) {
+          const float scale = block_scale(size), inv = inverse_scale(scale);
+          *reinterpret_cast<uint2*>(o + e0) = quantize_oct(x, inv);
+          *reinterpret_cast<uint2*>(o + e1) = quantize_oct(y, inv);
+          if (u == 0) *scale_target(p, at, h) = scale;
+        }
+      }
     }
     request(h + 8 * kSlots, slot);  // the slot just read, by this lane
     slot = slot + 1 == kSlots ? 0 : slot + 1;
@@ -290,6 +360,67 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ R
   }
 }
 
+// A cache in 8 bits at any alignment and head dimension: a warp a token's head,
+// which it reads twice, for the size and for the values.
+__global__ void __launch_bounds__(256) rope_quantize_any_kernel(const __grid_constant__ RopeParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = p.hq + 2 * p.hkv;
+  const float mag = fabsf(p.magnitude);
+  const int64_t all = (int64_t)p.T * heads;
+  for (int64_t id = (int64_t)blockIdx.x * 8 + warp; id < all; id += (int64_t)gridDim.x * 8) {
+    const int64_t t = id / heads;
+    const int h = (int)(id - t * heads);
+    const TokenPlace at = token_place(p, t, token_slot(p, t));
+    char* o = target(p, at, h, p.qo_kind, kE4m3);
+    if (!o) continue;
+    const char* src = source(p, at, h, p.q_kind, p.kv_kind);
+    const bool query = h < p.hq, turned = h < p.hq + p.hkv;
+    const int in = query ? p.q_kind : p.kv_kind, ie = elem_bytes(in);
+    const int half = turned ? p.half : 0, units = p.D - half;  // pairs, then single elements
+    auto places = [&](int u, int& e0, int& e1) {
+      if (u >= half)
+        e0 = half + u, e1 = -1;
+      else if (p.interleaved)
+        e0 = 2 * u, e1 = e0 + 1;
+      else
+        e0 = u, e1 = half + u;
+    };
+    float scale = 1.0f;
+    if (!query) {
+      uint32_t size = 0;
+      for (int u = lane; u < units; u += 32) {
+        int e0, e1;
+        places(u, e0, e1);
+        const float x = load_one(src + e0 * ie, in);
+        size = max(size, e1 < 0 ? size_bits(x) : pair_size(x, load_one(src + e1 * ie, in), mag));
+      }
+      scale = block_scale(__reduce_max_sync(0xffffffffu, size));
+      if (lane == 0) *scale_target(p, at, h) = scale;
+    }
+    const float inv = inverse_scale(scale);
+    const int64_t n = half ? token_position(p, t) : 0;
+    for (int u = lane; u < units; u += 32) {
+      int e0, e1;
+      places(u, e0, e1);
+      float x = load_one(src + e0 * ie, in), y = 0.0f;
+      if (e1 >= 0) {
+        float c, s;
+        turn<true>(p, n, u, c, s);
+        y = load_one(src + e1 * ie, in);
+        rotate(x, y, c, s);
+      }
+      if (query) {
+        const int oe = elem_bytes(p.qo_kind);
+        store_one(o + e0 * oe, p.qo_kind, x);
+        if (e1 >= 0) store_one(o + e1 * oe, p.qo_kind, y);
+      } else {
+        const uint32_t b = to_e4m3x2(x * inv, y * inv);
+        o[e0] = (char)b;
+        if (e1 >= 0) o[e1] = (char)(b >> 8);
+      }
+    }
+  }
+}
+
 template <int QK, int QO, int KV, int CK>
 cudaError_t launch_vec(const RopeParams& p, int num_sms, cudaStream_t stream) {
   const int units = p.half / 8 + (p.D - 2 * p.half) / 16, heads = p.hq + 2 * p.hkv;
@@ -304,7 +435,8 @@ cudaError_t launch_vec(const RopeParams& p, int num_sms, cudaStream_t stream) {
   if (blocks * z >= 4 * (int64_t)num_sms || heads > 8 * 65535) {
     constexpr size_t kRing = 6 * kSlot;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&rope_vec_kernel<QK, QO, KV, CK, 6>),
-                                  (int)(kRing + sizeof(float2) * kMaxTokens * BI_ROPE_MAX_PAIRS), 56 + QK + 1);
+                                  (int)(kRing + sizeof(float2) * kMaxTokens * BI_ROPE_MAX_PAIRS),
+                                  (CK == kE4m3 ? 96 : 56) + QK + 1);
     if (e != cudaSuccess) return e;
     rope_vec_kernel<QK, QO, KV, CK, 6>
         <<<dim3((unsigned)blocks, 1, z), 256, kRing + turns, stream>>>(p, units, tokens, heads);
@@ -326,7 +458,19 @@ bi_status launch_rope(const RopeParams& p, cudaStream_t stream, std::string* why
   const int kq = p.hq ? p.q_kind : p.kv_kind, ko = p.hq ? p.qo_kind : p.c_kind;
   const int kk = p.hkv ? p.kv_kind : kq, kc = p.hkv ? p.c_kind : ko;
   cudaError_t e;
-  if (!p.vec) {
+  if (kc == kE4m3) {
+    if (!p.vec) {
+      const int64_t warps = (int64_t)p.T * (p.hq + 2 * p.hkv);
+      rope_quantize_any_kernel<<<(unsigned)std::min<int64_t>((warps + 7) / 8, 1 << 20), 256, 0, stream>>>(q);
+      e = cudaGetLastError();
+    } else if (kq == 0 && (ko == 0 || !p.hq) && kk == 0) {
+      e = launch_vec<0, 0, 0, kE4m3>(q, dev.num_sms, stream);
+    } else if (kq == 1 && (ko == 1 || !p.hq) && kk == 1) {
+      e = launch_vec<1, 1, 1, kE4m3>(q, dev.num_sms, stream);
+    } else {
+      e = launch_vec<kAny, kAny, kAny, kE4m3>(q, dev.num_sms, stream);
+    }
+  } else if (!p.vec) {
     const int units = p.D - p.half;
     const int64_t grid = ((int64_t)p.T * units + 255) / 256;
     rope_any_kernel<<<(unsigned)grid, 256, 0, stream>>>(q, units);

@@ -55,16 +55,31 @@ struct RopeParams {
   void* q_out;
   int64_t qo_t, qo_h;
   PageView kc, vc;
+  PageView ks, vs;      // scales of a cache in 8 bits: fp32, element (page, row, h)
   const void* positions;  // [T] int32 or int64
   int32_t pos64;
   const int64_t* slots;   // [T]; negative: not stored
   int64_t num_slots;      // pages * page size
   int32_t T, hq, hkv, D, ps;
-  int32_t q_kind, qo_kind, kv_kind, c_kind;  // 0 bf16, 1 fp16, 2 fp32
+  int32_t q_kind, qo_kind, kv_kind, c_kind;  // 0 bf16, 1 fp16, 2 fp32, 3 e4m3 (caches)
   int32_t vec;          // 16-byte units: every row, stride and the rotary split are aligned
   unsigned int* status_word;
 };
 bi_status launch_rope(const RopeParams& p, cudaStream_t stream, std::string* why);
+
+// Rows of a cache in 8 bits, as numbers again (bi_cache8.cu).
+struct LoadParams {
+  PageView kc, vc, ks, vs;
+  void *k, *v;            // [T][H][D] of `kind`
+  int64_t k_t, k_h, v_t, v_h;
+  const int64_t* slots;   // [T]; negative: a row of zeros
+  int64_t num_slots;
+  int32_t T, H, D, ps;
+  int32_t kind;           // 0 bf16, 1 fp16, 2 fp32
+  int32_t vec;            // 16-byte units
+  unsigned int* status_word;
+};
+bi_status launch_paged_load(LoadParams& p, cudaStream_t stream, std::string* why);
 
 // Attention of one token per request over the paged cache.
 struct PagedAttnParams {
@@ -73,6 +88,7 @@ struct PagedAttnParams {
   const void* k;  // element (page, row, h, d) at page*k_page + row*k_row + h*k_head + d
   const void* v;
   int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  PageView ks, vs;       // scales of caches in 8 bits
   const int32_t* table;  // [B][W], row stride ld_table
   int64_t ld_table;
   const int32_t* lens;   // [B]
@@ -86,7 +102,8 @@ struct PagedAttnParams {
   int32_t max_splits;
   int32_t cap;           // keys a table row can name: min(W * ps, INT32_MAX)
   int32_t ps_shift;      // log2(ps), or -1 when ps is no power of two
-  int32_t in_f16, out_kind;
+  int32_t in_f16, out_kind;  // q's type; the caches have it too, or
+  int32_t e4m3;              // are in 8 bits with scales
   float score_log2;      // scale * log2(e), rounded once to fp32
   unsigned int* status_word;
 };

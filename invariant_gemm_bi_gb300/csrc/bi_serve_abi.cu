@@ -5,144 +5,9 @@
 #include <cstring>
 #include <string>
 
+#include "bi_check.h"
 #include "bi_launch.h"
 #include "bi_serve.h"
-
-namespace bi {
-namespace {
-
-bool is_float(int dtype) { return dtype == BI_BF16 || dtype == BI_F16 || dtype == BI_F32; }
-bool is_index(int dtype) { return dtype == BI_I32 || dtype == BI_I64; }
-int bytes_of(int dtype) { return dtype == BI_I64 ? 8 : (dtype == BI_F32 || dtype == BI_I32) ? 4 : 2; }
-int kind_of(int dtype) { return dtype == BI_F32 ? 2 : (dtype == BI_F16 ? 1 : 0); }
-bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// A check that fails keeps its status and reason; later checks are skipped.
-// Reasons are put together only then: a decode step makes these calls by the
-// hundred.
-struct Check {
-  bi_status st = BI_OK;
-  std::string why;
-
-  bool ok() const { return st == BI_OK; }
-  // `name` (if any): `reason`
-  void that(bool good, bi_status bad, const char* reason, const char* name = nullptr) {
-    if (good || !ok()) return;
-    st = bad;
-    why = name ? std::string(name) + ": " + reason : std::string(reason);
-  }
-  static bool empty(const bi_tensor* t) {
-    for (int i = 0; i < t->ndim; ++i)
-      if (t->shape[i] <= 0) return true;
-    return false;
-  }
-  // rank, type class, extents, strides, element alignment
-  void tensor(const bi_tensor* t, const char* name, int ndim, bool index) {
-    if (!ok()) return;
-    that(t != nullptr, BI_ERR_INVALID_ARG, "null tensor descriptor", name);
-    if (!ok()) return;
-    if (t->ndim != ndim) {
-      st = BI_ERR_INVALID_ARG;
-      why = std::string(name) + ": expected rank " + std::to_string(ndim) + ", got " + std::to_string(t->ndim);
-      return;
-    }
-    that(index ? is_index(t->dtype) : is_float(t->dtype), BI_ERR_UNSUPPORTED_DTYPE,
-         index ? "an integer type is needed" : "a bf16, fp16 or fp32 type is needed", name);
-    for (int i = 0; i < ndim; ++i) {
-      that(t->shape[i] >= 0 && t->shape[i] <= INT32_MAX, BI_ERR_INVALID_ARG, "an extent is out of range", name);
-      that(t->stride[i] >= 0 && t->stride[i] <= (int64_t)1 << 44, BI_ERR_UNSUPPORTED_LAYOUT,
-           "a stride is negative or out of range", name);
-    }
-    if (!ok()) return;
-    if (!empty(t)) {
-      double span = 1.0;
-      for (int i = 0; i < ndim; ++i) span += (double)(t->shape[i] - 1) * (double)t->stride[i];
-      that(span < 1125899906842624.0 /* 2^50 */, BI_ERR_UNSUPPORTED_LAYOUT, "spans more memory than there is", name);
-      that(t->ptr != nullptr, BI_ERR_INVALID_ARG, "null data pointer", name);
-      that(on(t->ptr, bytes_of(t->dtype)), BI_ERR_UNSUPPORTED_LAYOUT, "not aligned to its element size", name);
-    }
-    that(ndim == 0 || t->shape[ndim - 1] <= 1 || t->stride[ndim - 1] == 1, BI_ERR_UNSUPPORTED_LAYOUT,
-         "unit stride on the last dimension required", name);
-  }
-  // a contiguous index vector of n elements of the given type
-  void vec(const bi_tensor* t, const char* name, int64_t n, int dtype) {
-    tensor(t, name, 1, true);
-    if (!ok()) return;
-    if (t->shape[0] != n) {
-      st = BI_ERR_SHAPE_MISMATCH;
-      why = std::string(name) + ": expected " + std::to_string(n) + " elements";
-      return;
-    }
-    that(t->dtype == dtype, BI_ERR_UNSUPPORTED_DTYPE, dtype == BI_I64 ? "int64 is needed" : "int32 is needed", name);
-  }
-  // every element of an output has an address of its own
-  void distinct(const bi_tensor* t, const char* name) {
-    if (!ok() || empty(t)) return;
-    // dimensions in the order of their strides: each must clear what the smaller ones span
-    int order[4] = {0, 1, 2, 3};
-    for (int i = 0; i < t->ndim; ++i)
-      for (int j = i + 1; j < t->ndim; ++j)
-        if (t->stride[order[j]] < t->stride[order[i]]) std::swap(order[i], order[j]);
-    int64_t span = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-      const int d = order[i];
-      if (t->shape[d] == 1) continue;
-      that(t->stride[d] > span, BI_ERR_UNSUPPORTED_LAYOUT, "elements of the output overlap", name);
-      span += (t->shape[d] - 1) * t->stride[d];
-    }
-  }
-  // memory that t spans, as [begin, end)
-  static void range(const bi_tensor* t, uintptr_t* b, uintptr_t* e) {
-    *b = reinterpret_cast<uintptr_t>(t->ptr);
-    int64_t last = 0;
-    for (int i = 0; i < t->ndim; ++i) last += (t->shape[i] - 1) * t->stride[i];
-    *e = *b + (uintptr_t)((last + 1) * bytes_of(t->dtype));
-  }
-  void apart(const bi_tensor* out, const bi_tensor* in, const char* what) {
-    if (!ok() || !out || !in || empty(out) || empty(in)) return;
-    uintptr_t a0, a1, b0, b1;
-    range(out, &a0, &a1);
-    range(in, &b0, &b1);
-    if (a1 <= b0 || b1 <= a0) return;
-    that(interleaved(out, in), BI_ERR_INVALID_ARG, "an output overlaps another operand", what);
-  }
-  // Views of one buffer that interleave without touching (q, k and v of one
-  // projection; keys and values of one cache tensor): with some period s,
-  // each view's dimensions either lie within one period or step by whole
-  // periods, and the parts of the period they take are apart.
-  static bool interleaved(const bi_tensor* x, const bi_tensor* y) {
-    const int64_t es = bytes_of(x->dtype);
-    const int64_t d = reinterpret_cast<intptr_t>(y->ptr) - reinterpret_cast<intptr_t>(x->ptr);
-    if (es != bytes_of(y->dtype) || d % es != 0) return false;
-    for (int i = 0; i < x->ndim; ++i) {
-      const int64_t s = x->stride[i];
-      if (x->shape[i] < 2 || s < 1) continue;
-      const int64_t xs = within(x, s), ys = within(y, s);
-      if (xs <= 0 || ys <= 0) continue;
-      const int64_t off = ((d / es) % s + s) % s;  // y starts this far into x's period
-      if (off >= xs && off + ys <= s) return true;
-    }
-    return false;
-  }
-  // Elements that t spans inside a period of s; 0 when a dimension fits neither way.
-  static int64_t within(const bi_tensor* t, int64_t s) {
-    int64_t span = 1;
-    for (int i = 0; i < t->ndim; ++i) {
-      if (t->shape[i] < 2 || t->stride[i] % s == 0) continue;
-      if (t->stride[i] > s) return 0;
-      span += (t->shape[i] - 1) * t->stride[i];
-    }
-    return span <= s ? span : 0;
-  }
-};
-
-constexpr int64_t kMaxRequests = 1 << 22;  // of a plan and an attention call
-constexpr int64_t kMaxHeads = 1 << 30;     // head numbers of a token, and steps past them, fit 32 bits
-
-int64_t stride_or(const bi_tensor* t, int d, int64_t alone) { return t->shape[d] > 1 ? t->stride[d] : alone; }
-
-}  // namespace
-}  // namespace bi
 
 using namespace bi;
 
@@ -265,18 +130,6 @@ bi_status rope_config_ok(const bi_rope_config* cfg, std::string* why) {
     return BI_ERR_INVALID_ARG;
   }
   return BI_OK;
-}
-
-// Row and head strides (those that are walked) in whole 16-byte units.
-bool rows_on_16(const bi_tensor* t) {
-  const int e = bytes_of(t->dtype);
-  for (int i = 0; i + 1 < t->ndim; ++i)
-    if (t->shape[i] > 1 && (t->stride[i] * e) % 16 != 0) return false;
-  return on(t->ptr, 16);
-}
-
-bool same_view(const bi_tensor* a, const bi_tensor* b) {
-  return a->ptr == b->ptr && a->dtype == b->dtype && a->stride[0] == b->stride[0] && a->stride[1] == b->stride[1];
 }
 
 void positions_into(RopeParams* p, const bi_tensor* positions) {
@@ -406,10 +259,39 @@ extern "C" bi_status bi_rope(const bi_rope_config* config, const bi_tensor* x, c
   return abi_finish(c.st, c.why);
 }
 
-extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* positions,
-                                    const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
-                                    const bi_tensor* k, const bi_tensor* v, const bi_tensor* k_cache,
-                                    const bi_tensor* v_cache, bi_stream stream) {
+namespace {
+
+// The caches of a layer: two tensors [P, page_size, Hkv, D] of one type, and for
+// caches in 8 bits their scales [P, page_size, Hkv].
+struct Caches {
+  const bi_tensor *k, *v, *k_scales, *v_scales;
+  bool scaled;
+
+  void check(Check& c) const {
+    const Check::Kind kind = scaled ? Check::kE4m3 : Check::kFloat;
+    c.operand(k, "k_cache", 4, kind, true);
+    c.operand(v, "v_cache", 4, kind, true);
+    if (scaled) {
+      c.operand(k_scales, "k_scales", 3, Check::kScale, false);
+      c.operand(v_scales, "v_scales", 3, Check::kScale, false);
+    }
+    if (!c.ok()) return;
+    for (int i = 0; i < 4; ++i)
+      c.that(v->shape[i] == k->shape[i], BI_ERR_SHAPE_MISMATCH, "v_cache must have k_cache's shape");
+    for (int i = 0; scaled && i < 3; ++i)
+      c.that(k_scales->shape[i] == k->shape[i] && v_scales->shape[i] == k->shape[i], BI_ERR_SHAPE_MISMATCH,
+             "k_scales and v_scales must be [P, page_size, Hkv] as the caches");
+    c.that(v->dtype == k->dtype, BI_ERR_UNSUPPORTED_DTYPE, "k_cache and v_cache must have one type");
+  }
+  static PageView view(const bi_tensor* t) {
+    return {t->ptr, stride_or(t, 0, 0), stride_or(t, 1, 0), stride_or(t, 2, 0)};
+  }
+};
+
+bi_status store_impl(const bi_rope_config* config, const bi_tensor* positions, const bi_tensor* slots,
+                     const bi_tensor* q, const bi_tensor* q_out, const bi_tensor* k, const bi_tensor* v,
+                     const Caches& to, const char* name, bi_stream stream) {
+  const bi_tensor *k_cache = to.k, *v_cache = to.v;
   Check c;
   if (config) {
     c.st = rope_config_ok(config, &c.why);
@@ -421,8 +303,7 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
   c.that(!q == !q_out, BI_ERR_INVALID_ARG, "q and q_out are given together or not at all");
   c.tensor(k, "k", 3, false);
   c.tensor(v, "v", 3, false);
-  c.tensor(k_cache, "k_cache", 4, false);
-  c.tensor(v_cache, "v_cache", 4, false);
+  to.check(c);
   if (q) {
     c.tensor(q, "q", 3, false);
     c.tensor(q_out, "q_out", 3, false);
@@ -439,9 +320,6 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
   c.that(v->dtype == k->dtype, BI_ERR_UNSUPPORTED_DTYPE, "k and v must have one type");
   c.that(k_cache->shape[2] == H && k_cache->shape[3] == D, BI_ERR_SHAPE_MISMATCH,
          "the caches must be [P, page_size, Hkv, D] with k's Hkv and D");
-  for (int i = 0; i < 4; ++i)
-    c.that(v_cache->shape[i] == k_cache->shape[i], BI_ERR_SHAPE_MISMATCH, "v_cache must have k_cache's shape");
-  c.that(v_cache->dtype == k_cache->dtype, BI_ERR_UNSUPPORTED_DTYPE, "k_cache and v_cache must have one type");
   c.that(ps >= 1 && P * ps <= INT32_MAX, BI_ERR_INVALID_ARG, "page_size must be positive and P * page_size < 2^31");
   if (q) {
     c.that(q->shape[0] == T && q->shape[2] == D, BI_ERR_SHAPE_MISMATCH, "q must be [T, Hq, D] with k's T and D");
@@ -450,13 +328,14 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
   }
   if (!c.ok()) return abi_finish(c.st, c.why);
   const bi_tensor* in[5] = {k, v, slots, positions, q};
-  const bi_tensor* out[3] = {k_cache, v_cache, q_out};
-  for (int i = 0; i < 3; ++i) {
+  const bi_tensor* out[5] = {k_cache, v_cache, q_out, to.k_scales, to.v_scales};
+  const char* names[5] = {"k_cache", "v_cache", "q_out", "k_scales", "v_scales"};
+  for (int i = 0; i < 5; ++i) {
     if (!out[i]) continue;
-    c.distinct(out[i], i == 0 ? "k_cache" : i == 1 ? "v_cache" : "q_out");
+    c.distinct(out[i], names[i]);
     for (int j = 0; j < 5; ++j)
-      if (in[j] && !(i == 2 && j == 4 && same_view(q, q_out))) c.apart(out[i], in[j], "bi_paged_store");
-    for (int j = 0; j < i; ++j) c.apart(out[i], out[j], "bi_paged_store");
+      if (in[j] && !(i == 2 && j == 4 && same_view(q, q_out))) c.apart(out[i], in[j], name);
+    for (int j = 0; j < i; ++j) c.apart(out[i], out[j], name);
   }
   const int64_t Hq = q ? q->shape[1] : 0;
   c.that(Hq + 2 * H <= kMaxHeads, BI_ERR_INVALID_ARG, "too many heads");
@@ -474,15 +353,79 @@ extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tenso
   }
   p.k = {k->ptr, stride_or(k, 0, 0), stride_or(k, 1, 0)};
   p.v = {v->ptr, stride_or(v, 0, 0), stride_or(v, 1, 0)};
-  p.kc = {k_cache->ptr, stride_or(k_cache, 0, 0), stride_or(k_cache, 1, 0), stride_or(k_cache, 2, 0)};
-  p.vc = {v_cache->ptr, stride_or(v_cache, 0, 0), stride_or(v_cache, 1, 0), stride_or(v_cache, 2, 0)};
+  p.kc = Caches::view(k_cache), p.vc = Caches::view(v_cache);
+  if (to.scaled) p.ks = Caches::view(to.k_scales), p.vs = Caches::view(to.v_scales);
   p.slots = static_cast<const int64_t*>(slots->ptr);
   p.num_slots = P * ps;
   p.hq = (int32_t)Hq, p.hkv = (int32_t)H, p.D = (int32_t)D, p.ps = (int32_t)ps;
   p.kv_kind = kind_of(k->dtype), p.c_kind = kind_of(k_cache->dtype);
   p.vec = units_fit(p) && rows_on_16(k) && rows_on_16(v) && rows_on_16(k_cache) && rows_on_16(v_cache) &&
           (!q || (rows_on_16(q) && rows_on_16(q_out)));
+  // a scale is found by the lanes that hold a head: a whole, aligned group of one warp's
+  if (to.scaled) p.vec = p.vec && D <= 512 && (D & (D - 1)) == 0;
   c.st = run_rope(p, T, stream, &c.why);
+  return abi_finish(c.st, c.why);
+}
+
+}  // namespace
+
+extern "C" bi_status bi_paged_store(const bi_rope_config* config, const bi_tensor* positions,
+                                    const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
+                                    const bi_tensor* k, const bi_tensor* v, const bi_tensor* k_cache,
+                                    const bi_tensor* v_cache, bi_stream stream) {
+  return store_impl(config, positions, slots, q, q_out, k, v, {k_cache, v_cache, nullptr, nullptr, false},
+                    "bi_paged_store", stream);
+}
+
+extern "C" bi_status bi_paged_store_quantized(const bi_rope_config* config, const bi_tensor* positions,
+                                              const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,
+                                              const bi_tensor* k, const bi_tensor* v, const bi_tensor* k_cache,
+                                              const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                              const bi_tensor* v_scales, bi_stream stream) {
+  return store_impl(config, positions, slots, q, q_out, k, v, {k_cache, v_cache, k_scales, v_scales, true},
+                    "bi_paged_store_quantized", stream);
+}
+
+extern "C" bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_tensor* k_cache,
+                                             const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                             const bi_tensor* v_scales, const bi_tensor* k, const bi_tensor* v,
+                                             bi_stream stream) {
+  const Caches from = {k_cache, v_cache, k_scales, v_scales, true};
+  Check c;
+  from.check(c);
+  c.tensor(k, "k", 3, false);
+  c.tensor(v, "v", 3, false);
+  if (!c.ok()) return abi_finish(c.st, c.why);
+  const int64_t T = k->shape[0], H = k->shape[1], D = k->shape[2], P = k_cache->shape[0], ps = k_cache->shape[1];
+  c.vec(slots, "slots", T, BI_I64);
+  c.that(D >= 1 && D <= 1024, BI_ERR_INVALID_ARG, "the head dimension must be within [1, 1024]");
+  c.that(v->shape[0] == T && v->shape[1] == H && v->shape[2] == D, BI_ERR_SHAPE_MISMATCH, "v must have k's shape");
+  c.that(v->dtype == k->dtype, BI_ERR_UNSUPPORTED_DTYPE, "k and v must have one type");
+  c.that(k_cache->shape[2] == H && k_cache->shape[3] == D, BI_ERR_SHAPE_MISMATCH,
+         "the caches must be [P, page_size, Hkv, D] with k's Hkv and D");
+  c.that(ps >= 1 && P * ps <= INT32_MAX, BI_ERR_INVALID_ARG, "page_size must be positive and P * page_size < 2^31");
+  c.that(H <= kMaxHeads && (double)T * H * D <= 5e11, BI_ERR_INVALID_ARG, "too many elements");
+  if (!c.ok()) return abi_finish(c.st, c.why);
+  const bi_tensor* in[5] = {slots, k_cache, k_scales, v_cache, v_scales};
+  c.distinct(k, "k");
+  c.distinct(v, "v");
+  for (int j = 0; j < 5; ++j) {
+    c.apart(k, in[j], "bi_paged_load_quantized");
+    c.apart(v, in[j], "bi_paged_load_quantized");
+  }
+  c.apart(k, v, "bi_paged_load_quantized");
+  if (!c.ok() || T == 0 || H == 0) return abi_finish(c.st, c.why);
+  LoadParams p;
+  memset(&p, 0, sizeof(p));
+  p.kc = Caches::view(k_cache), p.vc = Caches::view(v_cache);
+  p.ks = Caches::view(k_scales), p.vs = Caches::view(v_scales);
+  p.k = k->ptr, p.k_t = stride_or(k, 0, 0), p.k_h = stride_or(k, 1, 0);
+  p.v = v->ptr, p.v_t = stride_or(v, 0, 0), p.v_h = stride_or(v, 1, 0);
+  p.slots = static_cast<const int64_t*>(slots->ptr);
+  p.num_slots = P * ps;
+  p.T = (int32_t)T, p.H = (int32_t)H, p.D = (int32_t)D, p.ps = (int32_t)ps, p.kind = kind_of(k->dtype);
+  p.vec = D % 16 == 0 && rows_on_16(k) && rows_on_16(v) && rows_on_16(k_cache) && rows_on_16(v_cache);
+  c.st = launch_paged_load(p, (cudaStream_t)stream, &c.why);
   return abi_finish(c.st, c.why);
 }
 
@@ -497,14 +440,15 @@ extern "C" int64_t bi_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int
   return rows > INT64_MAX / (n * (D + 2) * 4) ? INT64_MAX : rows * n * (D + 2) * 4;
 }
 
-extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const bi_tensor* v_cache,
-                                        const bi_tensor* page_table, const bi_tensor* seq_lens, float scale,
-                                        const bi_tensor* o, void* workspace, int64_t workspace_bytes,
-                                        bi_stream stream) {
+namespace {
+
+bi_status attention_impl(const bi_tensor* q, const Caches& caches, const bi_tensor* page_table,
+                         const bi_tensor* seq_lens, float scale, const bi_tensor* o, void* workspace,
+                         int64_t workspace_bytes, const char* name, bi_stream stream) {
+  const bi_tensor *k_cache = caches.k, *v_cache = caches.v;
   Check c;
   c.tensor(q, "q", 3, false);
-  c.tensor(k_cache, "k_cache", 4, false);
-  c.tensor(v_cache, "v_cache", 4, false);
+  caches.check(c);
   c.tensor(page_table, "page_table", 2, true);
   c.tensor(o, "o", 3, false);
   if (!c.ok()) return abi_finish(c.st, c.why);
@@ -514,12 +458,9 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   c.that(page_table->shape[0] == B, BI_ERR_SHAPE_MISMATCH, "page_table must be [B, W] with q's B");
   c.vec(seq_lens, "seq_lens", B, BI_I32);
   c.that(k_cache->shape[3] == D, BI_ERR_SHAPE_MISMATCH, "the caches must be [P, page_size, Hkv, D] with q's D");
-  for (int i = 0; i < 4; ++i)
-    c.that(v_cache->shape[i] == k_cache->shape[i], BI_ERR_SHAPE_MISMATCH, "v_cache must have k_cache's shape");
   c.that(o->shape[0] == B && o->shape[1] == Hq && o->shape[2] == D, BI_ERR_SHAPE_MISMATCH, "o must have q's shape");
   c.that(q->dtype == BI_BF16 || q->dtype == BI_F16, BI_ERR_UNSUPPORTED_DTYPE, "q must be bf16 or fp16");
-  c.that(k_cache->dtype == q->dtype && v_cache->dtype == q->dtype, BI_ERR_UNSUPPORTED_DTYPE,
-         "the caches must have q's type");
+  c.that(caches.scaled || k_cache->dtype == q->dtype, BI_ERR_UNSUPPORTED_DTYPE, "the caches must have q's type");
   c.that(attention_head_dim_ok(D), BI_ERR_INVALID_ARG, "head dimension must be 64, 128 or 256");
   const float score_log2 = (float)((double)scale * 1.4426950408889634);
   c.that(std::isfinite(score_log2), BI_ERR_INVALID_ARG, "scale and scale * log2(e) must be finite");
@@ -533,9 +474,9 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   for (int i = 0; i < 4; ++i)
     c.that(Check::empty(ts[i]) || rows_on_16(ts[i]), BI_ERR_UNSUPPORTED_LAYOUT,
            "base pointers and strides of q, the caches and o must be multiples of 16 bytes");
-  const bi_tensor* in[5] = {q, k_cache, v_cache, page_table, seq_lens};
+  const bi_tensor* in[7] = {q, k_cache, v_cache, page_table, seq_lens, caches.k_scales, caches.v_scales};
   c.distinct(o, "o");
-  for (int i = 0; i < 5; ++i) c.apart(o, in[i], "bi_paged_attention");
+  for (int i = 0; i < 7; ++i) c.apart(o, in[i], name);
   if (!c.ok() || B == 0 || Hq == 0) return abi_finish(c.st, c.why);
   const int64_t cap = W * ps, need = bi_paged_attention_workspace_bytes(B, Hq, D, cap);
   c.that(B * Hq * (D / 64) <= INT32_MAX && B <= kMaxRequests, BI_ERR_INVALID_ARG, "too many requests");
@@ -548,8 +489,8 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
     bi_tensor ws;
     memset(&ws, 0, sizeof(ws));
     ws.ptr = workspace, ws.ndim = 1, ws.dtype = BI_F32, ws.shape[0] = need / 4, ws.stride[0] = 1;
-    for (int i = 0; i < 5; ++i) c.apart(&ws, in[i], "bi_paged_attention: workspace");
-    c.apart(&ws, o, "bi_paged_attention: workspace");
+    for (int i = 0; i < 7; ++i) c.apart(&ws, in[i], "workspace");
+    c.apart(&ws, o, "workspace");
     if (!c.ok()) return abi_finish(c.st, c.why);
   }
   PagedAttnParams p;
@@ -571,11 +512,35 @@ extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_c
   p.W = (int32_t)W, p.ps = (int32_t)ps, p.P = (int32_t)P, p.cap = (int32_t)cap;
   p.group = (int32_t)(Hq / Hkv);
   p.ps_shift = (ps & (ps - 1)) == 0 ? __builtin_ctzll((unsigned long long)ps) : -1;
+  if (caches.scaled) {
+    p.ks = Caches::view(caches.k_scales), p.vs = Caches::view(caches.v_scales);
+    if (P * ps == 0) p.ks.ptr = p.vs.ptr = seq_lens->ptr;
+  }
+  p.e4m3 = caches.scaled;
   p.in_f16 = q->dtype == BI_F16;
   p.out_kind = kind_of(o->dtype);
   p.score_log2 = score_log2;
   c.st = launch_paged_attention(p, (cudaStream_t)stream, &c.why);
   return abi_finish(c.st, c.why);
+}
+
+}  // namespace
+
+extern "C" bi_status bi_paged_attention(const bi_tensor* q, const bi_tensor* k_cache, const bi_tensor* v_cache,
+                                        const bi_tensor* page_table, const bi_tensor* seq_lens, float scale,
+                                        const bi_tensor* o, void* workspace, int64_t workspace_bytes,
+                                        bi_stream stream) {
+  return attention_impl(q, {k_cache, v_cache, nullptr, nullptr, false}, page_table, seq_lens, scale, o, workspace,
+                        workspace_bytes, "bi_paged_attention", stream);
+}
+
+extern "C" bi_status bi_paged_attention_quantized(const bi_tensor* q, const bi_tensor* k_cache,
+                                                  const bi_tensor* k_scales, const bi_tensor* v_cache,
+                                                  const bi_tensor* v_scales, const bi_tensor* page_table,
+                                                  const bi_tensor* seq_lens, float scale, const bi_tensor* o,
+                                                  void* workspace, int64_t workspace_bytes, bi_stream stream) {
+  return attention_impl(q, {k_cache, v_cache, k_scales, v_scales, true}, page_table, seq_lens, scale, o, workspace,
+                        workspace_bytes, "bi_paged_attention_quantized", stream);
 }
 
 // ---------------------------------------------------------------------------
