@@ -2,30 +2,35 @@
 // 128 of the reduction:
 //   c[m,n] = sum_kb sa[m,kb] sb[kb,n/128] sum_{k in block kb} a[m,k] b[k,n]  (+ bias[n]).
 //
-// The scales change every 128 steps of K, so a tensor-core accumulator can run
-// over one block only; what the blocks leave is scaled and summed in registers:
-//   D = sum of the block's products (four tcgen05.mma steps of K = 32, fp32 in
-//       TMEM, the first one overwriting),
-//   acc = fma(D, RN(sa sb), acc), block after block, from zero.
-// One order for every element, whatever the tile it is computed in.
+// The scales are powers of two, so the tensor core can apply them as it
+// multiplies (tcgen05.mma, kind::mxf8f6f4, one 8-bit exponent for each row and 32
+// steps of K, here the same for the four steps of a block): accumulators run on
+// over blocks.  (With scales applied to each block's accumulator in registers,
+// 128 x 128 fp32 of TMEM a warp to read, scale and add every 512 cycles of MMAs,
+// the 8192 x 4096 x 14336 product took 554 us: bound by the latency of that
+// chain, 1400 cycles a block.)
+//   D = the products of a segment of 16 blocks (K = 2048), 64 steps of K = 32 in
+//       ascending order, fp32 in TMEM, the first one overwriting;
+//   acc = the segments' sums, added in order in fp32.
+// One order for every element, whatever the tile it is computed in.  Segments
+// bound how long a sum stays in the tensor core, whose adds may truncate.
 //
 // Pairs of CTAs (cta_group::2), tiles of 256 rows x BN columns:
 //   warp 0       producer: A (128 x 128 bytes) and this CTA's half of B's
-//                columns of each K block by TMA into a ring of stages (128-byte
+//                columns of two K blocks a stage by TMA into a ring (128-byte
 //                swizzle), as in the 16-bit product
-//   warp 1       TMEM allocation; in the even CTA the issuer of the MMAs, a
-//                K block to one of the ACC = 512 / BN accumulators, in turn
-//   warps 4-11   the sums: warp w has rows 32 (w % 4) .. + 31 and half of the
-//                tile's columns, BN / 2 fp32 registers a thread.  It reads a
-//                block's accumulator, frees it for the issuer at once and adds;
-//                after the last block bias, rounding and the store.
-// A block's MMAs take 4 x 128 cycles of a pair at BN = 256; reading 128 x 256
-// fp32 of TMEM a SM takes half of that, the sums (two a fused multiply-add
-// instruction) a quarter, so the tensor cores set the pace.
+//   warp 1       TMEM allocation; in the even CTA the issuer of the MMAs
+//   warps 4-7    scales: each loads 32 rows' of four blocks ahead, turns them
+//                into exponents and writes them to the stage's columns of TMEM,
+//                once for each quadrant of lanes, which is a warp's.  Their
+//                arrivals count on the stage's barrier beside the copies' bytes.
+//   warps 8-15   sums: a warp has 32 rows and half of the tile's columns, BN / 2
+//                fp32 registers a thread; it adds a segment's accumulator and
+//                frees it (there are two), then bias, rounding and the store.
 //
-// At decode sizes the weight's bytes do: BN is then narrower, so that there are
-// pairs enough, and the A stages of at most 32 rows leave room for more of B in
-// flight (the tensor core reads 128 rows either way; rows past M are never
+// At decode sizes the weight's bytes set the pace: BN is then narrower, so that
+// there are pairs enough, and A stages of at most 32 rows leave room for more of
+// B in flight (the tensor core reads 128 rows either way; rows past M are never
 // stored).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -41,10 +46,11 @@ namespace {
 
 constexpr int kBK8 = 128;     // K of a block and a stage: one 128-byte swizzle row
 constexpr int kUmmaK8 = 32;   // K of a tcgen05.mma of 8-bit operands
-constexpr int kThreads = 384;
-constexpr int kSumWarps = 8;
-constexpr int kGroup = 4;  // K blocks whose scales a thread holds
-constexpr uint32_t kSumRegs = 232, kOtherRegs = 40;  // 256 x 232 + 128 x 40 = 384 x 168
+constexpr int kStageBlocks = 2;      // K blocks of a stage
+constexpr int kSegmentStages = 8;    // stages of a segment: K = 2048
+constexpr int kThreads = 512;
+constexpr int kScaleWarps = 4, kSumWarps = 8, kParts = 2;
+constexpr int kScaleGroup = 4;       // K blocks whose scales are loaded at once
 
 struct ScaledParams {
   CUtensorMap tma_a;  // [M][K] bytes, box {128, 128 (32 for M <= 32)}
@@ -60,54 +66,72 @@ struct ScaledParams {
 
 template <int BN, int A_ROWS>
 struct Layout8 {
-  static constexpr int A_BYTES = A_ROWS * kBK8;
-  static constexpr int B_BYTES = BN / 2 * kBK8;  // this CTA's half of the tile's columns
-  static constexpr int ACC = 512 / BN > 8 ? 8 : 512 / BN;
+  static constexpr int PART = BN / kParts;  // columns of a sum warp
+  static constexpr int A_BYTES = A_ROWS * kBK8;          // a block
+  static constexpr int B_BYTES = BN / 2 * kBK8;          // this CTA's half of the tile's columns
+  static constexpr int STAGE_BYTES = kStageBlocks * (A_BYTES + B_BYTES);
+  static constexpr int ACC = 2;
+  // exponents of a block in TMEM, a 32-bit column for each 32 rows of A and of B
+  static constexpr int SFA_COLS = 4, SFB_COLS = BN > 128 ? 8 : 4, SF_COLS = SFA_COLS + SFB_COLS;
   static constexpr int BAR_BYTES = 1024;
-  static constexpr int STAGING_BYTES = A_ROWS == kBM ? kSumWarps * 2 * kStageOutBytes : 0;
+  static constexpr int EXCHANGE_BYTES = 2 * kBM * 4;  // exponents on their way between the scale warps
+  static constexpr int STAGING_BYTES = A_ROWS == kBM ? kSumWarps * kStageOutBytes : 0;
   static constexpr int MAX_DYN = 232448;
-  static constexpr int FIT = (MAX_DYN - 1024 - BAR_BYTES - STAGING_BYTES) / (A_BYTES + B_BYTES);
-  static constexpr int STAGES = FIT > 24 ? 24 : FIT;
-  static constexpr int DYN_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + BAR_BYTES + STAGING_BYTES;
-  // the tensor core reads up to 128 A rows from a stage's base
-  static constexpr int A_OVERREAD = (kBM - A_ROWS) * kBK8;
+  static constexpr int FIT = (MAX_DYN - 1024 - BAR_BYTES - EXCHANGE_BYTES - STAGING_BYTES) / STAGE_BYTES;
+  static constexpr int ROOM = (512 - ACC * BN) / (kStageBlocks * SF_COLS);  // stages whose exponents fit TMEM
+  static constexpr int STAGES = FIT < ROOM ? FIT : ROOM;
+  static constexpr int DYN_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + EXCHANGE_BYTES + STAGING_BYTES;
+  static constexpr int A_OVERREAD = (kBM - A_ROWS) * kBK8;  // the tensor core reads 128 A rows from a block's base
   static_assert(STAGES >= 3, "pipeline depth");
+  static_assert(ACC * BN + STAGES * kStageBlocks * SF_COLS <= 512, "accumulators and exponents fit TMEM");
   static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 8 <= BAR_BYTES, "barriers fit their block");
-  static_assert(A_OVERREAD <= STAGES * B_BYTES, "A over-read stays inside the B stages");
+  static_assert(A_OVERREAD <= STAGES * kStageBlocks * B_BYTES, "A over-read stays inside the B stages");
   static_assert(DYN_BYTES > 116 * 1024, "one CTA per SM: TMEM is allocated whole");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "stages hold whole swizzle atoms");
 };
 
-// CTA pair, kind::f8f6f4: as umma_bf16_pair with 8-bit operands.
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t tmem_d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// CTA pair, kind::mxf8f6f4: D (+)= (A 2^(ea - 127)) (B 2^(eb - 127)), as umma_bf16_pair; the exponents
+// of A's rows in each CTA's TMEM, of all of B's columns in both.
+__device__ __forceinline__ void umma_mx_pair(uint32_t tmem_d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t tmem_sfa, uint32_t tmem_sfb, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          tmem_d),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(tmem_sfa), "r"(tmem_sfb), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B e4m3 (0), both K-major.
-constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
+// Instruction descriptor of it: e4m3 A and B (0), both K-major, exponents as UE8M0 (bit 23), in byte 0 of their words.
+constexpr uint32_t idesc_mx(uint32_t m, uint32_t n) { return ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24); }
 
-// (d0, d1) * s + (a0, a1), two fused multiply-adds of one instruction.
-__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t d0, uint32_t d1, float s) {
-  asm("{\n\t.reg .b64 d, s, a;\n\t"
-      "mov.b64 d, {%2, %3};\n\t"
-      "mov.b64 s, {%4, %4};\n\t"
-      "mov.b64 a, {%0, %1};\n\t"
-      "fma.rn.f32x2 a, d, s, a;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "r"(d0), "r"(d1), "f"(s));
+__device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// One lane of a converged warp, known as such to the compiler: a branch on lane ==
+// 0 makes it move every descriptor through per-thread code (four MMAs 280 cycles
+// to issue, this way 65).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The exponent byte of a scale 2^(e - 127); anything else is a NaN to the tensor core.
+__device__ __forceinline__ uint32_t exponent_byte(float scale) {
+  const uint32_t b = __float_as_uint(scale);
+  return (b & 0x807fffffu) == 0 && b != 0 ? b >> 23 : 255u;
 }
 
 template <int BN, int A_ROWS, bool STREAM_B>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     scaled_gemm_kernel(const __grid_constant__ ScaledParams p) {
   using Lay = Layout8<BN, A_ROWS>;
-  constexpr int HALF = BN / 2, ACC = Lay::ACC;
+  constexpr int PART = Lay::PART, ACC = Lay::ACC;
   constexpr uint16_t kBoth = 3;
   const uint32_t crank = cluster_ctarank();
   const int stride = gridDim.x >> 1, first_tile = blockIdx.x >> 1;
@@ -115,27 +139,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  const uint32_t sA = base, sB = base + Lay::STAGES * Lay::A_BYTES;
-  const uint32_t staging0 = sB + Lay::STAGES * Lay::B_BYTES;
-  const uint32_t bar0 = staging0 + Lay::STAGING_BYTES;
+  const uint32_t sA = base, sB = base + Lay::STAGES * kStageBlocks * Lay::A_BYTES;
+  const uint32_t staging0 = sB + Lay::STAGES * kStageBlocks * Lay::B_BYTES;
+  uint32_t* exchange = reinterpret_cast<uint32_t*>(smem + (staging0 + Lay::STAGING_BYTES - base));
   PipeBars bars;
-  bars.full0 = bar0;
-  bars.empty0 = bar0 + 8 * Lay::STAGES;
+  bars.full0 = staging0 + Lay::STAGING_BYTES + Lay::EXCHANGE_BYTES;
+  bars.empty0 = bars.full0 + 8 * Lay::STAGES;
   bars.tfull0 = bars.empty0 + 8 * Lay::STAGES;
   bars.tempty0 = bars.tfull0 + 8 * ACC;
   bars.drain = bars.tempty0 + 8 * ACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars.drain + 8 - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = (p.k_blocks + kStageBlocks - 1) / kStageBlocks;  // of a tile
 
   if (threadIdx.x == 0) {
+    // Even CTA: a stage is full when the copies of both CTAs have landed and the
+    // scale warps of both have written; an accumulator is free when the sum warps
+    // of both have read it.
     for (int s = 0; s < Lay::STAGES; ++s) {
-      mbar_init(bars.full(s), 1);
+      mbar_init(bars.full(s), 1 + 2 * kScaleWarps);
       mbar_init(bars.empty(s), 1);
     }
     for (int b = 0; b < ACC; ++b) {
       mbar_init(bars.tfull(b), 1);
-      mbar_init(bars.tempty(b), 2 * kSumWarps);  // the sum warps of both CTAs
+      mbar_init(bars.tempty(b), 2 * kSumWarps);
     }
     mbar_init(bars.drain, 1);
     *abort_flag = 0;
@@ -151,21 +179,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
+  const uint32_t sf_base = tmem_base + ACC * BN;  // exponents of stage s: sf_base + s * kStageBlocks * SF_COLS
   cluster_arrive_relaxed();
   cluster_wait();  // both CTAs' barriers are initialised
   const WaitCtl wc{abort_flag, p.status_word, p.wait_limit_ns};
 
-  if (warp < 4) {
-    setmaxnreg_dec<kOtherRegs>();
-    if (warp == 0 && lane == 0) {
+  if (warp < 8) {
+    setmaxnreg_dec<72>();
+    if (warp == 0 && elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
         const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
         const int mb = 2 * tc.mb + (int)crank;
         const bool a_live = mb * kBM < p.M, peer_live = (mb + 1) * kBM < p.M;  // (peer_live: even CTA)
-        const int n0 = tc.nb * BN + (int)crank * HALF;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+        const int n0 = tc.nb * BN + (int)crank * (BN / 2);
+        for (int st = 0; st < stages; ++st, ++it) {
           const uint32_t s = it % Lay::STAGES, r = it / Lay::STAGES;
           if (r > 0 && !mbar_wait_bounded(bars.empty(s), (r - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                           status_code(6, kSiteProducerEmpty))) {
@@ -173,15 +202,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           if (crank == 0)
-            mbar_arrive_expect_tx(bars.full(s), 2 * Lay::B_BYTES + Lay::A_BYTES * (peer_live ? 2 : 1));
+            mbar_arrive_expect_tx(bars.full(s), kStageBlocks * (2 * Lay::B_BYTES + Lay::A_BYTES * (peer_live ? 2 : 1)));
           const uint32_t fb = cluster_map_shared(bars.full(s), 0);
-          if (STREAM_B) {  // B is used by one or two pairs, A by every column tile
-            tma_load_3d_pair_hint(sB + s * Lay::B_BYTES, &p.tma_b, fb, kb * kBK8, n0, 0, l2_policy_evict_first());
-            if (a_live)
-              tma_load_3d_pair_hint(sA + s * Lay::A_BYTES, &p.tma_a, fb, kb * kBK8, mb * kBM, 0, l2_policy_evict_last());
-          } else {
-            tma_load_3d_pair(sB + s * Lay::B_BYTES, &p.tma_b, fb, kb * kBK8, n0, 0);
-            if (a_live) tma_load_3d_pair(sA + s * Lay::A_BYTES, &p.tma_a, fb, kb * kBK8, mb * kBM, 0);
+#pragma unroll
+          for (int j = 0; j < kStageBlocks; ++j) {  // (a block past K is all zeros)
+            const int k = (st * kStageBlocks + j) * kBK8;
+            const uint32_t at = s * kStageBlocks + j;
+            if (STREAM_B) {  // B is used by one or two pairs, A by every column tile
+              tma_load_3d_pair_hint(sB + at * Lay::B_BYTES, &p.tma_b, fb, k, n0, 0, l2_policy_evict_first());
+              if (a_live)
+                tma_load_3d_pair_hint(sA + at * Lay::A_BYTES, &p.tma_a, fb, k, mb * kBM, 0, l2_policy_evict_last());
+            } else {
+              tma_load_3d_pair(sB + at * Lay::B_BYTES, &p.tma_b, fb, k, n0, 0);
+              if (a_live) tma_load_3d_pair(sA + at * Lay::A_BYTES, &p.tma_a, fb, k, mb * kBM, 0);
+            }
           }
         }
       }
@@ -191,15 +225,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(bars.empty(j % Lay::STAGES), (j / Lay::STAGES) & 1, nullptr, wc.status_word, wc.limit_ns,
                                status_code(6, kSiteDrain)))
           break;
-    } else if (warp == 1 && lane == 0 && crank == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3(2 * kBM, BN);
-      uint32_t it = 0;
+    } else if (warp == 1 && crank == 0 && elect_one()) {
+      constexpr uint32_t kIdesc = idesc_mx(2 * kBM, BN);
+      uint32_t it = 0, seg = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const uint32_t buf = it % ACC, use = it / ACC, s = it % Lay::STAGES;
-          if (use > 0 && !mbar_wait_bounded<true>(bars.tempty(buf), (use - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
-                                                  status_code(6, kSiteMmaTmemEmpty))) {
+        for (int st = 0; st < stages; ++st, ++it) {
+          const bool opens = st % kSegmentStages == 0;
+          const uint32_t buf = seg % ACC, use = seg / ACC, s = it % Lay::STAGES;
+          if (opens && use > 0 &&
+              !mbar_wait_bounded<true>(bars.tempty(buf), (use - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
+                                       status_code(6, kSiteMmaTmemEmpty))) {
             ok = false;
             break;
           }
@@ -209,109 +245,174 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = sA + s * Lay::A_BYTES, b = sB + s * Lay::B_BYTES;
 #pragma unroll
-          for (int k = 0; k < kBK8 / kUmmaK8; ++k)
-            umma_e4m3_pair(tmem_base + buf * BN, smem_desc_sw128(a + k * 32, 16, 1024),
-                           smem_desc_sw128(b + k * 32, 16, 1024), kIdesc, k != 0 ? 1u : 0u);
+          for (int j = 0; j < kStageBlocks; ++j) {
+            const uint32_t at = s * kStageBlocks + j;
+            const uint64_t a = smem_desc_sw128(sA + at * Lay::A_BYTES, 16, 1024);
+            const uint64_t b = smem_desc_sw128(sB + at * Lay::B_BYTES, 16, 1024);
+            const uint32_t sf = sf_base + at * Lay::SF_COLS;
+#pragma unroll
+            for (int k = 0; k < kBK8 / kUmmaK8; ++k)  // (the address is the low bits, in 16-byte units)
+              umma_mx_pair(tmem_base + buf * BN, a + 2 * k, b + 2 * k, kIdesc, sf, sf + Lay::SFA_COLS,
+                           opens && j == 0 && k == 0 ? 0u : 1u);
+          }
           umma_commit_pair(bars.empty(s), kBoth);
-          umma_commit_pair(bars.tfull(buf), kBoth);
+          if (st % kSegmentStages == kSegmentStages - 1 || st + 1 == stages) {
+            umma_commit_pair(bars.tfull(buf), kBoth);
+            ++seg;
+          }
         }
       }
       umma_commit_pair(bars.drain, 1);
       mbar_wait_bounded(bars.drain, 0, nullptr, wc.status_word, wc.limit_ns, status_code(6, kSiteDrain));
-    }
-    __syncwarp();
-  } else {
-    setmaxnreg_inc<kSumRegs>();
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    OutDesc o = p.out;
-    o.tma_c = (Lay::STAGING_BYTES > 0 && p.use_tma_store) ? &p.tma_c : nullptr;
-    const uint32_t staging = staging0 + (warp - 4) * 2 * kStageOutBytes;
-    uint32_t it = 0, chunk = 0;
-    bool ok = true;
-    for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
-      TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
-      tc.mb = 2 * tc.mb + (int)crank;
-      tc.nb = 2 * tc.nb + half;  // in units of HALF columns
-      const int m0 = tc.mb * kBM + q * 32, n0 = tc.nb * HALF;
-      const int n_left = p.N - n0;
-      const bool live = m0 < p.M && n_left > 0;  // any output here
-      TileBias<HALF> tb;
-      if (live) load_tile_bias<HALF>(o, 0, m0 + lane, n0, lane, tb);
-      const float* sa = p.sa + (int64_t)min(m0 + lane, p.M - 1) * p.sa_m;
-      const float* sb = p.sb + (int64_t)(min(n0, p.N - 1) / 128) * p.sb_n;
-      // The scales of kGroup blocks are loaded while the group before is summed: a
-      // product with one just requested would hold the warp for its latency.
-      float sa_next[kGroup], sb_next[kGroup];
-      auto request_scales = [&](int kb0) {
+    } else if (warp >= 4) {
+      const int q = warp - 4;
+      uint32_t it = 0, turn = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
+        const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
+        const int m0 = (2 * tc.mb + (int)crank) * kBM, n0 = tc.nb * BN;
+        // A: this lane's row, 32 q + lane; B: lanes 0-3 of the tile's first column block, lanes 4-7 of its second
+        const float* sa = p.sa + (int64_t)min(m0 + 32 * q + lane, p.M - 1) * p.sa_m;
+        const float* sb = p.sb + (int64_t)min(n0 / 128 + ((lane >> 2) & 1), (p.N - 1) / 128) * p.sb_n;
+        float a[kScaleGroup], b;
+        auto request = [&](int kb0) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          const bool there = live && kb0 + j < p.k_blocks;
-          sa_next[j] = there ? __ldg(sa + (kb0 + j) * p.sa_k) : 0.0f;
-          sb_next[j] = there ? __ldg(sb + (kb0 + j) * p.sb_k) : 0.0f;
-        }
-      };
-      request_scales(0);
-      float acc[HALF];
+          for (int j = 0; j < kScaleGroup; ++j) a[j] = kb0 + j < p.k_blocks ? __ldg(sa + (kb0 + j) * p.sa_k) : 1.0f;
+          const int kb = kb0 + (lane & 3);
+          b = kb < p.k_blocks ? __ldg(sb + kb * p.sb_k) : 1.0f;
+        };
+        request(0);
+        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kScaleGroup, ++turn) {
+          const uint32_t mine = exponent_byte(a[0]) | exponent_byte(a[1]) << 8 | exponent_byte(a[2]) << 16 | exponent_byte(a[3]) << 24;
+          const uint32_t col = exponent_byte(b);
+          request(kb0 + kScaleGroup);
+          uint32_t* x = exchange + (turn & 1) * kBM;  // (a warp is at most one turn ahead)
+          x[32 * q + lane] = mine;
+          ok = named_barrier_and(1, 32 * kScaleWarps, ok);  // all leave together
+          if (!ok) break;
+          uint32_t rows[4];
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
-      for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += kGroup) {
-        float scale[kGroup];
+          for (int c = 0; c < 4; ++c) rows[c] = x[32 * c + lane];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) scale[j] = __fmul_rn(sa_next[j], sb_next[j]);
-        request_scales(kb0 + kGroup);
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-          if (kb0 + g >= p.k_blocks) break;
-          const uint32_t buf = it % ACC, use = it / ACC;
-          const float s = scale[g];
-          ++it;
-          const bool got = mbar_wait_bounded(bars.tfull(buf), use & 1, wc.abort, wc.status_word, wc.limit_ns,
-                                             status_code(6, kSiteEpilogueTmemFull));
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t src = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + half * HALF;
-          uint32_t va[32], vb[32];
-          if (live) tmem_load_32cols(src, va);
-#pragma unroll
-          for (int j = 0; j < HALF / 32; ++j) {
-            uint32_t(&v)[32] = j & 1 ? vb : va;
-            uint32_t(&w)[32] = j & 1 ? va : vb;
-            if (live) {
-              tmem_load_wait(v);
-              if (j + 1 < HALF / 32) tmem_load_32cols(src + (j + 1) * 32, w);
+          for (int half = 0; half < kScaleGroup / kStageBlocks; ++half) {
+            if (kb0 + half * kStageBlocks >= p.k_blocks) break;
+            const uint32_t s = it % Lay::STAGES, r = it / Lay::STAGES;
+            ++it;
+            const bool got = r == 0 || mbar_wait_bounded(bars.empty(s), (r - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
+                                                         status_code(6, kSiteProducerEmpty));
+            if (!__all_sync(0xffffffffu, got)) {
+              ok = false;
+              break;
             }
-            if (j + 1 == HALF / 32) {  // all of it is in registers: the accumulator is free
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) {
-                if (crank != 0)
-                  mbar_arrive_remote(bars.tempty(buf), 0);
-                else
-                  mbar_arrive(bars.tempty(buf));
-              }
-            }
-            if (live) {
+            tc_fence_after_sync();
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) fma2(acc[32 * j + i], acc[32 * j + i + 1], v[i], v[i + 1], s);
+            for (int j = 0; j < kStageBlocks; ++j) {
+              const uint32_t pick = (half * kStageBlocks + j) * 0x1111u;  // a byte four times
+              const uint32_t at = sf_base + (s * kStageBlocks + j) * Lay::SF_COLS + ((uint32_t)(q * 32) << 16);
+              tmem_store_4cols(at, __byte_perm(rows[0], 0, pick), __byte_perm(rows[1], 0, pick),
+                               __byte_perm(rows[2], 0, pick), __byte_perm(rows[3], 0, pick));
+              // 32 columns of the tile lie in one block of 128
+              uint32_t w[8];
+#pragma unroll
+              for (int c = 0; c < Lay::SFB_COLS; ++c)
+                w[c] = __shfl_sync(0xffffffffu, col, ((n0 + 32 * c) / 128 - n0 / 128) % 2 * 4 + half * kStageBlocks + j) * 0x01010101u;
+              tmem_store_4cols(at + Lay::SFA_COLS, w[0], w[1], w[2], w[3]);
+              if (Lay::SFB_COLS > 4) tmem_store_4cols(at + Lay::SFA_COLS + 4, w[4], w[5], w[6], w[7]);
+            }
+            // (The stores to TMEM are complete by now; an arrival that also releases
+            // memory to the cluster would take a thousand cycles.)
+            tmem_store_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if (crank != 0)
+                mbar_arrive_remote(bars.full(s), 0);
+              else
+                mbar_arrive(bars.full(s));
             }
           }
         }
       }
-      if (!ok) break;
-      if (live) {
+    }
+    __syncwarp();
+  } else {
+    setmaxnreg_inc<184>();
+    const int q = warp & 3, part = (warp - 8) >> 2;
+    OutDesc o = p.out;
+    o.tma_c = (Lay::STAGING_BYTES > 0 && p.use_tma_store) ? &p.tma_c : nullptr;
+    const uint32_t staging = staging0 + (warp - 8) * kStageOutBytes;
+    uint32_t seg = 0, chunk = 0;
+    bool ok = true;
+    for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
+      const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
+      const int m0 = (2 * tc.mb + (int)crank) * kBM + q * 32, n0 = tc.nb * BN + part * PART;
+      const int n_left = p.N - n0;
+      const bool live = m0 < p.M && n_left > 0;  // any output here
+      TileBias<PART> tb;
+      if (live) load_tile_bias<PART>(o, 0, m0 + lane, n0, lane, tb);
+      float acc[PART];
 #pragma unroll
-        for (int j = 0; j < HALF / 32; ++j) {
-          if (32 * j < n_left) {
+      for (int i = 0; i < PART; ++i) acc[i] = 0.0f;
+      for (int st = 0; st < stages; st += kSegmentStages, ++seg) {
+        const uint32_t buf = seg % ACC;
+        const bool got = mbar_wait_bounded(bars.tfull(buf), (seg / ACC) & 1, wc.abort, wc.status_word, wc.limit_ns,
+                                           status_code(6, kSiteEpilogueTmemFull));
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t src = tmem_base + ((uint32_t)(q * 32) << 16) + buf * BN + part * PART;
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < PART / 32; ++j) {
             uint32_t v[32];
+            tmem_load_32cols(src + j * 32, v);
+            tmem_load_wait(v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);
-            epilogue_chunk<HALF>(o, j, tb, v, tc, m0, lane, true, staging, chunk);
+            for (int i = 0; i < 32; ++i) acc[32 * j + i] = __fadd_rn(acc[32 * j + i], __uint_as_float(v[i]));
           }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (crank != 0)
+            mbar_arrive_remote(bars.tempty(buf), 0);
+          else
+            mbar_arrive(bars.tempty(buf));
+        }
+      }
+      if (!ok) break;
+      if (!live) continue;
+#pragma unroll
+      for (int j = 0; j < PART / 32; ++j) {
+        if (32 * j >= n_left) break;
+        uint32_t v[32];
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);
+        epilogue_math<PART>(o, j, tb, v, f);
+        if (o.tma_c && m0 + 32 <= p.M) {
+          // 4 KB a warp: two 16-bit chunks of 32 x 32 in turn, or one of fp32
+          const uint32_t sbuf = staging + (o.out_f32 ? 0 : (chunk & 1) * (kStageOutBytes / 2));
+          if (lane == 0) {
+            if (o.out_f32)
+              bulk_wait_read_all();
+            else
+              bulk_wait_read_1();
+          }
+          __syncwarp();
+          stage_32(o, sbuf, lane, f);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(o.tma_c, sbuf, n0 + 32 * j, m0, 0);
+            bulk_commit();
+          }
+          ++chunk;
+        } else {
+          store_32_direct(o, 0, m0 + lane, n0 + 32 * j, true, f);
         }
       }
     }
@@ -355,7 +456,7 @@ cudaError_t launch_variant(ScaledParams& p, cudaStream_t stream, int slot) {
 
 template <int BN>
 cudaError_t launch_width(ScaledParams& p, cudaStream_t stream) {
-  constexpr int kSlot = 104 + (BN == 256 ? 0 : BN == 128 ? 3 : 6);
+  constexpr int kSlot = 104 + (BN == 192 ? 0 : BN == 128 ? 3 : 6);
   if (p.M <= kShortARows) return launch_variant<BN, kShortARows, true>(p, stream, kSlot);
   return p.m_tiles <= 2 ? launch_variant<BN, kBM, true>(p, stream, kSlot + 1)
                         : launch_variant<BN, kBM, false>(p, stream, kSlot + 2);
@@ -372,10 +473,14 @@ bi_status launch_scaled_gemm(const ScaledProblem& g, cudaStream_t stream, std::s
   p.M = (int32_t)g.M, p.N = (int32_t)g.N;
   p.m_tiles = (int32_t)((g.M + 2 * kBM - 1) / (2 * kBM));
   p.k_blocks = (int32_t)((g.K + kBK8 - 1) / kBK8);
-  // The widest tile that still gives every pair of SMs one.
+  // The width whose last round of tiles wastes least: columns a pair works through,
+  // and something for each tile's start and end; the wider one among equals.
   const int64_t pairs = dev.num_sms / 2;
   auto tiles = [&](int64_t bn) { return (int64_t)p.m_tiles * ((g.N + bn - 1) / bn); };
-  const int bn = tiles(256) >= pairs ? 256 : tiles(128) >= pairs ? 128 : 64;
+  auto cost = [&](int64_t bn) { return (tiles(bn) + pairs - 1) / pairs * (bn + 16); };
+  int bn = 192;
+  for (int w : {128, 64})
+    if (cost(w) < cost(bn)) bn = w;
   if (tiles(bn) > INT32_MAX) {
     *why = "tile count exceeds 2^31";
     return BI_ERR_INVALID_ARG;
@@ -397,7 +502,7 @@ bi_status launch_scaled_gemm(const ScaledProblem& g, cudaStream_t stream, std::s
   p.use_tma_store = encode_output_map(&p.tma_c, g.c, o.out_f32 != 0, o.out_f16 != 0, 1, g.M, g.N, g.ldc, 0) ? 1 : 0;
   p.status_word = dev.status_word;
   p.wait_limit_ns = kWaitLimitNs;
-  const cudaError_t e = bn == 256 ? launch_width<256>(p, stream) : bn == 128 ? launch_width<128>(p, stream) : launch_width<64>(p, stream);
+  const cudaError_t e = bn == 192 ? launch_width<192>(p, stream) : bn == 128 ? launch_width<128>(p, stream) : launch_width<64>(p, stream);
   if (e != cudaSuccess) {
     *why = std::string("block-scaled product launch: ") + cudaGetErrorString(e);
     return BI_ERR_CUDA;

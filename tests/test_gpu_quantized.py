@@ -125,14 +125,14 @@ def test_quantize_empty():
 # -- the block-scaled product ---------------------------------------------------------------
 
 def _operands(M, N, K, seed, fill=0x7F):
-    """e4m3 operands with fp32 scales of any size, in rows padded with NaNs."""
+    """e4m3 operands with powers of two for scales, in rows padded with NaNs."""
     Kp = (K + 15) // 16 * 16 + 16
     a = torch.full((M, Kp), fill, dtype=torch.uint8, device="cuda")
     b = torch.full((N, Kp), fill, dtype=torch.uint8, device="cuda")
     a[:, :K], b[:, :K] = _e4m3((M, K), seed).view(torch.uint8), _e4m3((N, K), seed + 1).view(torch.uint8)
     kb = -(-K // 128)
-    sa = torch.exp2(6 * _uniform((M, kb), seed + 2) - 8)
-    sb = torch.exp2(6 * _uniform((-(-N // 128), kb), seed + 3) - 8)
+    sa = torch.exp2(torch.floor(6 * _uniform((M, kb), seed + 2)) - 8)
+    sb = torch.exp2(torch.floor(6 * _uniform((-(-N // 128), kb), seed + 3)) - 8)
     return a.view(E4M3)[:, :K], sa, b.view(E4M3)[:, :K].t(), sb.t()
 
 
@@ -210,12 +210,19 @@ def test_mm_blockscaled_nan_stays_in_its_rows_and_empty_sums():
     bad = a.clone()
     bad.view(torch.uint8)[7, 299] = 0x7F
     sc = sa.clone()
-    sc[9, 1] = float("nan")
+    sc[9, 1], sc[11, 2], sc[12, 0], sc[13, 0] = float("nan"), 0.75, 0.0, -1.0  # none of them a power of two
     store = torch.zeros((M, 304), dtype=torch.uint8, device="cuda").view(E4M3)[:, :K]
     store.view(torch.uint8).copy_(bad.view(torch.uint8))
     c = bi.bi_mm_blockscaled(store, sc, b, sb, out_dtype=F32)
-    keep = [m for m in range(M) if m not in (7, 9)]
-    assert torch.isnan(c[[7, 9]]).all() and bits_equal(c[keep], clean[keep])
+    gone = [7, 9, 11, 12, 13]
+    keep = [m for m in range(M) if m not in gone]
+    assert torch.isnan(c[gone]).all() and bits_equal(c[keep], clean[keep])
+    wide = sa.clone()
+    wide[3], wide[4] = 2.0 ** 100, 2.0 ** -126  # the whole range
+    c = bi.bi_mm_blockscaled(a, wide, b, sb, out_dtype=F32)
+    want, bound = ref.mm(a, wide, b, sb, None, F32)
+    sref.assert_within(c[[3, 5]], want[[3, 5]], bound[[3, 5]])
+    assert (c[4].abs() < 2.0 ** -90).all()
     bias = _normal((N,), BF16, 1)
     e = bi.bi_mm_blockscaled(torch.empty((M, 0), device="cuda").to(E4M3), sa[:, :0],
                              torch.empty((N, 0), device="cuda").to(E4M3).t(), sb[:0], bias=bias, out_dtype=F32)

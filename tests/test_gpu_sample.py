@@ -245,7 +245,7 @@ def test_decode_step_in_8_bits():
     h = ref.from_e4m3(st["head"].values) * np.repeat(np.repeat(sref.f64(st["head"].scales), 128, 0)[:1000], 128, 1)
     plain = (y * np.repeat(ys, 128, 1)) @ h.T
     size = np.abs(y * np.repeat(ys, 128, 1)) @ np.abs(h).T
-    sref.assert_within(logits, plain, (2.0 ** -19 + 8 * 2.0 ** -24) * size + 2.0 ** -24 * np.abs(plain), "logits")
+    sref.assert_within(logits, plain, (16 * 2.0 ** -22 + 4 * 2.0 ** -24) * size + 2.0 ** -24 * np.abs(plain), "logits")
     for b in range(5):
         t, near = ref.sample(sref.f64(logits[b]), float(st["u"][b]), float(np.float32(0.8)), 50, float(np.float32(0.9)))
         assert near or int(tokens[b]) == t
