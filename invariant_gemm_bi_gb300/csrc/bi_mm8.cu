@@ -20,11 +20,13 @@
 //                columns of two K blocks a stage by TMA into a ring (128-byte
 //                swizzle), as in the 16-bit product
 //   warp 1       TMEM allocation; in the even CTA the issuer of the MMAs
-//   warps 4-7    scales: each loads 32 rows' of four blocks ahead, turns them
-//                into exponents and writes them to the stage's columns of TMEM,
-//                once for each quadrant of lanes, which is a warp's.  Their
-//                arrivals count on the stage's barrier beside the copies' bytes.
-//   warps 8-15   sums: a warp has 32 rows and half of the tile's columns, BN / 2
+//   warps 4-11   scales, two sets for every other stage: a warp loads 32 rows' of
+//                four blocks ahead, turns them into exponents and writes them to
+//                the stage's columns of TMEM, once for each quadrant of lanes,
+//                which is a warp's.  Their arrivals count on the stage's barrier
+//                beside the copies' bytes.  (One set: 730 cycles a stage, where
+//                the copies of a decode step's narrow tiles take 400.)
+//   warps 12-19  sums: a warp has 32 rows and half of the tile's columns, BN / 2
 //                fp32 registers a thread; it adds a segment's accumulator and
 //                frees it (there are two), then bias, rounding and the store.
 //
@@ -46,11 +48,11 @@ namespace {
 
 constexpr int kBK8 = 128;     // K of a block and a stage: one 128-byte swizzle row
 constexpr int kUmmaK8 = 32;   // K of a tcgen05.mma of 8-bit operands
-constexpr int kStageBlocks = 2;      // K blocks of a stage
-constexpr int kSegmentStages = 8;    // stages of a segment: K = 2048
-constexpr int kThreads = 512;
-constexpr int kScaleWarps = 4, kSumWarps = 8, kParts = 2;
-constexpr int kScaleGroup = 4;       // K blocks whose scales are loaded at once
+constexpr int kSegmentBlocks = 16;  // K blocks of a segment: K = 2048
+constexpr int kScaleWarps = 4, kScaleSets = 2, kSumWarps = 8, kParts = 2;
+constexpr int kFirstScale = 4, kFirstSum = kFirstScale + kScaleWarps * kScaleSets;  // warps
+constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
+constexpr int kGroupBlocks = 4;  // K blocks whose scales a set of warps loads at once
 
 struct ScaledParams {
   CUtensorMap tma_a;  // [M][K] bytes, box {128, 128 (32 for M <= 32)}
@@ -67,25 +69,30 @@ struct ScaledParams {
 template <int BN, int A_ROWS>
 struct Layout8 {
   static constexpr int PART = BN / kParts;  // columns of a sum warp
+  // K blocks of a stage.  One: the ring's bytes come free in small pieces, and more
+  // of it is in flight (8192 x 4096 x 14336 with two: XX us).  Two where a block's
+  // copies take less than the 335 cycles that a stage costs the issuer.
+  static constexpr int BLOCKS = 2;
+  static constexpr int SEGMENT = kSegmentBlocks / BLOCKS, GROUP = kGroupBlocks / BLOCKS;  // stages of each
   static constexpr int A_BYTES = A_ROWS * kBK8;          // a block
   static constexpr int B_BYTES = BN / 2 * kBK8;          // this CTA's half of the tile's columns
-  static constexpr int STAGE_BYTES = kStageBlocks * (A_BYTES + B_BYTES);
+  static constexpr int STAGE_BYTES = BLOCKS * (A_BYTES + B_BYTES);
   static constexpr int ACC = 2;
   // exponents of a block in TMEM, a 32-bit column for each 32 rows of A and of B
   static constexpr int SFA_COLS = 4, SFB_COLS = BN > 128 ? 8 : 4, SF_COLS = SFA_COLS + SFB_COLS;
   static constexpr int BAR_BYTES = 1024;
-  static constexpr int EXCHANGE_BYTES = 2 * kBM * 4;  // exponents on their way between the scale warps
+  static constexpr int EXCHANGE_BYTES = kScaleSets * 2 * kBM * 4;  // exponents on their way between the scale warps
   static constexpr int STAGING_BYTES = A_ROWS == kBM ? kSumWarps * kStageOutBytes : 0;
   static constexpr int MAX_DYN = 232448;
   static constexpr int FIT = (MAX_DYN - 1024 - BAR_BYTES - EXCHANGE_BYTES - STAGING_BYTES) / STAGE_BYTES;
-  static constexpr int ROOM = (512 - ACC * BN) / (kStageBlocks * SF_COLS);  // stages whose exponents fit TMEM
+  static constexpr int ROOM = (512 - ACC * BN) / (BLOCKS * SF_COLS);  // stages whose exponents fit TMEM
   static constexpr int STAGES = FIT < ROOM ? FIT : ROOM;
   static constexpr int DYN_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + EXCHANGE_BYTES + STAGING_BYTES;
   static constexpr int A_OVERREAD = (kBM - A_ROWS) * kBK8;  // the tensor core reads 128 A rows from a block's base
   static_assert(STAGES >= 3, "pipeline depth");
-  static_assert(ACC * BN + STAGES * kStageBlocks * SF_COLS <= 512, "accumulators and exponents fit TMEM");
+  static_assert(ACC * BN + STAGES * BLOCKS * SF_COLS <= 512, "accumulators and exponents fit TMEM");
   static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 8 <= BAR_BYTES, "barriers fit their block");
-  static_assert(A_OVERREAD <= STAGES * kStageBlocks * B_BYTES, "A over-read stays inside the B stages");
+  static_assert(A_OVERREAD <= STAGES * BLOCKS * B_BYTES, "A over-read stays inside the B stages");
   static_assert(DYN_BYTES > 116 * 1024, "one CTA per SM: TMEM is allocated whole");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "stages hold whole swizzle atoms");
 };
@@ -121,6 +128,12 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
+// A load that stays where it is written, ahead of the waits before its use.
+__device__ __forceinline__ float load_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 // The exponent byte of a scale 2^(e - 127); anything else is a NaN to the tensor core.
 __device__ __forceinline__ uint32_t exponent_byte(float scale) {
   const uint32_t b = __float_as_uint(scale);
@@ -139,8 +152,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  const uint32_t sA = base, sB = base + Lay::STAGES * kStageBlocks * Lay::A_BYTES;
-  const uint32_t staging0 = sB + Lay::STAGES * kStageBlocks * Lay::B_BYTES;
+  const uint32_t sA = base, sB = base + Lay::STAGES * Lay::BLOCKS * Lay::A_BYTES;
+  const uint32_t staging0 = sB + Lay::STAGES * Lay::BLOCKS * Lay::B_BYTES;
   uint32_t* exchange = reinterpret_cast<uint32_t*>(smem + (staging0 + Lay::STAGING_BYTES - base));
   PipeBars bars;
   bars.full0 = staging0 + Lay::STAGING_BYTES + Lay::EXCHANGE_BYTES;
@@ -151,7 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars.drain + 8 - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = (p.k_blocks + kStageBlocks - 1) / kStageBlocks;  // of a tile
+  const int stages = (p.k_blocks + Lay::BLOCKS - 1) / Lay::BLOCKS;  // of a tile
 
   if (threadIdx.x == 0) {
     // Even CTA: a stage is full when the copies of both CTAs have landed and the
@@ -179,13 +192,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t sf_base = tmem_base + ACC * BN;  // exponents of stage s: sf_base + s * kStageBlocks * SF_COLS
+  const uint32_t sf_base = tmem_base + ACC * BN;  // exponents of stage s: sf_base + s * Lay::BLOCKS * SF_COLS
   cluster_arrive_relaxed();
   cluster_wait();  // both CTAs' barriers are initialised
   const WaitCtl wc{abort_flag, p.status_word, p.wait_limit_ns};
 
-  if (warp < 8) {
-    setmaxnreg_dec<72>();
+  // 256 x 152 + 384 x 56 <= 640 x 96
+  if (warp < kFirstSum) {
+    setmaxnreg_dec<56>();
     if (warp == 0 && elect_one()) {
       uint32_t it = 0;
       bool ok = true;
@@ -202,12 +216,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           if (crank == 0)
-            mbar_arrive_expect_tx(bars.full(s), kStageBlocks * (2 * Lay::B_BYTES + Lay::A_BYTES * (peer_live ? 2 : 1)));
+            mbar_arrive_expect_tx(bars.full(s), Lay::BLOCKS * (2 * Lay::B_BYTES + Lay::A_BYTES * (peer_live ? 2 : 1)));
           const uint32_t fb = cluster_map_shared(bars.full(s), 0);
 #pragma unroll
-          for (int j = 0; j < kStageBlocks; ++j) {  // (a block past K is all zeros)
-            const int k = (st * kStageBlocks + j) * kBK8;
-            const uint32_t at = s * kStageBlocks + j;
+          for (int j = 0; j < Lay::BLOCKS; ++j) {  // (a block past K is all zeros)
+            const int k = (st * Lay::BLOCKS + j) * kBK8;
+            const uint32_t at = s * Lay::BLOCKS + j;
             if (STREAM_B) {  // B is used by one or two pairs, A by every column tile
               tma_load_3d_pair_hint(sB + at * Lay::B_BYTES, &p.tma_b, fb, k, n0, 0, l2_policy_evict_first());
               if (a_live)
@@ -231,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
         for (int st = 0; st < stages; ++st, ++it) {
-          const bool opens = st % kSegmentStages == 0;
+          const bool opens = st % Lay::SEGMENT == 0;
           const uint32_t buf = seg % ACC, use = seg / ACC, s = it % Lay::STAGES;
           if (opens && use > 0 &&
               !mbar_wait_bounded<true>(bars.tempty(buf), (use - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
@@ -239,15 +253,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (!mbar_wait_bounded<true>(bars.full(s), (it / Lay::STAGES) & 1, wc.abort, wc.status_word, wc.limit_ns,
+          if (!mbar_wait_bounded(bars.full(s), (it / Lay::STAGES) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                        status_code(6, kSiteMmaFull))) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
 #pragma unroll
-          for (int j = 0; j < kStageBlocks; ++j) {
-            const uint32_t at = s * kStageBlocks + j;
+          for (int j = 0; j < Lay::BLOCKS; ++j) {
+            const uint32_t at = s * Lay::BLOCKS + j;
             const uint64_t a = smem_desc_sw128(sA + at * Lay::A_BYTES, 16, 1024);
             const uint64_t b = smem_desc_sw128(sB + at * Lay::B_BYTES, 16, 1024);
             const uint32_t sf = sf_base + at * Lay::SF_COLS;
@@ -257,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            opens && j == 0 && k == 0 ? 0u : 1u);
           }
           umma_commit_pair(bars.empty(s), kBoth);
-          if (st % kSegmentStages == kSegmentStages - 1 || st + 1 == stages) {
+          if (st % Lay::SEGMENT == Lay::SEGMENT - 1 || st + 1 == stages) {
             umma_commit_pair(bars.tfull(buf), kBoth);
             ++seg;
           }
@@ -265,40 +279,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       umma_commit_pair(bars.drain, 1);
       mbar_wait_bounded(bars.drain, 0, nullptr, wc.status_word, wc.limit_ns, status_code(6, kSiteDrain));
-    } else if (warp >= 4) {
-      const int q = warp - 4;
-      uint32_t it = 0, turn = 0;
+    } else if (warp >= kFirstScale) {
+      const int q = warp & 3, set = (warp - kFirstScale) >> 2;  // the set takes every other stage
+      uint32_t first = 0, turn = 0;                             // stages of the tiles before; exchanges
       bool ok = true;
-      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
+      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride, first += stages) {
         const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
         const int m0 = (2 * tc.mb + (int)crank) * kBM, n0 = tc.nb * BN;
-        // A: this lane's row, 32 q + lane; B: lanes 0-3 of the tile's first column block, lanes 4-7 of its second
-        const float* sa = p.sa + (int64_t)min(m0 + 32 * q + lane, p.M - 1) * p.sa_m;
+        // A: this lane's row, 32 q + lane (short A has the first quadrant's only);
+        // B: lanes 0-3 the tile's first block of columns, lanes 4-7 its second
+        const float* sa = p.sa + (int64_t)min(m0 + (A_ROWS == kBM ? 32 * q : 0) + lane, p.M - 1) * p.sa_m;
         const float* sb = p.sb + (int64_t)min(n0 / 128 + ((lane >> 2) & 1), (p.N - 1) / 128) * p.sb_n;
-        float a[kScaleGroup], b;
-        auto request = [&](int kb0) {
-#pragma unroll
-          for (int j = 0; j < kScaleGroup; ++j) a[j] = kb0 + j < p.k_blocks ? __ldg(sa + (kb0 + j) * p.sa_k) : 1.0f;
-          const int kb = kb0 + (lane & 3);
-          b = kb < p.k_blocks ? __ldg(sb + kb * p.sb_k) : 1.0f;
+        // scales of this stage of the set and its next, four blocks, as exponents (a block past K: any)
+        float a[kGroupBlocks], b;
+        auto block_of = [&](int st, int j) {
+          return min((st + j / Lay::BLOCKS * kScaleSets) * Lay::BLOCKS + j % Lay::BLOCKS, p.k_blocks - 1);
         };
-        request(0);
-        for (int kb0 = 0; kb0 < p.k_blocks; kb0 += kScaleGroup, ++turn) {
+        auto request = [&](int st) {
+#pragma unroll
+          for (int j = 0; j < kGroupBlocks; ++j) a[j] = load_now(sa + block_of(st, j) * p.sa_k);
+          b = load_now(sb + block_of(st, lane & 3) * p.sb_k);
+        };
+        request(set);
+        for (int st = set; st < stages; st += Lay::GROUP * kScaleSets, ++turn) {
           const uint32_t mine = exponent_byte(a[0]) | exponent_byte(a[1]) << 8 | exponent_byte(a[2]) << 16 | exponent_byte(a[3]) << 24;
           const uint32_t col = exponent_byte(b);
-          request(kb0 + kScaleGroup);
-          uint32_t* x = exchange + (turn & 1) * kBM;  // (a warp is at most one turn ahead)
-          x[32 * q + lane] = mine;
-          ok = named_barrier_and(1, 32 * kScaleWarps, ok);  // all leave together
-          if (!ok) break;
-          uint32_t rows[4];
+          request(st + Lay::GROUP * kScaleSets);
+          uint32_t rows[4] = {mine, mine, mine, mine};
+          if constexpr (A_ROWS == kBM) {
+            uint32_t* x = exchange + (2 * set + (turn & 1)) * kBM;  // (a warp is at most one turn ahead)
+            x[32 * q + lane] = mine;
+            ok = named_barrier_and(1 + set, 32 * kScaleWarps, ok);  // all leave together
+            if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) rows[c] = x[32 * c + lane];
-#pragma unroll
-          for (int half = 0; half < kScaleGroup / kStageBlocks; ++half) {
-            if (kb0 + half * kStageBlocks >= p.k_blocks) break;
-            const uint32_t s = it % Lay::STAGES, r = it / Lay::STAGES;
-            ++it;
+            for (int c = 0; c < 4; ++c) rows[c] = x[32 * c + lane];
+          } else if (!ok) {
+            break;
+          }
+#pragma unroll 1
+          for (int half = 0; half < Lay::GROUP; ++half) {
+            if (st + half * kScaleSets >= stages) break;
+            const uint32_t it = first + st + half * kScaleSets, s = it % Lay::STAGES, r = it / Lay::STAGES;
             const bool got = r == 0 || mbar_wait_bounded(bars.empty(s), (r - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                                          status_code(6, kSiteProducerEmpty));
             if (!__all_sync(0xffffffffu, got)) {
@@ -307,16 +328,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_after_sync();
 #pragma unroll
-            for (int j = 0; j < kStageBlocks; ++j) {
-              const uint32_t pick = (half * kStageBlocks + j) * 0x1111u;  // a byte four times
-              const uint32_t at = sf_base + (s * kStageBlocks + j) * Lay::SF_COLS + ((uint32_t)(q * 32) << 16);
+            for (int j = 0; j < Lay::BLOCKS; ++j) {
+              const uint32_t pick = (half * Lay::BLOCKS + j) * 0x1111u;  // a byte four times
+              const uint32_t at = sf_base + (s * Lay::BLOCKS + j) * Lay::SF_COLS + ((uint32_t)(q * 32) << 16);
               tmem_store_4cols(at, __byte_perm(rows[0], 0, pick), __byte_perm(rows[1], 0, pick),
                                __byte_perm(rows[2], 0, pick), __byte_perm(rows[3], 0, pick));
               // 32 columns of the tile lie in one block of 128
               uint32_t w[8];
 #pragma unroll
               for (int c = 0; c < Lay::SFB_COLS; ++c)
-                w[c] = __shfl_sync(0xffffffffu, col, ((n0 + 32 * c) / 128 - n0 / 128) % 2 * 4 + half * kStageBlocks + j) * 0x01010101u;
+                w[c] = __shfl_sync(0xffffffffu, col, ((n0 + 32 * c) / 128 - n0 / 128) % 2 * 4 + half * Lay::BLOCKS + j) * 0x01010101u;
               tmem_store_4cols(at + Lay::SFA_COLS, w[0], w[1], w[2], w[3]);
               if (Lay::SFB_COLS > 4) tmem_store_4cols(at + Lay::SFA_COLS + 4, w[4], w[5], w[6], w[7]);
             }
@@ -337,11 +358,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    setmaxnreg_inc<184>();
-    const int q = warp & 3, part = (warp - 8) >> 2;
+    setmaxnreg_inc<152>();
+    const int q = warp & 3, part = (warp - kFirstSum) >> 2;
     OutDesc o = p.out;
     o.tma_c = (Lay::STAGING_BYTES > 0 && p.use_tma_store) ? &p.tma_c : nullptr;
-    const uint32_t staging = staging0 + (warp - 8) * kStageOutBytes;
+    const uint32_t staging = staging0 + (warp - kFirstSum) * kStageOutBytes;
     uint32_t seg = 0, chunk = 0;
     bool ok = true;
     for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
@@ -354,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float acc[PART];
 #pragma unroll
       for (int i = 0; i < PART; ++i) acc[i] = 0.0f;
-      for (int st = 0; st < stages; st += kSegmentStages, ++seg) {
+      for (int st = 0; st < stages; st += Lay::SEGMENT, ++seg) {
         const uint32_t buf = seg % ACC;
         const bool got = mbar_wait_bounded(bars.tfull(buf), (seg / ACC) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                            status_code(6, kSiteEpilogueTmemFull));
