@@ -17,15 +17,13 @@
 //
 // Pairs of CTAs (cta_group::2), tiles of 256 rows x BN columns:
 //   warp 0       producer: A (128 x 128 bytes) and this CTA's half of B's
-//                columns of two K blocks a stage by TMA into a ring (128-byte
+//                columns of a K block by TMA into a ring of stages (128-byte
 //                swizzle), as in the 16-bit product
 //   warp 1       TMEM allocation; in the even CTA the issuer of the MMAs
-//   warps 4-11   scales, two sets for every other stage: a warp loads 32 rows' of
-//                four blocks ahead, turns them into exponents and writes them to
-//                the stage's columns of TMEM, once for each quadrant of lanes,
-//                which is a warp's.  Their arrivals count on the stage's barrier
-//                beside the copies' bytes.  (One set: 730 cycles a stage, where
-//                the copies of a decode step's narrow tiles take 400.)
+//   warps 4-11   scales, two sets for every other group of four blocks: a warp
+//                loads 32 rows' ahead, turns them into exponents, and the four of
+//                a set write them all to TMEM, once for each quadrant of lanes,
+//                which is a warp's
 //   warps 12-19  sums: a warp has 32 rows and half of the tile's columns, BN / 2
 //                fp32 registers a thread; it adds a segment's accumulator and
 //                frees it (there are two), then bias, rounding and the store.
@@ -52,7 +50,8 @@ constexpr int kSegmentBlocks = 16;  // K blocks of a segment: K = 2048
 constexpr int kScaleWarps = 4, kScaleSets = 2, kSumWarps = 8, kParts = 2;
 constexpr int kFirstScale = 4, kFirstSum = kFirstScale + kScaleWarps * kScaleSets;  // warps
 constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-constexpr int kGroupBlocks = 4;  // K blocks whose scales a set of warps loads at once
+constexpr int kGroup = 4;  // K blocks whose scales are loaded and written at once
+constexpr int kStoreBytes = 2048;  // a sum warp's 32 x 32 results of 16 bits on their way out
 
 struct ScaledParams {
   CUtensorMap tma_a;  // [M][K] bytes, box {128, 128 (32 for M <= 32)}
@@ -69,11 +68,11 @@ struct ScaledParams {
 template <int BN, int A_ROWS>
 struct Layout8 {
   static constexpr int PART = BN / kParts;  // columns of a sum warp
-  // K blocks of a stage.  One: the ring's bytes come free in small pieces, and more
-  // of it is in flight (8192 x 4096 x 14336 with two: XX us).  Two where a block's
-  // copies take less than the 335 cycles that a stage costs the issuer.
-  static constexpr int BLOCKS = 2;
-  static constexpr int SEGMENT = kSegmentBlocks / BLOCKS, GROUP = kGroupBlocks / BLOCKS;  // stages of each
+  // K blocks of a stage of copies.  One: the ring comes free in small pieces, and
+  // more of it is in flight.  Two where a block's copies take less than the 225
+  // cycles that a stage costs the issuer.
+  static constexpr int BLOCKS = A_ROWS == kBM ? 1 : 2;
+  static constexpr int SLOTS = BN > 128 ? 2 : 4;  // groups of exponents in TMEM
   static constexpr int A_BYTES = A_ROWS * kBK8;          // a block
   static constexpr int B_BYTES = BN / 2 * kBK8;          // this CTA's half of the tile's columns
   static constexpr int STAGE_BYTES = BLOCKS * (A_BYTES + B_BYTES);
@@ -82,16 +81,17 @@ struct Layout8 {
   static constexpr int SFA_COLS = 4, SFB_COLS = BN > 128 ? 8 : 4, SF_COLS = SFA_COLS + SFB_COLS;
   static constexpr int BAR_BYTES = 1024;
   static constexpr int EXCHANGE_BYTES = kScaleSets * 2 * kBM * 4;  // exponents on their way between the scale warps
-  static constexpr int STAGING_BYTES = A_ROWS == kBM ? kSumWarps * kStageOutBytes : 0;
+  static constexpr int STAGING_BYTES = A_ROWS == kBM ? kSumWarps * kStoreBytes : 0;
   static constexpr int MAX_DYN = 232448;
   static constexpr int FIT = (MAX_DYN - 1024 - BAR_BYTES - EXCHANGE_BYTES - STAGING_BYTES) / STAGE_BYTES;
-  static constexpr int ROOM = (512 - ACC * BN) / (BLOCKS * SF_COLS);  // stages whose exponents fit TMEM
-  static constexpr int STAGES = FIT < ROOM ? FIT : ROOM;
+  static constexpr int STAGES = FIT > 16 ? 16 : FIT;
   static constexpr int DYN_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + EXCHANGE_BYTES + STAGING_BYTES;
   static constexpr int A_OVERREAD = (kBM - A_ROWS) * kBK8;  // the tensor core reads 128 A rows from a block's base
   static_assert(STAGES >= 3, "pipeline depth");
-  static_assert(ACC * BN + STAGES * BLOCKS * SF_COLS <= 512, "accumulators and exponents fit TMEM");
-  static_assert(8 * (2 * STAGES + 2 * ACC + 1) + 8 <= BAR_BYTES, "barriers fit their block");
+  static_assert(ACC * BN + SLOTS * kGroup * SF_COLS <= 512, "accumulators and exponents fit TMEM");
+  static_assert(SLOTS % kScaleSets == 0, "a slot is always the same warps', who see each of its phases");
+  static_assert(8 * (2 * STAGES + 2 * ACC + 2 * SLOTS + 1) + 8 <= BAR_BYTES, "barriers fit their block");
+  static_assert(kGroup % BLOCKS == 0 && kSegmentBlocks % kGroup == 0, "stages in groups in segments");
   static_assert(A_OVERREAD <= STAGES * BLOCKS * B_BYTES, "A over-read stays inside the B stages");
   static_assert(DYN_BYTES > 116 * 1024, "one CTA per SM: TMEM is allocated whole");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "stages hold whole swizzle atoms");
@@ -161,18 +161,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bars.tfull0 = bars.empty0 + 8 * Lay::STAGES;
   bars.tempty0 = bars.tfull0 + 8 * ACC;
   bars.drain = bars.tempty0 + 8 * ACC;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (bars.drain + 8 - base));
+  const uint32_t sfull0 = bars.drain + 8, sempty0 = sfull0 + 8 * Lay::SLOTS;  // of the groups of exponents
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (sempty0 + 8 * Lay::SLOTS - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = (p.k_blocks + Lay::BLOCKS - 1) / Lay::BLOCKS;  // of a tile
+  const int groups = (p.k_blocks + kGroup - 1) / kGroup;
 
   if (threadIdx.x == 0) {
-    // Even CTA: a stage is full when the copies of both CTAs have landed and the
-    // scale warps of both have written; an accumulator is free when the sum warps
-    // of both have read it.
+    // Even CTA: a stage is full when the copies of both CTAs have landed, a group
+    // of exponents when a set of scale warps in each has written them; an
+    // accumulator is free when the sum warps of both have read it.
     for (int s = 0; s < Lay::STAGES; ++s) {
-      mbar_init(bars.full(s), 1 + 2 * kScaleWarps);
+      mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 1);
+    }
+    for (int g = 0; g < Lay::SLOTS; ++g) {
+      mbar_init(sfull0 + 8 * g, 2 * kScaleWarps);
+      mbar_init(sempty0 + 8 * g, 1);
     }
     for (int b = 0; b < ACC; ++b) {
       mbar_init(bars.tfull(b), 1);
@@ -192,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t sf_base = tmem_base + ACC * BN;  // exponents of stage s: sf_base + s * Lay::BLOCKS * SF_COLS
+  const uint32_t sf_base = tmem_base + ACC * BN;  // exponents of block j of slot g: sf_base + (g * kGroup + j) * SF_COLS
   cluster_arrive_relaxed();
   cluster_wait();  // both CTAs' barriers are initialised
   const WaitCtl wc{abort_flag, p.status_word, p.wait_limit_ns};
@@ -241,20 +247,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
     } else if (warp == 1 && crank == 0 && elect_one()) {
       constexpr uint32_t kIdesc = idesc_mx(2 * kBM, BN);
-      uint32_t it = 0, seg = 0;
+      uint32_t it = 0, seg = 0, grp = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
         for (int st = 0; st < stages; ++st, ++it) {
-          const bool opens = st % Lay::SEGMENT == 0;
-          const uint32_t buf = seg % ACC, use = seg / ACC, s = it % Lay::STAGES;
+          const int kb = st * Lay::BLOCKS;
+          const bool opens = kb % kSegmentBlocks == 0;
+          const uint32_t buf = seg % ACC, use = seg / ACC, s = it % Lay::STAGES, slot = grp % Lay::SLOTS;
           if (opens && use > 0 &&
               !mbar_wait_bounded<true>(bars.tempty(buf), (use - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                        status_code(6, kSiteMmaTmemEmpty))) {
             ok = false;
             break;
           }
-          if (!mbar_wait_bounded(bars.full(s), (it / Lay::STAGES) & 1, wc.abort, wc.status_word, wc.limit_ns,
-                                       status_code(6, kSiteMmaFull))) {
+          // (CTA scope: what is waited for are copies and TMEM stores, complete
+          // when they arrive; the cluster's costs 150 cycles more a wait)
+          if ((kb % kGroup == 0 && !mbar_wait_bounded(sfull0 + 8 * slot, (grp / Lay::SLOTS) & 1, wc.abort, wc.status_word,
+                                                      wc.limit_ns, status_code(6, kSiteMmaFull))) ||
+              !mbar_wait_bounded(bars.full(s), (it / Lay::STAGES) & 1, wc.abort, wc.status_word, wc.limit_ns,
+                                 status_code(6, kSiteMmaFull))) {
             ok = false;
             break;
           }
@@ -264,14 +275,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t at = s * Lay::BLOCKS + j;
             const uint64_t a = smem_desc_sw128(sA + at * Lay::A_BYTES, 16, 1024);
             const uint64_t b = smem_desc_sw128(sB + at * Lay::B_BYTES, 16, 1024);
-            const uint32_t sf = sf_base + at * Lay::SF_COLS;
+            const uint32_t sf = sf_base + (slot * kGroup + (uint32_t)(kb + j) % kGroup) * Lay::SF_COLS;
 #pragma unroll
             for (int k = 0; k < kBK8 / kUmmaK8; ++k)  // (the address is the low bits, in 16-byte units)
               umma_mx_pair(tmem_base + buf * BN, a + 2 * k, b + 2 * k, kIdesc, sf, sf + Lay::SFA_COLS,
                            opens && j == 0 && k == 0 ? 0u : 1u);
           }
           umma_commit_pair(bars.empty(s), kBoth);
-          if (st % Lay::SEGMENT == Lay::SEGMENT - 1 || st + 1 == stages) {
+          const int next = kb + Lay::BLOCKS;
+          if (next % kGroup == 0 || st + 1 == stages) {
+            umma_commit_pair(sempty0 + 8 * slot, kBoth);
+            ++grp;
+          }
+          if (next % kSegmentBlocks == 0 || st + 1 == stages) {
             umma_commit_pair(bars.tfull(buf), kBoth);
             ++seg;
           }
@@ -280,31 +296,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       umma_commit_pair(bars.drain, 1);
       mbar_wait_bounded(bars.drain, 0, nullptr, wc.status_word, wc.limit_ns, status_code(6, kSiteDrain));
     } else if (warp >= kFirstScale) {
-      const int q = warp & 3, set = (warp - kFirstScale) >> 2;  // the set takes every other stage
-      uint32_t first = 0, turn = 0;                             // stages of the tiles before; exchanges
+      const int q = warp & 3, set = (warp - kFirstScale) >> 2;  // the set takes every other group
+      uint32_t first = 0, turn = 0;                             // groups of the tiles before; exchanges
       bool ok = true;
-      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride, first += stages) {
+      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride, first += groups) {
         const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
         const int m0 = (2 * tc.mb + (int)crank) * kBM, n0 = tc.nb * BN;
         // A: this lane's row, 32 q + lane (short A has the first quadrant's only);
         // B: lanes 0-3 the tile's first block of columns, lanes 4-7 its second
         const float* sa = p.sa + (int64_t)min(m0 + (A_ROWS == kBM ? 32 * q : 0) + lane, p.M - 1) * p.sa_m;
         const float* sb = p.sb + (int64_t)min(n0 / 128 + ((lane >> 2) & 1), (p.N - 1) / 128) * p.sb_n;
-        // scales of this stage of the set and its next, four blocks, as exponents (a block past K: any)
-        float a[kGroupBlocks], b;
-        auto block_of = [&](int st, int j) {
-          return min((st + j / Lay::BLOCKS * kScaleSets) * Lay::BLOCKS + j % Lay::BLOCKS, p.k_blocks - 1);
-        };
-        auto request = [&](int st) {
+        float a[kGroup], b;
+        auto request = [&](int g) {  // (a block past K: any)
 #pragma unroll
-          for (int j = 0; j < kGroupBlocks; ++j) a[j] = load_now(sa + block_of(st, j) * p.sa_k);
-          b = load_now(sb + block_of(st, lane & 3) * p.sb_k);
+          for (int j = 0; j < kGroup; ++j) a[j] = load_now(sa + min(g * kGroup + j, p.k_blocks - 1) * p.sa_k);
+          b = load_now(sb + min(g * kGroup + (lane & 3), p.k_blocks - 1) * p.sb_k);
         };
-        request(set);
-        for (int st = set; st < stages; st += Lay::GROUP * kScaleSets, ++turn) {
+        const int g0 = (set + kScaleSets - (int)(first % kScaleSets)) % kScaleSets;
+        request(g0);
+        for (int g = g0; g < groups; g += kScaleSets, ++turn) {
           const uint32_t mine = exponent_byte(a[0]) | exponent_byte(a[1]) << 8 | exponent_byte(a[2]) << 16 | exponent_byte(a[3]) << 24;
           const uint32_t col = exponent_byte(b);
-          request(st + Lay::GROUP * kScaleSets);
+          request(g + kScaleSets);
           uint32_t rows[4] = {mine, mine, mine, mine};
           if constexpr (A_ROWS == kBM) {
             uint32_t* x = exchange + (2 * set + (turn & 1)) * kBM;  // (a warp is at most one turn ahead)
@@ -313,45 +326,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
 #pragma unroll
             for (int c = 0; c < 4; ++c) rows[c] = x[32 * c + lane];
-          } else if (!ok) {
+          }
+          const uint32_t slot = (first + g) % Lay::SLOTS, use = (first + g) / Lay::SLOTS;
+          const bool got = use == 0 || mbar_wait_bounded(sempty0 + 8 * slot, (use - 1) & 1, wc.abort, wc.status_word,
+                                                         wc.limit_ns, status_code(6, kSiteProducerEmpty));
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            if constexpr (A_ROWS == kBM) continue;  // to the next exchange, which all leave by
             break;
           }
-#pragma unroll 1
-          for (int half = 0; half < Lay::GROUP; ++half) {
-            if (st + half * kScaleSets >= stages) break;
-            const uint32_t it = first + st + half * kScaleSets, s = it % Lay::STAGES, r = it / Lay::STAGES;
-            const bool got = r == 0 || mbar_wait_bounded(bars.empty(s), (r - 1) & 1, wc.abort, wc.status_word, wc.limit_ns,
-                                                         status_code(6, kSiteProducerEmpty));
-            if (!__all_sync(0xffffffffu, got)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
+          tc_fence_after_sync();
+          const uint32_t to = sf_base + slot * kGroup * Lay::SF_COLS + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-            for (int j = 0; j < Lay::BLOCKS; ++j) {
-              const uint32_t pick = (half * Lay::BLOCKS + j) * 0x1111u;  // a byte four times
-              const uint32_t at = sf_base + (s * Lay::BLOCKS + j) * Lay::SF_COLS + ((uint32_t)(q * 32) << 16);
-              tmem_store_4cols(at, __byte_perm(rows[0], 0, pick), __byte_perm(rows[1], 0, pick),
-                               __byte_perm(rows[2], 0, pick), __byte_perm(rows[3], 0, pick));
-              // 32 columns of the tile lie in one block of 128
-              uint32_t w[8];
+          for (int j = 0; j < kGroup; ++j) {
+            const uint32_t pick = j * 0x1111u;  // a byte four times
+            tmem_store_4cols(to + j * Lay::SF_COLS, __byte_perm(rows[0], 0, pick), __byte_perm(rows[1], 0, pick),
+                             __byte_perm(rows[2], 0, pick), __byte_perm(rows[3], 0, pick));
+            // 32 columns of the tile lie in one block of 128
+            const uint32_t lo = __shfl_sync(0xffffffffu, col, j) * 0x01010101u, hi = __shfl_sync(0xffffffffu, col, 4 + j) * 0x01010101u;
+            uint32_t w[8];
 #pragma unroll
-              for (int c = 0; c < Lay::SFB_COLS; ++c)
-                w[c] = __shfl_sync(0xffffffffu, col, ((n0 + 32 * c) / 128 - n0 / 128) % 2 * 4 + half * Lay::BLOCKS + j) * 0x01010101u;
-              tmem_store_4cols(at + Lay::SFA_COLS, w[0], w[1], w[2], w[3]);
-              if (Lay::SFB_COLS > 4) tmem_store_4cols(at + Lay::SFA_COLS + 4, w[4], w[5], w[6], w[7]);
-            }
-            // (The stores to TMEM are complete by now; an arrival that also releases
-            // memory to the cluster would take a thousand cycles.)
-            tmem_store_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if (crank != 0)
-                mbar_arrive_remote(bars.full(s), 0);
-              else
-                mbar_arrive(bars.full(s));
-            }
+            for (int c = 0; c < 8; ++c) w[c] = (n0 + 32 * c) / 128 == n0 / 128 ? lo : hi;
+            tmem_store_4cols(to + j * Lay::SF_COLS + Lay::SFA_COLS, w[0], w[1], w[2], w[3]);
+            if (Lay::SFB_COLS > 4) tmem_store_4cols(to + j * Lay::SF_COLS + Lay::SFA_COLS + 4, w[4], w[5], w[6], w[7]);
+          }
+          // (The stores to TMEM are complete by now; an arrival that also releases
+          // memory to the cluster would take a thousand cycles.)
+          tmem_store_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (crank != 0)
+              mbar_arrive_remote(sfull0 + 8 * slot, 0);
+            else
+              mbar_arrive(sfull0 + 8 * slot);
           }
         }
       }
@@ -361,9 +369,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     setmaxnreg_inc<152>();
     const int q = warp & 3, part = (warp - kFirstSum) >> 2;
     OutDesc o = p.out;
-    o.tma_c = (Lay::STAGING_BYTES > 0 && p.use_tma_store) ? &p.tma_c : nullptr;
-    const uint32_t staging = staging0 + (warp - kFirstSum) * kStageOutBytes;
-    uint32_t seg = 0, chunk = 0;
+    o.tma_c = (Lay::STAGING_BYTES > 0 && p.use_tma_store) ? &p.tma_c : nullptr;  // 16 bits
+    const uint32_t sbuf = staging0 + (warp - kFirstSum) * kStoreBytes;
+    uint32_t seg = 0;
     bool ok = true;
     for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride) {
       const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
@@ -375,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float acc[PART];
 #pragma unroll
       for (int i = 0; i < PART; ++i) acc[i] = 0.0f;
-      for (int st = 0; st < stages; st += Lay::SEGMENT, ++seg) {
+      for (int st = 0; st < stages; st += kSegmentBlocks / Lay::BLOCKS, ++seg) {
         const uint32_t buf = seg % ACC;
         const bool got = mbar_wait_bounded(bars.tfull(buf), (seg / ACC) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                            status_code(6, kSiteEpilogueTmemFull));
@@ -415,14 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * j + i]);
         epilogue_math<PART>(o, j, tb, v, f);
         if (o.tma_c && m0 + 32 <= p.M) {
-          // 4 KB a warp: two 16-bit chunks of 32 x 32 in turn, or one of fp32
-          const uint32_t sbuf = staging + (o.out_f32 ? 0 : (chunk & 1) * (kStageOutBytes / 2));
-          if (lane == 0) {
-            if (o.out_f32)
-              bulk_wait_read_all();
-            else
-              bulk_wait_read_1();
-          }
+          if (lane == 0) bulk_wait_read_all();  // the chunk before has left the buffer
           __syncwarp();
           stage_32(o, sbuf, lane, f);
           fence_proxy_async_smem();
@@ -431,7 +432,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_store_3d(o.tma_c, sbuf, n0 + 32 * j, m0, 0);
             bulk_commit();
           }
-          ++chunk;
         } else {
           store_32_direct(o, 0, m0 + lane, n0 + 32 * j, true, f);
         }
@@ -494,11 +494,12 @@ bi_status launch_scaled_gemm(const ScaledProblem& g, cudaStream_t stream, std::s
   p.M = (int32_t)g.M, p.N = (int32_t)g.N;
   p.m_tiles = (int32_t)((g.M + 2 * kBM - 1) / (2 * kBM));
   p.k_blocks = (int32_t)((g.K + kBK8 - 1) / kBK8);
-  // The width whose last round of tiles wastes least: columns a pair works through,
-  // and something for each tile's start and end; the wider one among equals.
+  // The width whose rounds of tiles take least: a K block takes a pair a time of
+  // about BN + 128 columns' (short A: BN + 64); the wider one among equals.
   const int64_t pairs = dev.num_sms / 2;
   auto tiles = [&](int64_t bn) { return (int64_t)p.m_tiles * ((g.N + bn - 1) / bn); };
-  auto cost = [&](int64_t bn) { return (tiles(bn) + pairs - 1) / pairs * (bn + 16); };
+  const int64_t each = g.M <= kShortARows ? 64 : 128;
+  auto cost = [&](int64_t bn) { return (tiles(bn) + pairs - 1) / pairs * (bn + each); };
   int bn = 192;
   for (int w : {128, 64})
     if (cost(w) < cost(bn)) bn = w;
@@ -520,7 +521,7 @@ bi_status launch_scaled_gemm(const ScaledProblem& g, cudaStream_t stream, std::s
   o.out_f32 = g.c_kind == 2, o.out_f16 = g.c_kind == 1;
   o.vec_store = g.vec_store;
   o.bias_groups = 1, o.tile_rows = kBM;
-  p.use_tma_store = encode_output_map(&p.tma_c, g.c, o.out_f32 != 0, o.out_f16 != 0, 1, g.M, g.N, g.ldc, 0) ? 1 : 0;
+  p.use_tma_store = !o.out_f32 && encode_output_map(&p.tma_c, g.c, false, o.out_f16 != 0, 1, g.M, g.N, g.ldc, 0) ? 1 : 0;
   p.status_word = dev.status_word;
   p.wait_limit_ns = kWaitLimitNs;
   const cudaError_t e = bn == 192 ? launch_width<192>(p, stream) : bn == 128 ? launch_width<128>(p, stream) : launch_width<64>(p, stream);
