@@ -21,13 +21,19 @@
 // The unit is 2^-sh of the largest weight, sh = 62 - ceil(log2 N), at most 46.
 //
 // Work.  A row is a cluster's, a slice of it a CTA's, held in shared memory from
-// the only read of it on.  Prefixes are found by counting: 2048 bins of y (of
-// the bits of x, below) with the number and the weight of their elements, the
-// weight as three sums of 16 bits in 32; the CTAs add up a share of the bins
-// each; the bin where the k-th element, or the given weight, is reached is
-// narrowed to its largest and smallest element, and binned again by their bits
-// until it is one value, of which the first t by index are kept.  The draw sums
-// the kept elements by warps' segments in index order, then looks into one.
+// the only read of it on.  Prefixes are found by counting, once for both limits:
+//   fp32 and fp16  2048 bins of y, each with the number and the weight of its
+//     elements (the weight as three sums of 16 bits in 32).  The elements of the
+//     bin where a limit is reached, a few hundred as a rule, are gathered by every
+//     CTA and sorted; more than 512 are binned again by their bits until one value
+//     or few elements are left.
+//   bf16  a bin for each number of 2^-8 .. 2^6 of either sign: counts alone, whose
+//     weights come from a table of the row's (3584 weights in place of a row's
+//     128256), and a bin that is reached is a value already.  Numbers nearer to
+//     zero share a bin and are weighed one by one; rows with others go the way of
+//     fp32.
+// The CTAs add up a share of the bins each.  The draw sums the kept elements by
+// warps' segments in index order, then looks into one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -40,7 +46,7 @@
 namespace bi {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxWarps = 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCl = 8;
 constexpr float kRange = 62.0f;              // y from here on: weight 0
@@ -62,23 +68,49 @@ constexpr Powers powers() {
 }
 __device__ const Powers kPowers = powers();
 
+constexpr int kList = 512;  // elements of a bin that are sorted
+// bf16: numbers of exponents -8 .. 5, in the order of their values: the positive
+// ones, what lies between, the negative ones.
+constexpr int kBase16 = (127 - 8) << 7, kSpan16 = 14 << 7, kMiddle16 = kSpan16, kBins16 = 2 * kSpan16 + 1;
+__device__ __forceinline__ int bin16(uint32_t bits) {  // -1: outside
+  const int t = (int)(bits & 0x7fffu) - kBase16;
+  if (t < 0) return kMiddle16;
+  if (t >= kSpan16) return -1;
+  return bits & 0x8000u ? kMiddle16 + 1 + t : kSpan16 - 1 - t;
+}
+__device__ __forceinline__ float value16(int bin) {  // (not of the middle)
+  const uint32_t bits = bin < kMiddle16 ? kBase16 + kSpan16 - 1 - bin : (0x8000u | (kBase16 + bin - kMiddle16 - 1));
+  return __uint_as_float(bits << 16);
+}
+
+template <int KIND>
 struct Shared {
   uint64_t table[256];  // 2^40 2^(-j / 256)
-  float tablef[256];    // 2^40 2^(-j / 256) again
-  uint32_t n[kBins], w0[kBins], w1[kBins], w2[kBins];
+  float tablef[256];    // the same
   // written by every CTA of the cluster
-  uint64_t seg_w[kMaxCl * kWarps];
-  uint32_t seg_n[kMaxCl * kWarps];
+  uint64_t seg_w[kMaxCl * kMaxWarps];
+  uint32_t seg_n[kMaxCl * kMaxWarps];
   uint32_t top[kMaxCl], bad[kMaxCl], lo[kMaxCl], hi[kMaxCl];
   uint64_t part_w[kMaxCl];
   uint32_t part_n[kMaxCl];
   uint64_t found_w;
   uint32_t found_n, found_bin, found_count;
+  uint32_t listed;  // the first CTA's counts for all
+  uint64_t list[kList];
   // this CTA's own
-  uint64_t warp_w[kWarps];
-  uint32_t warp_n[kWarps], warp_m[kWarps];
+  uint64_t warp_w[kMaxWarps], middle_w, cut_w;
+  uint32_t warp_n[kMaxWarps], warp_m[kMaxWarps], cut_key, cut_n;
   float ch, cl, floor;
-  int32_t k;
+  // bins: number, and weight in three parts; or for bf16 the number, and the table of weights
+  union {
+    struct {
+      uint32_t n[kBins], w0[kBins], w1[kBins], w2[kBins];
+    };
+    struct {
+      uint64_t weight16[KIND == 0 ? kBins16 : 1];
+      uint32_t n16[KIND == 0 ? kBins16 : 1];
+    };
+  };
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
@@ -121,9 +153,22 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // inclus
   return v;
 }
 
-template <int KIND>
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += x;
+  }
+  return v;
+}
+
+// T threads.  KIND 0: bf16, 1: fp16, 2: fp32.
+template <int KIND, int T>
 struct Row {
-  Shared& sm;
+  static constexpr int kWarps = T / 32;
+  static constexpr int kEach = ((KIND == 0 ? kBins16 : kBins) + T - 1) / T;  // bins of a thread, at most
+
+  Shared<KIND>& sm;
   const unsigned char* x;  // the slice
   int count, first;        // its elements, and the row's index of the first
   int cl, rank, sh;
@@ -145,14 +190,27 @@ struct Row {
     float e = __fmaf_rn(d, ch, -p);
     e = __fmaf_rn(d, lo, e);
     e = __fmaf_rn(dl, ch, e);
-    const int k = __float2int_rn(p * 256.0f);
-    const float r = __fadd_rn(__fmaf_rn(__int2float_rn(k), -1.0f / 256.0f, p), e);
+    // k = RN(256 p) in the low bits of 1.5 * 2^23 + k
+    const float m = __fmaf_rn(p, 256.0f, 12582912.0f);
+    const int k = __float_as_int(m) & 0x3fffff;
+    const float r = __fadd_rn(__fmaf_rn(__fsub_rn(m, 12582912.0f), -1.0f / 256.0f, p), e);
     const float a = r * -0.693147180559945f;
     const float g = a * fmaf(a, fmaf(a, fmaf(a, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), 1.0f);
     const int j = k & 255, i = k >> 8;
     uint64_t w = sm.table[j] + (int64_t)__float2int_rn(g * sm.tablef[j]);
     w <<= sh - 40;
     return (w + (((uint64_t)1 << i) >> 1)) >> i;
+  }
+  // The same from the row's table where there is one.
+  __device__ __forceinline__ uint64_t weight_at(int i, float v, bool tabled) const {
+    if constexpr (KIND == 0) {
+      if (tabled) {
+        const int b = bin16(__float_as_uint(v) >> 16);
+        if (b < 0) return 0;
+        if (b != kMiddle16) return sm.weight16[b];
+      }
+    }
+    return weight(v);
   }
 
   // --- exchanges: one value of this CTA to all, then a barrier of the cluster
@@ -168,8 +226,9 @@ struct Row {
     return __reduce_max_sync(0xffffffffu, lane < kWarps ? sm.warp_m[lane] : 0u);
   }
 
+  // --- bins of y or of bits
   __device__ __forceinline__ void clear_bins() const {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sm.n[i] = sm.w0[i] = sm.w1[i] = sm.w2[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += T) sm.n[i] = sm.w0[i] = sm.w1[i] = sm.w2[i] = 0;
     __syncthreads();
   }
   __device__ __forceinline__ void into_bin(int b, float v, bool weigh) const {
@@ -182,68 +241,80 @@ struct Row {
     }
   }
 
-  // The bin where the running count (or weight) over all CTAs' bins reaches what
-  // is left of the target: its number and count; n and w get what lies before
-  // it.  False if the bins hold less (then the same in every CTA).
-  __device__ __forceinline__ bool find_bin(bool by_weight, uint64_t target, uint32_t& n, uint64_t& w, int& bin,
-                                           uint32_t& in_bin) const {
+  // What a thread knows of the cluster's bins: its own ones', and before them.
+  struct Scan {
+    uint32_t bn[kEach], cn, all_n;
+    uint64_t bw[kEach], cw, all_w;
+    int base, each;  // its first bin, and how many
+  };
+  // Adds every CTA's bins up, a share a CTA, starting from (n, w).
+  template <class F>
+  __device__ __forceinline__ void scan_bins(int bins, uint32_t n, uint64_t w, Scan& s, F fetch) const {
     cluster_sync_all();  // every CTA's bins are counted
-    const int per = kBins / cl, each = max(1, per / kThreads), mine = threadIdx.x * each;
-    uint32_t bn[kBins / kThreads], sn = 0;
-    uint64_t bw[kBins / kThreads], sw = 0;
+    const int per = (bins + cl - 1) / cl, end = min(bins, (rank + 1) * per);
+    s.each = (per + T - 1) / T;
+    s.base = rank * per + (int)threadIdx.x * s.each;
+    uint32_t sn = 0;
+    uint64_t sw = 0;
 #pragma unroll
-    for (int i = 0; i < kBins / kThreads; ++i) {
-      bn[i] = 0, bw[i] = 0;
-      if (i < each && mine + i < per) {
-        const int b = rank * per + mine + i;
-        for (int r = 0; r < cl; ++r) {
-          bn[i] += ld_cluster_u32(smem_u32(&sm.n[b]), r);
-          bw[i] += (uint64_t)ld_cluster_u32(smem_u32(&sm.w0[b]), r) + ((uint64_t)ld_cluster_u32(smem_u32(&sm.w1[b]), r) << 16) +
-                   ((uint64_t)ld_cluster_u32(smem_u32(&sm.w2[b]), r) << 32);
-        }
-      }
-      sn += bn[i], sw += bw[i];
+    for (int i = 0; i < kEach; ++i) {
+      s.bn[i] = 0, s.bw[i] = 0;
+      if (i < s.each && s.base + i < end) fetch(s.base + i, s.bn[i], s.bw[i]);
+      sn += s.bn[i], sw += s.bw[i];
     }
-    // running sums over the threads
-    uint32_t cn = sn;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, cn, d);
-      if (lane >= d) cn += y;
-    }
+    uint32_t cn = warp_scan(sn, lane);
     uint64_t cw = warp_scan(sw, lane);
     if (lane == 31) sm.warp_n[warp] = cn, sm.warp_w[warp] = cw;
     __syncthreads();
-    uint32_t all_n = 0;
-    uint64_t all_w = 0;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i == warp) cn += all_n, cw += all_w;
-      all_n += sm.warp_n[i], all_w += sm.warp_w[i];
-    }
+    uint32_t all_n = lane < kWarps ? sm.warp_n[lane] : 0;
+    uint64_t all_w = lane < kWarps ? sm.warp_w[lane] : 0;
+    all_n = warp_scan(all_n, lane), all_w = warp_scan(all_w, lane);
+    const uint32_t before_n = __shfl_sync(0xffffffffu, all_n, max(warp - 1, 0));
+    const uint64_t before_w = __shfl_sync(0xffffffffu, all_w, max(warp - 1, 0));
+    if (warp > 0) cn += before_n, cw += before_w;
+    all_n = __shfl_sync(0xffffffffu, all_n, 31), all_w = __shfl_sync(0xffffffffu, all_w, 31);
     to_all([&](int r) {
       st_cluster_u32(&sm.part_n[rank], r, all_n);
       st_cluster_u64(&sm.part_w[rank], r, all_w);
     });
     cluster_sync_all();
-    uint64_t sum_n = n, sum_w = w;
     for (int r = 0; r < cl; ++r) {
-      if (r == rank) cn += (uint32_t)sum_n, cw += sum_w;
-      sum_n += sm.part_n[r], sum_w += sm.part_w[r];
+      if (r == rank) s.cn = cn - sn + n, s.cw = cw - sw + w;
+      n += sm.part_n[r], w += sm.part_w[r];
     }
-    if ((by_weight ? sum_w : sum_n) < target) return false;
-    cn -= sn, cw -= sw;  // before this thread's
+    s.all_n = n, s.all_w = w;
+  }
+  __device__ __forceinline__ void scan_bins(uint32_t n, uint64_t w, bool weigh, Scan& s) const {
+    scan_bins(kBins, n, w, s, [&](int b, uint32_t& bn, uint64_t& bw) {
+      for (int r = 0; r < cl; ++r) {
+        bn += ld_cluster_u32(smem_u32(&sm.n[b]), r);
+        if (weigh)
+          bw += (uint64_t)ld_cluster_u32(smem_u32(&sm.w0[b]), r) + ((uint64_t)ld_cluster_u32(smem_u32(&sm.w1[b]), r) << 16) +
+                ((uint64_t)ld_cluster_u32(smem_u32(&sm.w2[b]), r) << 32);
+      }
+    });
+  }
+  // The bin where the running count, or weight, reaches the target: its number and
+  // count; n and w get what lies before it.  False if all of them hold less (the
+  // same in every CTA).
+  __device__ __forceinline__ bool find_bin(const Scan& s, bool by_weight, uint64_t target, uint32_t& n, uint64_t& w, int& bin,
+                                           uint32_t& in_bin) const {
+    if ((by_weight ? s.all_w : (uint64_t)s.all_n) < target) return false;
+    uint32_t cn = s.cn;
+    uint64_t cw = s.cw;
 #pragma unroll
-    for (int i = 0; i < kBins / kThreads; ++i) {
-      const uint64_t from = by_weight ? cw : cn, to = by_weight ? cw + bw[i] : cn + bn[i];
-      if (from < target && to >= target)
+    for (int i = 0; i < kEach; ++i) {
+      const uint64_t from = by_weight ? cw : cn, to = by_weight ? cw + s.bw[i] : cn + s.bn[i];
+      if (i < s.each && from < target && to >= target)
         for (int r = 0; r < cl; ++r) {
-          st_cluster_u32(&sm.found_bin, r, (uint32_t)(rank * per + mine + i));
-          st_cluster_u32(&sm.found_count, r, bn[i]);
+          st_cluster_u32(&sm.found_bin, r, (uint32_t)(s.base + i));
+          st_cluster_u32(&sm.found_count, r, s.bn[i]);
           st_cluster_u32(&sm.found_n, r, cn);
           st_cluster_u64(&sm.found_w, r, cw);
         }
-      cn += bn[i], cw += bw[i];
+      cn += s.bn[i], cw += s.bw[i];
     }
+    if (threadIdx.x == 0) sm.listed = 0;
     cluster_sync_all();
     bin = (int)sm.found_bin, in_bin = sm.found_count;
     n = sm.found_n, w = sm.found_w;
@@ -254,7 +325,7 @@ struct Row {
   template <class F>
   __device__ __forceinline__ void range_of(F in, uint32_t& kmin, uint32_t& kmax) const {
     uint32_t hi = 0, lo_inv = 0;
-    for (int i = threadIdx.x; i < count; i += kThreads) {
+    for (int i = threadIdx.x; i < count; i += T) {
       const float v = at(i);
       const uint32_t k = key_of(v);
       if (in(v, k)) hi = max(hi, k), lo_inv = max(lo_inv, ~k);
@@ -271,75 +342,138 @@ struct Row {
     kmax = hi, kmin = ~lo_inv;
   }
 
-  // The shortest prefix that holds `target` elements (of weight above 0), or the
-  // weight `target`: all above the value, and its first `ties`.  sum: the
-  // prefix's weight, if `weigh`.  False if there is less.
-  __device__ __forceinline__ bool prefix(bool by_weight, bool weigh, uint64_t target, float& value, uint32_t& ties,
-                                         uint64_t& sum) const {
-    uint32_t n = 0, in_bin;
-    uint64_t w = 0;
-    int bin;
-    clear_bins();
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-      const float v = at(i), y = bits_below(v);
-      if (y < kRange) into_bin((int)(y * kBinsPerBit), v, weigh);
+  // Where in a bin of at most kList elements, which `in` holds for, the target is
+  // reached: every CTA gathers and sorts them, by value and then by index.
+  template <class F>
+  __device__ __forceinline__ void within_list(F in, uint32_t size, bool by_weight, bool weigh, uint64_t target, uint32_t n,
+                                              uint64_t w, float& value, uint32_t& ties, uint64_t& sum) const {
+    int m = 32;  // what is sorted: a power of two
+    while (m < (int)size) m *= 2;
+    for (int i0 = warp * 32; i0 < count; i0 += T) {
+      const int i = i0 + lane;
+      const float v = i < count ? at(i) : 0.0f;
+      const uint32_t k = key_of(v);
+      const bool hit = i < count && in(v, k);
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (hits) {
+        uint32_t at0 = 0;
+        if (lane == 0)
+          asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                       : "=r"(at0)
+                       : "r"(cluster_map_shared(smem_u32(&sm.listed), 0)), "r"((uint32_t)__popc(hits))
+                       : "memory");
+        at0 = __shfl_sync(0xffffffffu, at0, 0) + __popc(hits & ((1u << lane) - 1));
+        if (hit && at0 < (uint32_t)kList)
+          for (int r = 0; r < cl; ++r)
+            st_cluster_u64(&sm.list[at0], r, (uint64_t)k << 32 | (0xffffffffu - (uint32_t)(first + i)));
+      }
     }
-    if (!find_bin(by_weight, target, n, w, bin, in_bin)) return false;
+    for (int i = (int)size + (int)threadIdx.x; i < m; i += T) sm.list[i] = 0;
+    cluster_sync_all();
+    for (int k = 2; k <= m; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        const int i = threadIdx.x;
+        if (i < m && (i ^ j) > i) {
+          const uint64_t a = sm.list[i], b = sm.list[i ^ j];
+          if ((a < b) == ((i & k) == 0)) sm.list[i] = b, sm.list[i ^ j] = a;
+        }
+        __syncthreads();
+      }
+    // running weights, a thread an element
+    const int i = threadIdx.x;
+    const bool there = i < (int)size;
+    const uint64_t e = there ? sm.list[i] : 0;
+    const uint32_t key = (uint32_t)(e >> 32);
+    const uint64_t own = there && weigh ? weight(of_key(key)) : 0;
+    uint64_t upto = warp_scan(own, lane);
+    if (lane == 31) sm.warp_w[warp] = upto;
+    __syncthreads();
+    for (int k = 0; k < min(warp, kList / 32); ++k) upto += sm.warp_w[k];
+    upto += w;
+    const uint64_t to = by_weight ? upto : (uint64_t)n + i + 1, from = by_weight ? upto - own : (uint64_t)n + i;
+    if (there && from < target && to >= target) {
+      int same = i;  // the first element of its value
+      while (same > 0 && (uint32_t)(sm.list[same - 1] >> 32) == key) --same;
+      sm.cut_key = key, sm.cut_n = i - same + 1, sm.cut_w = upto;
+    }
+    __syncthreads();
+    value = of_key(sm.cut_key), ties = sm.cut_n, sum = sm.cut_w;
+  }
+
+  // Where in a bin the target is reached: everything above `value`, and its first
+  // `ties`; sum: the weight of that, if `weigh`.
+  __device__ __forceinline__ void within_bin(int bin, uint32_t in_bin, bool by_weight, bool weigh, uint64_t target, uint32_t n,
+                                             uint64_t w, float& value, uint32_t& ties, uint64_t& sum) const {
+    auto in_y = [&](float v, uint32_t) {
+      const float y = bits_below(v);
+      return y < kRange && (int)(y * kBinsPerBit) == bin;
+    };
+    if (in_bin <= kList) return within_list(in_y, in_bin, by_weight, weigh, target, n, w, value, ties, sum);
     uint32_t kmin, kmax;
-    range_of([&](float v, uint32_t) { const float y = bits_below(v); return y < kRange && (int)(y * kBinsPerBit) == bin; },
-             kmin, kmax);
+    range_of(in_y, kmin, kmax);
     while (kmin != kmax) {
       const int bits = 32 - __clz(kmax - kmin), shift = max(0, bits - 11);
       clear_bins();
-      for (int i = threadIdx.x; i < count; i += kThreads) {
+      for (int i = threadIdx.x; i < count; i += T) {
         const float v = at(i);
         const uint32_t k = key_of(v);
         if (k >= kmin && k <= kmax) into_bin((int)((kmax - k) >> shift), v, weigh);
       }
-      find_bin(by_weight, target, n, w, bin, in_bin);  // (there is one: the bin before held it)
+      Scan s;
+      scan_bins(n, w, weigh, s);
+      find_bin(s, by_weight, target, n, w, bin, in_bin);  // (there is one: the bin before held it)
       const uint32_t hi = kmax - ((uint32_t)bin << shift);
-      if (shift == 0) {
+      const uint32_t width = (1u << shift) - 1, low = hi - kmin > width ? hi - width : kmin;
+      auto in_keys = [&](float, uint32_t k) { return k >= low && k <= hi; };
+      if (shift > 0 && in_bin <= kList) return within_list(in_keys, in_bin, by_weight, weigh, target, n, w, value, ties, sum);
+      if (shift == 0)
         kmin = kmax = hi;
-      } else {
-        const uint32_t width = (1u << shift) - 1, low = hi - kmin > width ? hi - width : kmin;
-        range_of([&](float, uint32_t k) { return k >= low && k <= hi; }, kmin, kmax);
-      }
+      else
+        range_of(in_keys, kmin, kmax);
     }
     value = of_key(kmax);
     const uint64_t each = weigh ? weight(value) : 0;
     ties = (uint32_t)(by_weight ? (target - w + each - 1) / each : target - n);
     sum = w + ties * each;
-    return true;
   }
 };
 
-template <int KIND>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int cl, int slice, int sh) {
-  constexpr int E = KIND == 2 ? 4 : 2;
+template <int KIND, int T>
+__global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams p, int cl, int slice, int sh) {
+  constexpr int E = KIND == 2 ? 4 : 2, kWarps = T / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
-  Shared& sm = *reinterpret_cast<Shared*>(dyn);
+  Shared<KIND>& sm = *reinterpret_cast<Shared<KIND>*>(dyn);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r = blockIdx.x / (unsigned)cl;
   const int rank = (int)(blockIdx.x % (unsigned)cl), first = min(p.N, rank * slice), count = min(p.N - first, slice);
 
+  // --- the row's settings
+  const float u = __ldg(p.u + r), t_in = p.temperature ? __ldg(p.temperature + r) : 1.0f;
+  const float top_p = p.top_p ? __ldg(p.top_p + r) : 1.0f, min_p = p.min_p ? __ldg(p.min_p + r) : 0.0f;
+  const int top_k = p.top_k ? __ldg(p.top_k + r) : 0;
+  const bool settings = u >= 0.0f && u < 1.0f && t_in >= 0.0f && t_in <= 1048576.0f && top_p == top_p && min_p == min_p;
+  // Temperatures below 2^-20 take the most likely token: the first of the largest.
+  const bool greedy = t_in < 9.5367431640625e-7f || top_k == 1 || top_p <= 0.0f;
+  const bool by_k = !greedy && top_k > 0 && top_k < p.N, by_p = !greedy && top_p < 1.0f;
+
   // --- the slice, at its address's place in a 16-byte unit
   const unsigned char* src = static_cast<const unsigned char*>(p.x) + (r * p.ld_x + first) * E;
   const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15), end = off + count * E;
-  unsigned char* data = dyn + (sizeof(Shared) + 15) / 16 * 16;
+  unsigned char* data = dyn + (sizeof(Shared<KIND>) + 15) / 16 * 16;
   float top = -INFINITY;
   bool bad = false;
   auto look = [&](float v) { top = fmaxf(top, v), bad |= !(v < INFINITY); };
   constexpr int U = 8;
-  for (int u0 = threadIdx.x; 16 * u0 < end; u0 += U * kThreads) {
+  for (int u0 = threadIdx.x; 16 * u0 < end; u0 += U * T) {
     uint4 v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int at = 16 * (u0 + i * kThreads);
+      const int at = 16 * (u0 + i * T);
       if (at >= off && at + 16 <= end) v[i] = __ldcs(reinterpret_cast<const uint4*>(src - off + at));
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int at = 16 * (u0 + i * kThreads);
+      const int at = 16 * (u0 + i * T);
       if (at >= off && at + 16 <= end) {
         *reinterpret_cast<uint4*>(data + at) = v[i];
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -365,13 +499,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }
     }
   }
-  // --- the row's settings, once a CTA
-  if (threadIdx.x < 256) {
-    const uint64_t t = kPowers.v[threadIdx.x];
-    sm.table[threadIdx.x] = t;
-    sm.tablef[threadIdx.x] = (float)t;
+  for (int i = threadIdx.x; i < 256; i += T) {
+    const uint64_t t = kPowers.v[i];
+    sm.table[i] = t;
+    sm.tablef[i] = (float)t;
   }
-  Row<KIND> row{sm, data + off, count, first, cl, rank, sh, 0.0f, 0.0f, 0.0f, warp, lane};
+  if constexpr (KIND == 0) {
+    if (by_k || by_p) {
+      for (int i = threadIdx.x; i < kBins16; i += T) sm.n16[i] = 0;
+      if (threadIdx.x == 0) sm.middle_w = 0;
+    }
+  } else if (by_k || by_p) {
+    for (int i = threadIdx.x; i < kBins; i += T) sm.n[i] = sm.w0[i] = sm.w1[i] = sm.w2[i] = 0;
+  }
+  double below = 0.0;  // how far below the largest logit min_p reaches
+  if (threadIdx.x == T - 1) {
+    const double temp = greedy ? 1.0 : (double)t_in, c = 1.4426950408889634074 / temp;
+    sm.ch = (float)c;
+    sm.cl = (float)(c - (double)sm.ch);
+    if (min_p > 0.0f && min_p < 1.0f) below = temp * log((double)min_p);
+  }
+  Row<KIND, T> row{sm, data + off, count, first, cl, rank, sh, 0.0f, 0.0f, 0.0f, warp, lane};
   {
     const uint32_t k = row.block_max(key_of(top)), b = row.block_max(bad ? 1u : 0u);
     row.to_all([&](int to) {
@@ -383,10 +531,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   uint32_t key = 0, spoiled = 0;
   for (int i = 0; i < cl; ++i) key = max(key, sm.top[i]), spoiled |= sm.bad[i];
   top = of_key(key);
-  const float u = __ldg(p.u + r), t_in = p.temperature ? __ldg(p.temperature + r) : 1.0f;
-  const float top_p = p.top_p ? __ldg(p.top_p + r) : 1.0f, min_p = p.min_p ? __ldg(p.min_p + r) : 0.0f;
-  int top_k = p.top_k ? __ldg(p.top_k + r) : 0;
-  const bool settings = u >= 0.0f && u < 1.0f && t_in >= 0.0f && t_in <= 1048576.0f && top_p == top_p && min_p == min_p;
   if (!settings || spoiled || top == -INFINITY) {  // the same in every CTA of the cluster
     if (rank == 0 && threadIdx.x == 0) {
       if (!settings) record_failure(p.status_word, status_code(BI_ERR_INVALID_ARG, kSiteSample));
@@ -397,56 +541,111 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     return;
   }
-  // Temperatures below 2^-20 take the most likely token: the first of the largest.
-  const bool greedy = t_in < 9.5367431640625e-7f || top_k == 1 || top_p <= 0.0f;
-  if (threadIdx.x == 0) {
-    const double T = greedy ? 1.0 : (double)t_in, c = 1.4426950408889634074 / T;
-    sm.ch = (float)c;
-    sm.cl = (float)(c - (double)sm.ch);
-    float f = -INFINITY;  // the smallest logit that min_p keeps
-    if (min_p > 0.0f) {
-      const double d = min_p >= 1.0f ? (double)top : (double)top + T * log((double)min_p);
-      f = __double2float_ru(d);
+  if (threadIdx.x == T - 1)  // the smallest logit that min_p keeps
+    sm.floor = min_p > 0.0f ? __double2float_ru((double)top + below) : -INFINITY;
+  row.top = top, row.ch = sm.ch, row.lo = sm.cl;
+
+  // --- bf16: the row's weights by value, if its numbers that have any are in the bins
+  bool tabled = false;
+  if constexpr (KIND == 0) {
+    const float far = top - kRange / row.ch;  // (what rounding leaves out there weighs nothing)
+    tabled = !greedy && top < 64.0f && far > -64.0f;
+    if (tabled) {
+      for (int b = threadIdx.x; b < kBins16; b += T) {
+        const float v = value16(b);
+        sm.weight16[b] = b == kMiddle16 || v > top ? 0 : row.weight(v);
+      }
     }
-    sm.floor = f;
   }
   __syncthreads();
-  row.top = top, row.ch = sm.ch, row.lo = sm.cl;
+
   float cut = sm.floor;
   uint32_t ties = 0xffffffffu;
+  auto lower = [&](float v, uint32_t n) {  // what is kept is what both limits keep
+    if (v < cut) return;
+    ties = v > cut || n < ties ? n : ties;
+    cut = v;
+  };
   if (greedy) {
     cut = top, ties = 1;
-  } else {
-    const bool by_k = top_k > 0 && top_k < p.N, by_p = top_p < 1.0f;
+  } else if (by_k || by_p) {
+    typename Row<KIND, T>::Scan s;
     float v;
-    uint32_t n;
-    uint64_t sum = 0;
-    bool some = false;
-    if (by_k) {
-      some = row.prefix(false, by_p, (uint64_t)top_k, v, n, sum);
-      if (some && v >= cut) {
-        ties = v > cut || n < ties ? n : ties;
-        cut = v;
+    uint32_t n = 0, m, in_bin;
+    uint64_t w = 0, sum = 0;
+    int bin;
+    bool done = false;
+    if constexpr (KIND == 0) {
+      if (tabled) {
+        uint64_t mine = 0;
+        for (int i = threadIdx.x; i < count; i += T) {
+          const uint32_t bits = reinterpret_cast<const uint16_t*>(row.x)[i];
+          const int b = bin16(bits);
+          if (b >= 0) atomicAdd(&sm.n16[b], 1u);  // (others have no weight)
+          if (b == kMiddle16) mine += row.weight(__uint_as_float(bits << 16));
+        }
+        if (__any_sync(0xffffffffu, mine != 0)) {
+          mine = warp_sum(mine);
+          if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.middle_w), (unsigned long long)mine);
+        }
+        row.scan_bins(kBins16, 0, 0, s, [&](int b, uint32_t& bn, uint64_t& bw) {
+          for (int c = 0; c < cl; ++c) bn += ld_cluster_u32(smem_u32(&sm.n16[b]), c);
+          if (b != kMiddle16)
+            bw = bn * sm.weight16[b];
+          else
+            for (int c = 0; c < cl; ++c) {
+              const uint32_t a = smem_u32(&sm.middle_w);
+              bw += (uint64_t)ld_cluster_u32(a, c) | (uint64_t)ld_cluster_u32(a + 4, c) << 32;
+            }
+        });
+        done = true;
+        const uint64_t all = s.all_w;
+        sum = all;
+        if (by_k && row.find_bin(s, false, (uint64_t)top_k, n, w, bin, in_bin)) {
+          if (bin == kMiddle16) {
+            done = false;
+          } else {
+            m = (uint32_t)top_k - n;
+            sum = w + m * sm.weight16[bin];
+            if (sm.weight16[bin] > 0) lower(value16(bin), m);
+          }
+        }
+        if (done && by_p) {
+          const uint64_t want = min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
+          if (row.find_bin(s, true, want, n, w, bin, in_bin)) {
+            if (bin == kMiddle16) {
+              done = false;
+            } else {
+              const uint64_t each = sm.weight16[bin];
+              lower(value16(bin), (uint32_t)((want - w + each - 1) / each));
+            }
+          }
+        }
+        if (!done) {
+          cut = sm.floor, ties = 0xffffffffu;
+          tabled = false;
+          cluster_sync_all();  // every CTA has read the others' counts
+        }
       }
+      if (!done) row.clear_bins();
     }
-    if (by_p) {
-      if (!some) {  // all of the row
-        uint64_t s = 0;
-        for (int i = threadIdx.x; i < count; i += kThreads) s += row.weight(row.at(i));
-        s = warp_sum(s);
-        if (lane == 0) sm.warp_w[warp] = s;
-        __syncthreads();
-        s = 0;
-        for (int i = 0; i < kWarps; ++i) s += sm.warp_w[i];
-        row.to_all([&](int to) { st_cluster_u64(&sm.part_w[rank], to, s); });
-        cluster_sync_all();
-        for (int i = 0; i < cl; ++i) sum += sm.part_w[i];
-        cluster_sync_all();  // read by all before it is written again
+    if (!done) {
+      for (int i = threadIdx.x; i < count; i += T) {
+        const float x = row.at(i), y = row.bits_below(x);
+        if (y < kRange) row.into_bin((int)(y * kBinsPerBit), x, by_p);
       }
-      const uint64_t want = min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
-      if (row.prefix(true, true, want, v, n, sum) && v >= cut) {
-        ties = v > cut || n < ties ? n : ties;
-        cut = v;
+      row.scan_bins(0, 0, by_p, s);
+      sum = s.all_w;
+      if (by_k && row.find_bin(s, false, (uint64_t)top_k, n, w, bin, in_bin)) {
+        row.within_bin(bin, in_bin, false, by_p, (uint64_t)top_k, n, w, v, m, sum);
+        lower(v, m);
+      }
+      if (by_p) {
+        const uint64_t want = min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
+        if (row.find_bin(s, true, want, n, w, bin, in_bin)) {
+          row.within_bin(bin, in_bin, true, true, want, n, w, v, m, sum);
+          lower(v, m);
+        }
       }
     }
   }
@@ -458,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     for (int i = from + lane; i < to; i += 32) {
       const float v = row.at(i);
       if (v > cut)
-        w += row.weight(v);
+        w += row.weight_at(i, v, tabled);
       else if (v == cut)
         ++n;
     }
@@ -477,23 +676,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
   cluster_sync_all();
   const uint64_t each = cut > -INFINITY ? row.weight(cut) : 0;
-  uint64_t all = 0;
-  uint32_t seen = 0;  // elements at the cut so far
-  for (int s = 0; s < cl * kWarps; ++s) {
-    const uint32_t n = min(sm.seg_n[s], ties - seen);
-    all += sm.seg_w[s] + n * each;
-    seen += n;
+  // running sums of all segments, some a lane: first of the elements at the cut, which are kept in index order
+  const int segs = cl * kWarps, per = (segs + 31) / 32;
+  uint32_t tied = 0;
+  for (int i = lane * per; i < min(segs, lane * per + per); ++i) tied += sm.seg_n[i];
+  uint32_t seen = warp_scan(tied, lane) - tied;
+  const uint32_t seen0 = min(seen, ties);
+  uint64_t mine = 0;
+  seen = seen0;
+  for (int i = lane * per; i < min(segs, lane * per + per); ++i) {
+    const uint32_t n = min(sm.seg_n[i], ties - seen);
+    mine += sm.seg_w[i] + n * each, seen += n;
   }
+  uint64_t run = warp_scan(mine, lane);
+  const uint64_t all = __shfl_sync(0xffffffffu, run, 31);
   const uint64_t want = min(all - 1, (uint64_t)((double)u * (double)all));
-  uint64_t run = 0;
-  int seg = 0;
-  seen = 0;
-  for (;; ++seg) {
+  const int hit = __ffs(__ballot_sync(0xffffffffu, run > want)) - 1;
+  run -= mine, seen = seen0;
+  int seg = lane * per;
+  for (; seg + 1 < min(segs, lane * per + per); ++seg) {
     const uint32_t n = min(sm.seg_n[seg], ties - seen);
     const uint64_t w = sm.seg_w[seg] + n * each;
-    if (run + w > want || seg + 1 == cl * kWarps) break;
+    if (run + w > want) break;
     run += w, seen += n;
   }
+  seg = __shfl_sync(0xffffffffu, seg, hit);
+  run = __shfl_sync(0xffffffffu, run, hit);
+  seen = __shfl_sync(0xffffffffu, seen, hit);
   if (seg / kWarps != rank) return;  // no CTA reads another's memory from here on
   // the segment's parts, a warp each
   const int from = min(count, (seg % kWarps) * len), to = min(count, from + len);
@@ -513,10 +722,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   for (int i = a; i < b; i += 32) {
     const float v = i + lane < b ? row.at(i + lane) : -INFINITY;
     const bool tie = i + lane < b && v == cut;
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+    const uint32_t tied_lanes = __ballot_sync(0xffffffffu, tie);
     uint64_t m = 0;
-    if (v > cut) m = row.weight(v);
-    if (tie && (uint32_t)__popc(tied & ((1u << lane) - 1)) < ties - seen) m = each;
+    if (v > cut) m = row.weight_at(i + lane, v, tabled);
+    if (tie && (uint32_t)__popc(tied_lanes & ((1u << lane) - 1)) < ties - seen) m = each;
     const uint64_t upto = run + warp_scan(m, lane);
     const uint32_t over = __ballot_sync(0xffffffffu, upto > want);
     if (over) {
@@ -530,29 +739,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       return;
     }
     run = __shfl_sync(0xffffffffu, upto, 31);
-    seen += min((uint32_t)__popc(tied), ties - seen);
+    seen += min((uint32_t)__popc(tied_lanes), ties - seen);
   }
 }
 
-template <int KIND>
-cudaError_t launch(const SampleParams& p, cudaStream_t stream) {
+template <int KIND, int T>
+cudaError_t launch(const SampleParams& p, int cl, cudaStream_t stream) {
   constexpr int E = KIND == 2 ? 4 : 2;
-  constexpr int kHead = (sizeof(Shared) + 15) / 16 * 16 + 16;
+  constexpr int kHead = (sizeof(Shared<KIND>) + 15) / 16 * 16 + 16;
   constexpr int kMost = kHead + (int)(kMaxVocab / kMaxCl) * E;
   static_assert(kMost <= 232448, "shared memory of a CTA");
   static_assert(kMaxVocab / kMaxCl <= 65536, "three 16-bit sums of a slice fit 32 bits");
-  // Slices of at most 16384 elements while a cluster of eight has them.
-  int cl = 1;
-  while (cl < kMaxCl && p.N > 16384 * cl) cl *= 2;
   const int slice = ((p.N + cl - 1) / cl + 7) / 8 * 8;  // (16 bytes keep their place)
   int bits = 0;
   while ((1 << bits) < p.N) ++bits;
-  const void* fn = reinterpret_cast<const void*>(&sample_kernel<KIND>);
-  cudaError_t e = set_smem_once(fn, kMost, 130 + KIND);
+  const void* fn = reinterpret_cast<const void*>(&sample_kernel<KIND, T>);
+  cudaError_t e = set_smem_once(fn, kMost, (T == 1024 ? 133 : 130) + KIND);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.R * cl));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = kHead + slice * E;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {};
@@ -562,7 +768,16 @@ cudaError_t launch(const SampleParams& p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<KIND>, p, cl, slice, std::min(46, 62 - bits));
+  return cudaLaunchKernelEx(&cfg, sample_kernel<KIND, T>, p, cl, slice, std::min(46, 62 - bits));
+}
+
+template <int KIND>
+cudaError_t launch(const SampleParams& p, int num_sms, cudaStream_t stream) {
+  // Slices of at most 16384 elements while a cluster of eight has them.
+  int cl = 1;
+  while (cl < kMaxCl && p.N > 16384 * cl) cl *= 2;
+  // An SM to each CTA: twice the threads, half the time of a pass.
+  return p.R * cl <= num_sms ? launch<KIND, 1024>(p, cl, stream) : launch<KIND, 512>(p, cl, stream);
 }
 
 }  // namespace
@@ -572,7 +787,9 @@ bi_status launch_sample(SampleParams& p, cudaStream_t stream, std::string* why) 
   const bi_status st = current_device_info(&dev, why);
   if (st != BI_OK) return st;
   p.status_word = dev.status_word;
-  const cudaError_t e = p.x_kind == 2 ? launch<2>(p, stream) : p.x_kind == 1 ? launch<1>(p, stream) : launch<0>(p, stream);
+  const cudaError_t e = p.x_kind == 2   ? launch<2>(p, dev.num_sms, stream)
+                        : p.x_kind == 1 ? launch<1>(p, dev.num_sms, stream)
+                                        : launch<0>(p, dev.num_sms, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     *why = std::string("sampling launch: ") + cudaGetErrorString(e);
