@@ -14,11 +14,13 @@
 // e^(z - max z) as a 64-bit integer, good to about 2^-33 of itself, and sums of
 // integers do not depend on their order: not on the split of a row, not on the
 // atomics that count, not on the batch.
-//   e^(z - max) = 2^-y, y = (max - x) log2(e) / T in pairs of fp32 (difference
-//   and product with their exact errors); y = k / 256 + r; the table's
-//   2^(-(k mod 256) / 256) to 2^-41, times a polynomial of r ln 2 < 2^-9.5, whose
-//   fp32 roundings are 2^-24 of it; shifted by k / 256.
-// The unit is 2^-sh of the largest weight, sh = 62 - ceil(log2 N), at most 46.
+//   e^(z - max) = 2^-y, y = Y - x c, c = log2(e) / T in two fp32, Y = max c cut to
+//   a multiple of 1/256 (every weight of a row then has the same factor 2^(Y - max c)
+//   too much).  The product with its exact error; y = k / 256 - f, f below 2^-8, from
+//   differences that fp32 has exactly; the table's 2^(-(k mod 256) / 256) to 2^-41,
+//   times a polynomial of f ln 2, whose fp32 roundings are 2^-24 of it; shifted by k /
+//   256.  Rows whose largest |max c| is 8000 or more take the difference first.
+// The unit is 2^-40 of the largest weight.
 //
 // Work.  A row is a cluster's, a slice of it a CTA's, held in shared memory from
 // the only read of it on.  Prefixes are found by counting, once for both limits:
@@ -49,7 +51,8 @@ namespace {
 constexpr int kMaxWarps = 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCl = 8;
-constexpr float kRange = 62.0f;              // y from here on: weight 0
+constexpr float kRange = 62.0f;               // y from here on: weight 0
+constexpr float kMagic = 12582912.0f;         // 1.5 * 2^23: added, it leaves an integer in the low bits
 constexpr float kBinsPerBit = kBins / 64.0f;  // kRange of them end below kBins
 
 // 2^40 2^(-j / 256), by repeated multiplication: off by 256 roundings of 2^-53 at
@@ -68,7 +71,7 @@ constexpr Powers powers() {
 }
 __device__ const Powers kPowers = powers();
 
-constexpr int kList = 512;  // elements of a bin that are sorted
+constexpr int kList = 512, kShort = 128;  // elements of a bin that are sorted; by rank
 // bf16: numbers of exponents -8 .. 5, in the order of their values: the positive
 // ones, what lies between, the negative ones.
 constexpr int kBase16 = (127 - 8) << 7, kSpan16 = 14 << 7, kMiddle16 = kSpan16, kBins16 = 2 * kSpan16 + 1;
@@ -86,13 +89,10 @@ __device__ __forceinline__ float value16(int bin) {  // (not of the middle)
 template <int KIND>
 struct Shared {
   uint64_t table[256];  // 2^40 2^(-j / 256)
-  float tablef[256];    // the same
   // written by every CTA of the cluster
-  uint64_t seg_w[kMaxCl * kMaxWarps];
-  uint32_t seg_n[kMaxCl * kMaxWarps];
-  uint32_t top[kMaxCl], bad[kMaxCl], lo[kMaxCl], hi[kMaxCl];
-  uint64_t part_w[kMaxCl];
-  uint32_t part_n[kMaxCl];
+  uint32_t top[kMaxCl], lo[kMaxCl], hi[kMaxCl];
+  uint64_t part_w[kMaxCl], sum_w[kMaxCl];
+  uint32_t part_n[kMaxCl], sum_n[kMaxCl];
   uint64_t found_w;
   uint32_t found_n, found_bin, found_count;
   uint32_t listed;  // the first CTA's counts for all
@@ -108,14 +108,14 @@ struct Shared {
     };
     struct {
       uint64_t weight16[KIND == 0 ? kBins16 : 1];
-      uint32_t n16[KIND == 0 ? kBins16 : 1];
+      uint32_t n16[KIND == 0 ? kBins16 / 2 + 1 : 1];  // two bins a word: a slice has fewer than 2^16 elements
     };
   };
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map_shared(addr, rank)) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map_shared(addr, rank)));
   return v;
 }
 __device__ __forceinline__ void st_cluster_u32(const void* p, uint32_t rank, uint32_t v) {
@@ -171,8 +171,10 @@ struct Row {
   Shared<KIND>& sm;
   const unsigned char* x;  // the slice
   int count, first;        // its elements, and the row's index of the first
-  int cl, rank, sh;
+  int cl, rank;
   float top, ch, lo;       // the row's maximum; log2(e) / T in two parts
+  float start;             // 256 Y + 1.5 * 2^23, or 0 for rows that take the difference first
+  float least;             // x c from here on: weight 0
   int warp, lane;
 
   __device__ __forceinline__ float at(int i) const { return element<KIND>(x, i); }
@@ -182,23 +184,41 @@ struct Row {
   // y of an element, without its low part: never smaller for a smaller x
   __device__ __forceinline__ float bits_below(float v) const { return __fmul_rn(__fsub_rn(top, v), ch); }
 
+  // Settings that a row's weights go by, from its maximum and log2(e) / T.
+  __device__ __forceinline__ void set(float max, float hi, float low) {
+    top = max, ch = hi, lo = low;
+    const float y = __fmul_rn(top, ch);
+    const float m = __fmaf_rn(y, 256.0f, kMagic);
+    start = fabsf(y) < 8000.0f ? m : 0.0f;
+    least = __fsub_rn(y, kRange);
+  }
   __device__ __forceinline__ uint64_t weight(float v) const {
-    const float d = __fsub_rn(top, v), p = __fmul_rn(d, ch);
-    if (!(p < kRange)) return 0;
-    // what the difference's rounding left out (Knuth's two-sum), and the product's
-    const float t = __fsub_rn(d, top), dl = __fsub_rn(__fsub_rn(top, __fsub_rn(d, t)), __fadd_rn(v, t));
-    float e = __fmaf_rn(d, ch, -p);
-    e = __fmaf_rn(d, lo, e);
-    e = __fmaf_rn(dl, ch, e);
-    // k = RN(256 p) in the low bits of 1.5 * 2^23 + k
-    const float m = __fmaf_rn(p, 256.0f, 12582912.0f);
+    float f, m;
+    if (start != 0.0f) {
+      const float p = __fmul_rn(v, ch);
+      if (!(p > least)) return 0;
+      float e = __fmaf_rn(v, ch, -p);
+      e = __fmaf_rn(v, lo, e);
+      m = __fmaf_rn(p, -256.0f, start);  // kMagic + k + what p is of it: the low bits are k's
+      f = __fadd_rn(__fmaf_rn(__fsub_rn(m, start), 1.0f / 256.0f, p), e);
+    } else {
+      const float d = __fsub_rn(top, v), p = __fmul_rn(d, ch);
+      if (!(p < kRange)) return 0;
+      // what the difference's rounding left out (Knuth's two-sum), and the product's
+      const float t = __fsub_rn(d, top), dl = __fsub_rn(__fsub_rn(top, __fsub_rn(d, t)), __fadd_rn(v, t));
+      float e = __fmaf_rn(d, ch, -p);
+      e = __fmaf_rn(d, lo, e);
+      e = __fmaf_rn(dl, ch, e);
+      m = __fmaf_rn(p, 256.0f, kMagic);
+      f = -__fadd_rn(__fmaf_rn(__fsub_rn(m, kMagic), -1.0f / 256.0f, p), e);
+    }
     const int k = __float_as_int(m) & 0x3fffff;
-    const float r = __fadd_rn(__fmaf_rn(__fsub_rn(m, 12582912.0f), -1.0f / 256.0f, p), e);
-    const float a = r * -0.693147180559945f;
-    const float g = a * fmaf(a, fmaf(a, fmaf(a, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), 1.0f);
+    const float a = f * 0.693147180559945f;
+    const float g = a * fmaf(a, fmaf(a, 1.0f / 6.0f, 0.5f), 1.0f);
     const int j = k & 255, i = k >> 8;
-    uint64_t w = sm.table[j] + (int64_t)__float2int_rn(g * sm.tablef[j]);
-    w <<= sh - 40;
+    const uint64_t t = sm.table[j];
+    // (g times it: its upper 32 of 41 bits do, from a register and not a second table)
+    const uint64_t w = t + (int64_t)__float2int_rn(g * (__uint2float_rn((uint32_t)(t >> 9)) * 512.0f));
     return (w + (((uint64_t)1 << i) >> 1)) >> i;
   }
   // The same from the row's table where there is one.
@@ -286,11 +306,26 @@ struct Row {
   }
   __device__ __forceinline__ void scan_bins(uint32_t n, uint64_t w, bool weigh, Scan& s) const {
     scan_bins(kBins, n, w, s, [&](int b, uint32_t& bn, uint64_t& bw) {
-      for (int r = 0; r < cl; ++r) {
-        bn += ld_cluster_u32(smem_u32(&sm.n[b]), r);
-        if (weigh)
-          bw += (uint64_t)ld_cluster_u32(smem_u32(&sm.w0[b]), r) + ((uint64_t)ld_cluster_u32(smem_u32(&sm.w1[b]), r) << 16) +
-                ((uint64_t)ld_cluster_u32(smem_u32(&sm.w2[b]), r) << 32);
+#pragma unroll
+      for (int r0 = 0; r0 < kMaxCl; r0 += 4) {
+        if (r0 >= cl) break;
+        uint32_t v[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // requested together
+          const uint32_t from = (uint32_t)min(r0 + r, cl - 1);
+          v[r][0] = ld_cluster_u32(smem_u32(&sm.n[b]), from);
+          if (weigh) {
+            v[r][1] = ld_cluster_u32(smem_u32(&sm.w0[b]), from);
+            v[r][2] = ld_cluster_u32(smem_u32(&sm.w1[b]), from);
+            v[r][3] = ld_cluster_u32(smem_u32(&sm.w2[b]), from);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (r0 + r >= cl) break;
+          bn += v[r][0];
+          if (weigh) bw += (uint64_t)v[r][1] + ((uint64_t)v[r][2] << 16) + ((uint64_t)v[r][3] << 32);
+        }
       }
     });
   }
@@ -300,19 +335,28 @@ struct Row {
   __device__ __forceinline__ bool find_bin(const Scan& s, bool by_weight, uint64_t target, uint32_t& n, uint64_t& w, int& bin,
                                            uint32_t& in_bin) const {
     if ((by_weight ? s.all_w : (uint64_t)s.all_n) < target) return false;
-    uint32_t cn = s.cn;
-    uint64_t cw = s.cw;
+    uint32_t cn = s.cn, hit_n = 0, hit_count = 0;
+    uint64_t cw = s.cw, hit_w = 0;
+    int hit = -1;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const uint64_t from = by_weight ? cw : cn, to = by_weight ? cw + s.bw[i] : cn + s.bn[i];
-      if (i < s.each && from < target && to >= target)
-        for (int r = 0; r < cl; ++r) {
-          st_cluster_u32(&sm.found_bin, r, (uint32_t)(s.base + i));
-          st_cluster_u32(&sm.found_count, r, s.bn[i]);
-          st_cluster_u32(&sm.found_n, r, cn);
-          st_cluster_u64(&sm.found_w, r, cw);
-        }
+      if (i < s.each && from < target && to >= target) hit = s.base + i, hit_n = cn, hit_count = s.bn[i], hit_w = cw;
       cn += s.bn[i], cw += s.bw[i];
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, hit >= 0);
+    if (who) {  // its warp tells the cluster, a CTA a lane
+      const int from = __ffs(who) - 1;
+      hit = __shfl_sync(0xffffffffu, hit, from);
+      hit_n = __shfl_sync(0xffffffffu, hit_n, from);
+      hit_count = __shfl_sync(0xffffffffu, hit_count, from);
+      hit_w = __shfl_sync(0xffffffffu, hit_w, from);
+      if (lane < cl) {
+        st_cluster_u32(&sm.found_bin, lane, (uint32_t)hit);
+        st_cluster_u32(&sm.found_count, lane, hit_count);
+        st_cluster_u32(&sm.found_n, lane, hit_n);
+        st_cluster_u64(&sm.found_w, lane, hit_w);
+      }
     }
     if (threadIdx.x == 0) sm.listed = 0;
     cluster_sync_all();
@@ -349,13 +393,22 @@ struct Row {
                                               uint64_t w, float& value, uint32_t& ties, uint64_t& sum) const {
     int m = 32;  // what is sorted: a power of two
     while (m < (int)size) m *= 2;
-    for (int i0 = warp * 32; i0 < count; i0 += T) {
-      const int i = i0 + lane;
-      const float v = i < count ? at(i) : 0.0f;
-      const uint32_t k = key_of(v);
-      const bool hit = i < count && in(v, k);
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-      if (hits) {
+    constexpr int U = 4;
+    for (int i0 = warp * 32; i0 < count; i0 += U * T) {
+      float v[U];
+      bool hit[U], some = false;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * T + lane;
+        v[j] = i < count ? at(i) : 0.0f;
+        hit[j] = i < count && in(v[j], key_of(v[j]));
+        some |= hit[j];
+      }
+      if (!__any_sync(0xffffffffu, some)) continue;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const uint32_t hits = __ballot_sync(0xffffffffu, hit[j]);
+        if (!hits) continue;
         uint32_t at0 = 0;
         if (lane == 0)
           asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
@@ -363,22 +416,36 @@ struct Row {
                        : "r"(cluster_map_shared(smem_u32(&sm.listed), 0)), "r"((uint32_t)__popc(hits))
                        : "memory");
         at0 = __shfl_sync(0xffffffffu, at0, 0) + __popc(hits & ((1u << lane) - 1));
-        if (hit && at0 < (uint32_t)kList)
+        if (hit[j] && at0 < (uint32_t)kList)
           for (int r = 0; r < cl; ++r)
-            st_cluster_u64(&sm.list[at0], r, (uint64_t)k << 32 | (0xffffffffu - (uint32_t)(first + i)));
+            st_cluster_u64(&sm.list[at0], r, (uint64_t)key_of(v[j]) << 32 | (0xffffffffu - (uint32_t)(first + i0 + j * T + lane)));
       }
     }
-    for (int i = (int)size + (int)threadIdx.x; i < m; i += T) sm.list[i] = 0;
+    if (size > kShort)
+      for (int i = (int)size + (int)threadIdx.x; i < m; i += T) sm.list[i] = 0;
     cluster_sync_all();
-    for (int k = 2; k <= m; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        const int i = threadIdx.x;
-        if (i < m && (i ^ j) > i) {
-          const uint64_t a = sm.list[i], b = sm.list[i ^ j];
-          if ((a < b) == ((i & k) == 0)) sm.list[i] = b, sm.list[i ^ j] = a;
-        }
-        __syncthreads();
+    if (size <= kShort) {  // each to its rank
+      const int i = threadIdx.x;
+      uint64_t mine = 0;
+      int place = 0;
+      if (i < (int)size) {
+        mine = sm.list[i];
+        for (int k = 0; k < (int)size; ++k) place += sm.list[k] > mine;
       }
+      __syncthreads();
+      if (i < (int)size) sm.list[place] = mine;
+      __syncthreads();
+    } else {
+      for (int k = 2; k <= m; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+          const int i = threadIdx.x;
+          if (i < m && (i ^ j) > i) {
+            const uint64_t a = sm.list[i], b = sm.list[i ^ j];
+            if ((a < b) == ((i & k) == 0)) sm.list[i] = b, sm.list[i ^ j] = a;
+          }
+          __syncthreads();
+        }
+    }
     // running weights, a thread an element
     const int i = threadIdx.x;
     const bool there = i < (int)size;
@@ -439,7 +506,7 @@ struct Row {
 };
 
 template <int KIND, int T>
-__global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams p, int cl, int slice, int sh) {
+__global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams p, int cl, int slice) {
   constexpr int E = KIND == 2 ? 4 : 2, kWarps = T / 32;
   extern __shared__ __align__(16) unsigned char dyn[];
   Shared<KIND>& sm = *reinterpret_cast<Shared<KIND>*>(dyn);
@@ -502,11 +569,10 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   for (int i = threadIdx.x; i < 256; i += T) {
     const uint64_t t = kPowers.v[i];
     sm.table[i] = t;
-    sm.tablef[i] = (float)t;
   }
   if constexpr (KIND == 0) {
     if (by_k || by_p) {
-      for (int i = threadIdx.x; i < kBins16; i += T) sm.n16[i] = 0;
+      for (int i = threadIdx.x; i < kBins16 / 2 + 1; i += T) sm.n16[i] = 0;
       if (threadIdx.x == 0) sm.middle_w = 0;
     }
   } else if (by_k || by_p) {
@@ -519,19 +585,16 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
     sm.cl = (float)(c - (double)sm.ch);
     if (min_p > 0.0f && min_p < 1.0f) below = temp * log((double)min_p);
   }
-  Row<KIND, T> row{sm, data + off, count, first, cl, rank, sh, 0.0f, 0.0f, 0.0f, warp, lane};
+  Row<KIND, T> row{sm, data + off, count, first, cl, rank, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, warp, lane};
   {
-    const uint32_t k = row.block_max(key_of(top)), b = row.block_max(bad ? 1u : 0u);
-    row.to_all([&](int to) {
-      st_cluster_u32(&sm.top[rank], to, k);
-      st_cluster_u32(&sm.bad[rank], to, b);
-    });
+    const uint32_t k = row.block_max(bad ? 0xffffffffu : key_of(top));  // above any number's
+    row.to_all([&](int to) { st_cluster_u32(&sm.top[rank], to, k); });
   }
   cluster_sync_all();
-  uint32_t key = 0, spoiled = 0;
-  for (int i = 0; i < cl; ++i) key = max(key, sm.top[i]), spoiled |= sm.bad[i];
+  uint32_t key = 0;
+  for (int i = 0; i < cl; ++i) key = max(key, sm.top[i]);
   top = of_key(key);
-  if (!settings || spoiled || top == -INFINITY) {  // the same in every CTA of the cluster
+  if (!settings || key == 0xffffffffu || top == -INFINITY) {  // the same in every CTA of the cluster
     if (rank == 0 && threadIdx.x == 0) {
       if (!settings) record_failure(p.status_word, status_code(BI_ERR_INVALID_ARG, kSiteSample));
       if (p.tok64)
@@ -543,7 +606,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   }
   if (threadIdx.x == T - 1)  // the smallest logit that min_p keeps
     sm.floor = min_p > 0.0f ? __double2float_ru((double)top + below) : -INFINITY;
-  row.top = top, row.ch = sm.ch, row.lo = sm.cl;
+  row.set(top, sm.ch, sm.cl);
 
   // --- bf16: the row's weights by value, if its numbers that have any are in the bins
   bool tabled = false;
@@ -578,10 +641,11 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
     if constexpr (KIND == 0) {
       if (tabled) {
         uint64_t mine = 0;
+#pragma unroll 4
         for (int i = threadIdx.x; i < count; i += T) {
           const uint32_t bits = reinterpret_cast<const uint16_t*>(row.x)[i];
           const int b = bin16(bits);
-          if (b >= 0) atomicAdd(&sm.n16[b], 1u);  // (others have no weight)
+          if (b >= 0) atomicAdd(&sm.n16[b >> 1], b & 1 ? 65536u : 1u);  // (others have no weight)
           if (b == kMiddle16) mine += row.weight(__uint_as_float(bits << 16));
         }
         if (__any_sync(0xffffffffu, mine != 0)) {
@@ -589,7 +653,11 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
           if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.middle_w), (unsigned long long)mine);
         }
         row.scan_bins(kBins16, 0, 0, s, [&](int b, uint32_t& bn, uint64_t& bw) {
-          for (int c = 0; c < cl; ++c) bn += ld_cluster_u32(smem_u32(&sm.n16[b]), c);
+          uint32_t v[kMaxCl];
+#pragma unroll
+          for (int c = 0; c < kMaxCl; ++c) v[c] = ld_cluster_u32(smem_u32(&sm.n16[b >> 1]), (uint32_t)min(c, cl - 1));
+#pragma unroll
+          for (int c = 0; c < kMaxCl; ++c) bn += c < cl ? (b & 1 ? v[c] >> 16 : v[c] & 0xffffu) : 0;
           if (b != kMiddle16)
             bw = bn * sm.weight16[b];
           else
@@ -630,6 +698,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
       if (!done) row.clear_bins();
     }
     if (!done) {
+#pragma unroll 2
       for (int i = threadIdx.x; i < count; i += T) {
         const float x = row.at(i), y = row.bits_below(x);
         if (y < kRange) row.into_bin((int)(y * kBinsPerBit), x, by_p);
@@ -654,6 +723,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   const int len = row.seg_len();
   auto sum_of = [&](int from, int to, uint64_t& w, uint32_t& n) {  // weight above the cut, elements at it
     w = 0, n = 0;
+#pragma unroll 4
     for (int i = from + lane; i < to; i += 32) {
       const float v = row.at(i);
       if (v > cut)
@@ -669,43 +739,47 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
     uint64_t w;
     uint32_t n;
     sum_of(from, to, w, n);
-    if (lane < cl) {
-      st_cluster_u64(&sm.seg_w[rank * kWarps + warp], lane, w);
-      st_cluster_u32(&sm.seg_n[rank * kWarps + warp], lane, n);
+    if (lane == 0) sm.warp_w[warp] = w, sm.warp_n[warp] = n;
+    __syncthreads();
+    if (warp == 0) {
+      const uint64_t mw = lane < kWarps ? sm.warp_w[lane] : 0;
+      const uint64_t all_w = warp_sum(mw);
+      const uint32_t all_n = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.warp_n[lane] : 0u);
+      if (lane < cl) {
+        st_cluster_u64(&sm.sum_w[rank], lane, all_w);
+        st_cluster_u32(&sm.sum_n[rank], lane, all_n);
+      }
     }
   }
   cluster_sync_all();
   const uint64_t each = cut > -INFINITY ? row.weight(cut) : 0;
-  // running sums of all segments, some a lane: first of the elements at the cut, which are kept in index order
-  const int segs = cl * kWarps, per = (segs + 31) / 32;
-  uint32_t tied = 0;
-  for (int i = lane * per; i < min(segs, lane * per + per); ++i) tied += sm.seg_n[i];
-  uint32_t seen = warp_scan(tied, lane) - tied;
-  const uint32_t seen0 = min(seen, ties);
-  uint64_t mine = 0;
-  seen = seen0;
-  for (int i = lane * per; i < min(segs, lane * per + per); ++i) {
-    const uint32_t n = min(sm.seg_n[i], ties - seen);
-    mine += sm.seg_w[i] + n * each, seen += n;
+  uint64_t all = 0;
+  uint32_t seen = 0;  // elements at the cut so far, which are kept in index order
+  for (int c = 0; c < cl; ++c) {
+    const uint32_t n = min(sm.sum_n[c], ties - seen);
+    all += sm.sum_w[c] + n * each, seen += n;
   }
-  uint64_t run = warp_scan(mine, lane);
-  const uint64_t all = __shfl_sync(0xffffffffu, run, 31);
   const uint64_t want = min(all - 1, (uint64_t)((double)u * (double)all));
-  const int hit = __ffs(__ballot_sync(0xffffffffu, run > want)) - 1;
-  run -= mine, seen = seen0;
-  int seg = lane * per;
-  for (; seg + 1 < min(segs, lane * per + per); ++seg) {
-    const uint32_t n = min(sm.seg_n[seg], ties - seen);
-    const uint64_t w = sm.seg_w[seg] + n * each;
-    if (run + w > want) break;
-    run += w, seen += n;
+  uint64_t run = 0;
+  seen = 0;
+  for (int c = 0; c < rank; ++c) {
+    const uint32_t n = min(sm.sum_n[c], ties - seen);
+    run += sm.sum_w[c] + n * each, seen += n;
   }
-  seg = __shfl_sync(0xffffffffu, seg, hit);
-  run = __shfl_sync(0xffffffffu, run, hit);
-  seen = __shfl_sync(0xffffffffu, seen, hit);
-  if (seg / kWarps != rank) return;  // no CTA reads another's memory from here on
+  const uint64_t upto_cta = run + sm.sum_w[rank] + min(sm.sum_n[rank], ties - seen) * each;
+  if (run > want || upto_cta <= want) return;  // another CTA's (none reads another's memory from here on)
+  // its segments, a lane each
+  int seg;
+  {
+    const uint32_t n = lane < kWarps ? sm.warp_n[lane] : 0;
+    const uint32_t n_before = min(ties - seen, warp_scan(n, lane) - n), kept = min(n, ties - seen - n_before);
+    const uint64_t w = (lane < kWarps ? sm.warp_w[lane] : 0) + kept * each, upto = run + warp_scan(w, lane);
+    seg = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
+    run = __shfl_sync(0xffffffffu, upto - w, seg);
+    seen += __shfl_sync(0xffffffffu, n_before, seg);
+  }
   // the segment's parts, a warp each
-  const int from = min(count, (seg % kWarps) * len), to = min(count, from + len);
+  const int from = min(count, seg * len), to = min(count, from + len);
   const int part = ((to - from + kWarps - 1) / kWarps + 31) & ~31;
   const int a = min(to, from + warp * part), b = min(to, a + part);
   uint64_t w;
@@ -749,10 +823,9 @@ cudaError_t launch(const SampleParams& p, int cl, cudaStream_t stream) {
   constexpr int kHead = (sizeof(Shared<KIND>) + 15) / 16 * 16 + 16;
   constexpr int kMost = kHead + (int)(kMaxVocab / kMaxCl) * E;
   static_assert(kMost <= 232448, "shared memory of a CTA");
-  static_assert(kMaxVocab / kMaxCl <= 65536, "three 16-bit sums of a slice fit 32 bits");
+  static_assert(kMaxVocab / kMaxCl < 65536, "sums of 16 bits of a slice's weights fit 32");
+  static_assert(kMaxVocab <= 1 << 22, "sums of a row's weights fit 63 bits");
   const int slice = ((p.N + cl - 1) / cl + 7) / 8 * 8;  // (16 bytes keep their place)
-  int bits = 0;
-  while ((1 << bits) < p.N) ++bits;
   const void* fn = reinterpret_cast<const void*>(&sample_kernel<KIND, T>);
   cudaError_t e = set_smem_once(fn, kMost, (T == 1024 ? 133 : 130) + KIND);
   if (e != cudaSuccess) return e;
@@ -768,16 +841,25 @@ cudaError_t launch(const SampleParams& p, int cl, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<KIND, T>, p, cl, slice, std::min(46, 62 - bits));
+  return cudaLaunchKernelEx(&cfg, sample_kernel<KIND, T>, p, cl, slice);
 }
 
 template <int KIND>
 cudaError_t launch(const SampleParams& p, int num_sms, cudaStream_t stream) {
-  // Slices of at most 16384 elements while a cluster of eight has them.
-  int cl = 1;
-  while (cl < kMaxCl && p.N > 16384 * cl) cl *= 2;
-  // An SM to each CTA: twice the threads, half the time of a pass.
-  return p.R * cl <= num_sms ? launch<KIND, 1024>(p, cl, stream) : launch<KIND, 512>(p, cl, stream);
+  // Slices of at most 16384 elements while a cluster of eight has them; in 16 bits
+  // 32768 for batches that fill the GPU in any case, two CTAs an SM: half of what
+  // each does whatever its slice is (256 bf16 rows of 128256 with top-p: 121 us
+  // against 158).  An SM to each CTA, when there are so few: twice the threads,
+  // half the time of a pass.
+  auto clusters = [&](int slice) {
+    int cl = 1;
+    while (cl < kMaxCl && p.N > slice * cl) cl *= 2;
+    return cl;
+  };
+  int cl = clusters(16384);
+  if (p.R * cl <= num_sms) return launch<KIND, 1024>(p, cl, stream);
+  if (KIND != 2 && p.R * cl > 2 * (int64_t)num_sms) cl = clusters(32768);
+  return launch<KIND, 512>(p, cl, stream);
 }
 
 }  // namespace
