@@ -37,6 +37,15 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   return to_e4m3x2(a, b) | to_e4m3x2(c, d) << 16;
 }
+// The two pairs of four e4m3 numbers as fp16.
+__device__ __forceinline__ void e4m3x4_to_half2s(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
+}
 // Two e4m3 numbers as fp16, which holds them all.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
   uint32_t r;

@@ -107,11 +107,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // Kinds of cache: bf16 and fp16 as q, or e4m3 with scales.
 constexpr int kCache16 = 1, kCache8 = 2;  // fp16, e4m3
 // What a weight is multiplied by before it is cut into 16-bit numbers, and what
-// takes it off the joined result (in 8 bits a unit's end does).
+// takes it off the joined result.  (In 8 bits weights go up to 2.)
 template <int C>
 struct Up {
   static constexpr float v = C == kCache8 ? 16384.0f : C == kCache16 ? 32768.0f : 1.0f;
-  static constexpr float back = C == kCache8 ? 1.0f : 1.0f / v;
+  static constexpr float back = 1.0f / v;
 };
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -165,9 +165,11 @@ struct Unit {
 
 template <int C, int D, int NT>
 struct Shape {
+  static constexpr int HT = 8 * NT;                          // query heads of a unit
+
   static constexpr bool kBig = C != kCache8 && (D == 256 || (D == 128 && NT == 2));
   static constexpr int W = kBig ? 8 : 4;                     // warps of a CTA
-  static constexpr int kCtas = C == kCache8 ? (D == 64 && NT == 1 ? 4 : D == 128 && NT == 1 ? 3 : 2)
+  static constexpr int kCtas = C == kCache8 ? (D == 64 && NT == 1 ? 4 : NT == 1 && D == 128 ? 3 : 2)
                                : kBig       ? 1
                                             : (D == 64 ? (NT == 1 ? 4 : 3) : 2);  // CTAs of an SM
   static constexpr int E = C == kCache8 ? 1 : 2;             // bytes of an element
@@ -179,8 +181,8 @@ struct Shape {
   static constexpr int kRow = D + 4;                         // padded row of the join: no bank conflicts
   struct Shared {
     unsigned char ring[W][3][kSlotBytes];
-    float o[W / 2][8 * NT][kRow];
-    float m[W / 2][8 * NT], l[W / 2][8 * NT];
+    float o[W / 2][HT][kRow];
+    float m[W / 2][HT], l[W / 2][HT];
     int32_t start[32 * W + 1];  // pieces of the requests before thread i's
     int32_t warp_sum[W];
   };
@@ -209,6 +211,12 @@ __device__ __forceinline__ uint4 read_transposed(uint32_t a) {
                : "memory");
   return v;
 }
+// A load that stays where it is written, a tile before its use.
+__device__ __forceinline__ float load_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void barrier_arrive(uint32_t id, uint32_t count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -221,6 +229,7 @@ template <int C, int D, int NT, bool ONE>
 __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCtas)
     paged_attn_kernel(const PagedAttnParams p) {
   using Sh = Shape<C, D, NT>;
+  constexpr int HT = Sh::HT;
   constexpr bool Q8 = C == kCache8;
   constexpr int F16 = C != 0;  // the tensor cores' operand type
   extern __shared__ __align__(1024) unsigned char dyn[];
@@ -316,8 +325,8 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
       const int kvh = u.hk / p.head_tiles;
       pkey = u.k0 + warp * Sh::kTile, pend = u.k1;
       ptab = p.table + u.b * p.ld_table;
-      kb = static_cast<const unsigned char*>(p.k) + kvh * p.k_head * Sh::E + 16 * c;
-      vb = static_cast<const unsigned char*>(p.v) + kvh * p.v_head * Sh::E + 16 * c;
+      kb = static_cast<const unsigned char*>(p.k) + kvh * p.k_head * Sh::E + 16 * (Q8 ? lane % (D / 16) : c);
+      vb = static_cast<const unsigned char*>(p.v) + kvh * p.v_head * Sh::E + 16 * (Q8 ? lane % (D / 16) : c);
       if constexpr (Q8) {
         ksb = static_cast<const float*>(p.ks.ptr) + kvh * p.ks.head;
         vsb = static_cast<const float*>(p.vs.ptr) + kvh * p.vs.head;
@@ -335,7 +344,11 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
   const uint32_t ring = smem_u32(sm.ring[warp][0]);
   uint32_t live_next = 0;  // mask of the requested tile's keys
   int64_t vo = 0;          // byte offset of the lane's key in the value cache
-  float ks_next = 0.0f, vs_next = 0.0f;  // scales of the lane's key in the requested tile
+  float ks_next = 0.0f, vs_next = 0.0f;  // in 8 bits: its scales
+  // In 8 bits a key's row goes to as many lanes as it has chunks, whole lines of
+  // memory to a request; where it lands is the same.
+  constexpr int kRowLanes = Q8 ? D / 16 : 4, kRowKeys = 32 / kRowLanes;
+  [[maybe_unused]] const int chunk = lane % kRowLanes, rkey = lane / kRowLanes;
   // Keys: lane (g, c) takes chunks c, c + 4, ... of keys g, g + 8, ... to a place of its own.
   auto request_keys = [&](int slot) {
     const bool there = page >= 0 && page < p.P;
@@ -344,17 +357,30 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     const int64_t ko = there ? (page * p.k_page + row * p.k_row) * Sh::E : 0;
     vo = there ? (page * p.v_page + row * p.v_row) * Sh::E : 0;
     if constexpr (Q8) {
-      ks_next = there ? __ldg(ksb + page * p.ks.page + row * p.ks.row) : 0.0f;
-      vs_next = there ? __ldg(vsb + page * p.vs.page + row * p.vs.row) : 0.0f;
+      ks_next = vs_next = 0.0f;
+      if (there) {
+        ks_next = load_now(ksb + page * p.ks.page + row * p.ks.row);
+        vs_next = load_now(vsb + page * p.vs.page + row * p.vs.row);
+      }
     }
     if (pi < units) {
-      uint32_t dst = ring + slot * Sh::kSlotBytes + lane * 16;
+      if constexpr (Q8) {
 #pragma unroll
-      for (int r = 0; r < 2 * KT; ++r) {
-        const unsigned char* a = kb + __shfl_sync(0xffffffffu, ko, 8 * r + g);
-        const bool ok = (live_next >> (8 * r + g)) & 1;
+        for (int i = 0; i < Sh::kTile / kRowKeys; ++i) {
+          const int key = kRowKeys * i + rkey;
+          const unsigned char* a = kb + __shfl_sync(0xffffffffu, ko, key);
+          copy16(ring + slot * Sh::kSlotBytes + (((key >> 3) * KJ + (chunk >> 2)) * 32 + (key & 7) * 4 + (chunk & 3)) * 16, a,
+                 (live_next >> key) & 1);
+        }
+      } else {
+        uint32_t dst = ring + slot * Sh::kSlotBytes + lane * 16;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j, dst += 512) copy16(dst, a + 64 * j, ok);
+        for (int r = 0; r < 2 * KT; ++r) {
+          const unsigned char* a = kb + __shfl_sync(0xffffffffu, ko, 8 * r + g);
+          const bool ok = (live_next >> (8 * r + g)) & 1;
+#pragma unroll
+          for (int j = 0; j < KJ; ++j, dst += 512) copy16(dst, a + 64 * j, ok);
+        }
       }
     }
     copies_commit();
@@ -363,15 +389,24 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
   // that the transposing reads of eight keys meet no bank twice.
   auto request_values = [&](int slot) {
     if (pi < units) {
-      // (rows of 64 bytes: two keys to a line of all banks, the chunk permuted by the pair)
-      const uint32_t swap = Q8 && D == 64 ? (g >> 1) & 3 : g;
-      const uint32_t dst = ring + slot * Sh::kSlotBytes + g * (D * Sh::E) + ((c ^ swap) & 3) * 16 + (swap >> 2) * 64;
+      if constexpr (Q8) {
+        // (rows of 64 bytes: two keys to a line of all banks, the chunk permuted by the pair)
 #pragma unroll
-      for (int r = 0; r < 2 * KT; ++r) {
-        const unsigned char* a = vb + __shfl_sync(0xffffffffu, vo, 8 * r + g);
-        const bool ok = (live_next >> (8 * r + g)) & 1;
+        for (int i = 0; i < Sh::kTile / kRowKeys; ++i) {
+          const int key = kRowKeys * i + rkey;
+          const unsigned char* a = vb + __shfl_sync(0xffffffffu, vo, key);
+          copy16(ring + slot * Sh::kSlotBytes + key * D + (chunk ^ (D == 64 ? (key >> 1) & 3 : key & 7)) * 16, a,
+                 (live_next >> key) & 1);
+        }
+      } else {
+        const uint32_t dst = ring + slot * Sh::kSlotBytes + g * (2 * D) + ((c ^ g) & 3) * 16 + (g >> 2) * 64;
 #pragma unroll
-        for (int j = 0; j < KJ; ++j) copy16((dst + r * 8 * D * Sh::E) ^ (j * 64), a + 64 * j, ok);
+        for (int r = 0; r < 2 * KT; ++r) {
+          const unsigned char* a = vb + __shfl_sync(0xffffffffu, vo, 8 * r + g);
+          const bool ok = (live_next >> (8 * r + g)) & 1;
+#pragma unroll
+          for (int j = 0; j < KJ; ++j) copy16((dst + r * 16 * D) ^ (j * 64), a + 64 * j, ok);
+        }
       }
     }
     copies_commit();
@@ -379,19 +414,24 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
   // Q^T fragments: head g of tile n, dimensions 32 j + 8 c .. + 7; with caches in
   // 8 bits chunks of 16 dimensions, 64 (j / 2) + 16 c + 8 (j % 2) .. + 7
   constexpr int QJ = D / 32;
-  uint4 q[NT][QJ], qn[NT][QJ];
+  uint4 q[NT][QJ], qn[NT][QJ];  // (qn, the next unit's, in 16 bits: 8 have 16 warps an SM to wait beside)
   float qs[NT][2];  // in 8 bits: a score's factor for heads 2c, 2c + 1
-  auto load_queries = [&](const Unit& u) {
-    const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
+  auto load_queries = [&](const Unit& u, bool now) {
+    const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * HT;
     const unsigned short* qb =
         static_cast<const unsigned short*>(p.q) + u.b * p.q_b + (kvh * p.group + h0 + g) * p.q_h + (Q8 ? 16 : 8) * c;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < QJ; ++j)
-        qn[n][j] = h0 + 8 * n + g < p.group
-                       ? __ldg(reinterpret_cast<const uint4*>(qb + 8 * n * p.q_h + (Q8 ? 64 * (j / 2) + 8 * (j % 2) : 32 * j)))
-                       : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < QJ; ++j) {
+        const unsigned short* a = qb + 8 * n * p.q_h + (Q8 ? 64 * (j / 2) + 8 * (j % 2) : 32 * j);
+        const bool there = h0 + 8 * n + g < p.group;
+        if (Q8 && !now) {
+          if (there && j % 2 == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+        } else {
+          qn[n][j] = there ? __ldg(reinterpret_cast<const uint4*>(a)) : make_uint4(0, 0, 0, 0);
+        }
+      }
   };
   // With caches in 8 bits, whose numbers are fp16 to the tensor cores, so is q,
   // brought to a largest element of 2^13 .. 2^14 a head by a power of two: exact
@@ -406,20 +446,24 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint32_t top = 0;
         auto both = [&](uint32_t w, float& lo, float& hi) {
           lo = p.in_f16 ? low16<1>(w) : low16<0>(w);
           hi = p.in_f16 ? high16<1>(w) : high16<0>(w);
         };
-        auto look = [&](uint32_t w) {
-          float lo, hi;
-          both(w, lo, hi);
-          top = max(top, max(__float_as_uint(lo) & 0x7fffffffu, __float_as_uint(hi) & 0x7fffffffu));
-        };
+        // magnitudes of 16-bit numbers are ordered as their bits are, a NaN's above all
+        uint32_t most = 0;
 #pragma unroll
-        for (int j = 0; j < QJ; ++j) look(qn[n][j].x), look(qn[n][j].y), look(qn[n][j].z), look(qn[n][j].w);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        for (int j = 0; j < QJ; ++j) {
+          const uint32_t w[4] = {qn[n][j].x, qn[n][j].y, qn[n][j].z, qn[n][j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+        }
+        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        most = max(most & 0xffffu, most >> 16);
+        float lo, hi;
+        both(most, lo, hi);
+        const uint32_t top = __float_as_uint(lo);
         const int e = max(min((int)(top >> 23) - 127, 127), -100) - 13;
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
         auto scaled = [&](uint32_t w) {
@@ -447,42 +491,40 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
   auto dim = [&](int i, int x) { return Q8 ? 16 * i + 2 * g + x : 16 * i + 8 * x + g; };
 
   Unit u = unit_at(0, cw);
-  load_queries(u);
+  load_queries(u, false);
   advance();
   request_keys(0);
   request_values(1);
   advance();
   int sk = 0;  // slot of the tile's keys; its values are in the slot after it
   for (int64_t ui = 0; ui < units; ++ui) {
+    if constexpr (Q8) load_queries(u, true);
     take_queries();
     const Unit next = unit_at(min(ui + 1, units - 1), cw);
-    load_queries(next);
+    load_queries(next, false);
     float o[MT][NT][4] = {};
-    float m[NT][2], l[NT][2];
-    float mo[NT][2];  // in 8 bits: the reference of o, the largest t + log2 of a value's scale
+    float m[NT][2], l[NT][2];  // (in 8 bits m is of t + log2 of a value's scale)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
-      if constexpr (Q8) mo[n][0] = mo[n][1] = -INFINITY;
-    }
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
     for (int key = u.k0 + warp * Sh::kTile; key < u.k1; key += Sh::kStep) {
       const int sv = sk == 2 ? 0 : sk + 1, sn = sk == 0 ? 2 : sk - 1;
       copies_wait<1>();  // this tile's keys are here
       __syncwarp();      // and every lane is done with the last tile's values
       const uint32_t live = live_next;
-      // in 8 bits: scales of keys 8 r + g, the values' as 2^vlog * vfrac
-      float ks[2 * KT], vlog[2 * KT], vfrac[2 * KT];
+      // in 8 bits: scales of keys 8 r + g, the values' as 2^vlog * vfrac; vsum = 2^-vlog
+      float ks[2 * KT], vlog[2 * KT], vfrac[2 * KT], vsum[2 * KT];
       if constexpr (Q8) {
+        // below 2^-60 (zero, and what is not a number) vfrac takes the rest
         const uint32_t bits = __float_as_uint(vs_next), e = (bits >> 23) & 255u;
-        const bool plain = e != 0 && e != 255;
-        const float lg = plain ? (float)((int)e - 127) : e == 0 ? -127.0f : 0.0f;
-        const float fr = plain ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u)
-                               : vs_next * (e == 0 ? 1.7014118346046923e38f /* 2^127 */ : 1.0f);
+        const bool plain = e >= 127 - 60 && e != 255;
+        const float lg = plain ? (float)((int)e - 127) : (bits << 1) == 0 ? -20.0f : -60.0f;
+        const float fr = plain ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : vs_next * 1152921504606846976.0f;
 #pragma unroll
         for (int r = 0; r < 2 * KT; ++r) {
           ks[r] = __shfl_sync(0xffffffffu, ks_next, 8 * r + g);
           vlog[r] = __shfl_sync(0xffffffffu, lg, 8 * r + g);
           vfrac[r] = __shfl_sync(0xffffffffu, fr, 8 * r + g);
+          vsum[r] = ex2_approx(-vlog[r]);  // (a power of two: exact)
         }
       }
       request_keys(sn);
@@ -503,8 +545,9 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
               }
             } else {
               auto step = [&](uint32_t w0, uint32_t w1, int h, bool upper) {  // four dimensions of a lane
-                const uint32_t a0 = e4m3x2_to_half2(w0 & 0xffffu), a2 = e4m3x2_to_half2(w0 >> 16);
-                const uint32_t a1 = e4m3x2_to_half2(w1 & 0xffffu), a3 = e4m3x2_to_half2(w1 >> 16);
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_half2s(w0, a0, a2);
+                e4m3x4_to_half2s(w1, a1, a3);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                   const uint4& b = q[n][2 * j + h];
@@ -523,7 +566,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
         for (int t = 0; t < KT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            s[t][n][e] = Q8 ? __fmul_rn(__fmul_rn(s[t][n][e], ks[2 * t + (e >> 1)]), qs[n][e & 1])
+            s[t][n][e] = Q8 ? __fadd_rn(__fmul_rn(__fmul_rn(s[t][n][e], ks[2 * t + (e >> 1)]), qs[n][e & 1]), vlog[2 * t + (e >> 1)])
                             : __fmul_rn(s[t][n][e], p.score_log2);
         if (live != (Sh::kTile == 32 ? 0xffffffffu : live | 0xffffu)) {
 #pragma unroll
@@ -541,29 +584,12 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
         for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], x));
-        float mxo[2] = {0.0f, 0.0f};
-        if constexpr (Q8) {
-          mxo[0] = mo[n][0], mxo[1] = mo[n][1];
-#pragma unroll
-          for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mxo[e & 1] = fmaxf(mxo[e & 1], __fadd_rn(s[t][n][e], vlog[2 * t + (e >> 1)]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) mxo[h] = fmaxf(mxo[h], __shfl_xor_sync(0xffffffffu, mxo[h], x));
-        }
-        const bool moved = mx[0] != m[n][0] || mx[1] != m[n][1] || (Q8 && (mxo[0] != mo[n][0] || mxo[1] != mo[n][1]));
-        if (__any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, mx[0] != m[n][0] || mx[1] != m[n][1])) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float alpha = mx[h] == -INFINITY ? 0.0f : ex2_approx(m[n][h] - mx[h]);
+            const float alpha = mx[h] == -INFINITY ? 0.0f : ex2_approx(m[n][h] - mx[h]);
             m[n][h] = mx[h];
             l[n][h] = __fmul_rn(l[n][h], alpha);
-            if constexpr (Q8) {
-              alpha = mxo[h] == -INFINITY ? 0.0f : ex2_approx(mo[n][h] - mxo[h]);
-              mo[n][h] = mxo[h];
-            }
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][n][h] *= alpha, o[i][n][2 + h] *= alpha;
           }
@@ -576,13 +602,11 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
           for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int e = h; e < 4; e += 2) {
-              if constexpr (Q8) {
-                const float refo = mxo[h] == -INFINITY ? 0.0f : mxo[h];
-                const float weight = ex2_approx(__fsub_rn(__fadd_rn(s[t][n][e], vlog[2 * t + (e >> 1)]), refo));
-                sum += ex2_approx(__fsub_rn(s[t][n][e], ref));
-                s[t][n][e] = __fmul_rn(weight, vfrac[2 * t + (e >> 1)]);
+              s[t][n][e] = ex2_approx(__fsub_rn(s[t][n][e], ref));
+              if constexpr (Q8) {  // e^score for the sum, e^score times the value's scale for the product
+                sum = __fmaf_rn(s[t][n][e], vsum[2 * t + (e >> 1)], sum);
+                s[t][n][e] = __fmul_rn(s[t][n][e], vfrac[2 * t + (e >> 1)]);
               } else {
-                s[t][n][e] = ex2_approx(__fsub_rn(s[t][n][e], ref));
                 sum += s[t][n][e];
               }
             }
@@ -618,9 +642,9 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
           // of a key two neighbouring dimensions: bytes (k, d) (k, d + 1) (k + 1, d) (k + 1, d + 1)
           const uint4 a = read_transposed(src + t * (16 * D) + (((i + vchunk) ^ vkey) * 16));
           auto step = [&](uint32_t k0, uint32_t k8, int i) {
-            k0 = __byte_perm(k0, 0, 0x3120), k8 = __byte_perm(k8, 0, 0x3120);
-            const uint32_t a0 = e4m3x2_to_half2(k0 & 0xffffu), a1 = e4m3x2_to_half2(k0 >> 16);
-            const uint32_t a2 = e4m3x2_to_half2(k8 & 0xffffu), a3 = e4m3x2_to_half2(k8 >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_half2s(__byte_perm(k0, 0, 0x3120), a0, a1);
+            e4m3x4_to_half2s(__byte_perm(k8, 0, 0x3120), a2, a3);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -646,18 +670,8 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     // Join: warp w + H into warp w, then warps 1 .. H - 1 into warp 0, through
     // shared memory; a warp that has handed its result over goes on to the
     // next unit.
-    const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
-    const int head = kvh * p.group + h0, heads = min(8 * NT, p.group - h0);
-    if constexpr (Q8) {  // o relative to m, as l is
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = mo[n][h] == -INFINITY ? 0.0f : ex2_approx(mo[n][h] - m[n][h]) * (1.0f / Up<C>::v);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) o[i][n][h] *= f, o[i][n][2 + h] *= f;
-        }
-    }
+    const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * HT;
+    const int head = kvh * p.group + h0, heads = min(HT, p.group - h0);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -755,8 +769,8 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     // group of them (a piece that the request has not adds zeros).
     cluster_sync_all();
     if (cluster_ctarank() == 0) {
-      const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * 8 * NT;
-      const int head = kvh * p.group + h0, heads = min(8 * NT, p.group - h0);
+      const int kvh = u.hk / p.head_tiles, h0 = (u.hk - kvh * p.head_tiles) * HT;
+      const int head = kvh * p.group + h0, heads = min(HT, p.group - h0);
       for (int e = threadIdx.x; e < heads * (D / 4); e += kThreads) {
         const int h = e / (D / 4), d = (e % (D / 4)) * 4;
         const uint32_t am = smem_u32(&sm.m[0][h]), al = smem_u32(&sm.l[0][h]), ao = smem_u32(&sm.o[0][h][d]);
@@ -916,7 +930,7 @@ cudaError_t launch(PagedAttnParams& p, int num_sms, bool* joined, cudaStream_t s
   constexpr int kSlot = C == kCache8 ? 115 + (D == 256 ? 4 : (D == 128 ? 2 : 0) + NT - 1)
                                      : 24 + (D == 256 ? 8 + C : (D == 128 ? 4 : 0) + 2 * C + NT - 1);
   constexpr int kOneSlot = C == kCache8 ? kSlot + 5 : kSlot + 40;
-  p.head_tiles = (p.group + 8 * NT - 1) / (8 * NT);
+  p.head_tiles = (p.group + Sh::HT - 1) / Sh::HT;
   const int64_t most = (int64_t)p.B * p.max_splits * p.Hkv * p.head_tiles;
   // Tables of at most 4096 keys whose units all run at once: a CTA a unit and a
   // cluster a request's head tile, joined in place -- one launch, and no search
