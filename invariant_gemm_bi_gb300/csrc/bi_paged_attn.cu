@@ -75,18 +75,23 @@ namespace {
 // 4096 keys of 16 ungrouped heads 96 against 98, one request of 4096 keys, all
 // in a cluster then, 10.5 against 11.4; one of 8192 is left to fewer SMs, 14.0
 // against 12.8).  At most 128 pieces: 256 made 131071 keys at D = 256 wait
-// longer for the join than the evener split saved (97.7 us against 97.1).
+// longer for the join than the evener split saved (97.7 us against 97.1).  In 8
+// bits what a unit costs beside its keys (820 instructions a warp; 90 a tile of 32
+// keys at four tiles a unit) weighs twice as much: beyond 8192 keys pieces have at
+// least 1024 (32 requests of 65536, 8 heads over 2, 120 us against 127; 64 ragged
+// ones of up to 8192 keep 512, since with 1024 a CTA has five units or six: 128 us
+// against 115).
 constexpr int kMinSplit = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kManySplits = 128;
 
-__host__ __device__ inline int32_t paged_split_len(int64_t len) {
-  int64_t s = len <= kMaxCluster * kMinSplit ? kMinSplit : 2 * kMinSplit;
+__host__ __device__ inline int32_t paged_split_len(int64_t len, bool e4m3) {
+  int64_t s = len <= kMaxCluster * kMinSplit ? kMinSplit : (e4m3 && len > 32 * kMinSplit ? 4 : 2) * kMinSplit;
   while (len > kManySplits * s) s *= 2;
   return (int32_t)s;
 }
-__host__ __device__ inline int32_t split_count(int64_t len) {
-  const int32_t s = paged_split_len(len);
+__host__ __device__ inline int32_t split_count(int64_t len, bool e4m3) {
+  const int32_t s = paged_split_len(len, e4m3);
   return len <= 0 ? 1 : (int32_t)((len + s - 1) / s);  // an empty request is one unit that writes zeros
 }
 
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     // pieces before each thread's requests
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int n = 0;
-    for (int b = b0; b < b1; ++b) n += split_count(request_len(p, b));
+    for (int b = b0; b < b1; ++b) n += split_count(request_len(p, b), Q8);
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
       const int id = (int)blockIdx.x / p.max_splits;
       u.b = id / inner, u.hk = id - u.b * inner, u.piece = (int)blockIdx.x % p.max_splits;
       u.len = request_len(p, u.b);
-      const int n = paged_split_len(u.len);
+      const int n = paged_split_len(u.len, Q8);
       u.k0 = u.piece * n, u.k1 = min(u.len, u.k0 + n);  // below k0 for a piece that the request has not
       return u;
     }
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
         int at = sm.start[lo];
         w.b = lo * per;
         w.len = request_len(p, w.b);
-        while (ss >= at + split_count(w.len)) at += split_count(w.len), w.len = request_len(p, ++w.b);
+        while (ss >= at + split_count(w.len, Q8)) at += split_count(w.len, Q8), w.len = request_len(p, ++w.b);
         w.piece = ss - at;
       }
       __syncwarp();
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
     u.hk = __shfl_sync(0xffffffffu, w.hk, src);
     u.piece = __shfl_sync(0xffffffffu, w.piece, src);
     u.len = __shfl_sync(0xffffffffu, w.len, src);
-    const int n = paged_split_len(u.len);
+    const int n = paged_split_len(u.len, Q8);
     u.k0 = u.piece * n, u.k1 = min(u.len, u.k0 + n);
     return u;
   };
@@ -733,7 +738,7 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
           hand_over(0);  // for the cluster's first CTA, where this warp alone has read
           continue;
         }
-        const int pieces = split_count(u.len);
+        const int pieces = split_count(u.len, Q8);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -884,7 +889,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const Paged
   if (bh >= (int64_t)p.B * p.Hq) return;
   const int d0 = kSplit ? (int)(blockIdx.x % slices) * 64 : 0;
   const int b = (int)(bh / p.Hq), h = (int)(bh % p.Hq);
-  const int n = split_count(request_len(p, b)), groups = (n + kJoinGroup - 1) / kJoinGroup;
+  const int n = split_count(request_len(p, b), p.e4m3 != 0), groups = (n + kJoinGroup - 1) / kJoinGroup;
   if (n == 1) return;  // written by its only piece
   const int64_t row0 = (int64_t)b * p.max_splits * p.Hq + h;
   Part<V> r = {};
@@ -975,10 +980,10 @@ cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream
 
 }  // namespace
 
-int32_t paged_max_splits(int64_t cap) {
-  if (cap <= kMaxCluster * kMinSplit) return split_count(cap);
-  if (cap >= (int64_t)kManySplits * 2 * kMinSplit) return kManySplits;
-  return std::max(split_count(cap), (int32_t)kMaxCluster);  // or a request of 2048 keys
+int32_t paged_max_splits(int64_t cap, bool e4m3) {
+  if (cap <= kMaxCluster * kMinSplit) return split_count(cap, e4m3);
+  if (cap >= (int64_t)kManySplits * (e4m3 ? 4 : 2) * kMinSplit) return kManySplits;
+  return std::max(split_count(cap, e4m3), (int32_t)kMaxCluster);  // or a request of 2048 keys
 }
 
 bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::string* why) {

@@ -108,7 +108,7 @@ struct PagedAttnParams {
   unsigned int* status_word;
 };
 // The most pieces of a key range, over all lengths up to cap.
-int32_t paged_max_splits(int64_t cap);
+int32_t paged_max_splits(int64_t cap, bool e4m3);
 bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::string* why);
 
 // Log probabilities of given tokens, entropies and the best alternatives.

@@ -434,7 +434,7 @@ extern "C" bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_te
 // ---------------------------------------------------------------------------
 extern "C" int64_t bi_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t max_len) {
   if (B <= 0 || Hq <= 0 || max_len <= 0 || B > INT32_MAX || Hq > INT32_MAX || !attention_head_dim_ok(D)) return 0;
-  const int64_t n = paged_max_splits(max_len);
+  const int64_t n = paged_max_splits(max_len, false);
   if (n <= 1) return 0;
   const int64_t rows = B * Hq;  // below 2^62
   return rows > INT64_MAX / (n * (D + 2) * 4) ? INT64_MAX : rows * n * (D + 2) * 4;
@@ -505,7 +505,7 @@ bi_status attention_impl(const bi_tensor* q, const Caches& caches, const bi_tens
   p.ld_table = stride_or(page_table, 0, W);
   p.lens = static_cast<const int32_t*>(seq_lens->ptr);
   p.o = o->ptr, p.o_b = stride_or(o, 0, 0), p.o_h = stride_or(o, 1, 0);
-  p.max_splits = paged_max_splits(cap);
+  p.max_splits = paged_max_splits(cap, caches.scaled);
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o ? p.ws_o + B * p.max_splits * Hq * D : nullptr;
   p.B = (int32_t)B, p.Hq = (int32_t)Hq, p.Hkv = (int32_t)Hkv, p.D = (int32_t)D;
