@@ -121,30 +121,29 @@ struct Check {
     that(interleaved(out, in), BI_ERR_INVALID_ARG, "an output overlaps another operand", what);
   }
   // Views of one buffer that interleave without touching (q, k and v of one
-  // projection; keys and values of one cache tensor): with some period s,
+  // projection; keys, values and scales of one cache buffer): with some period s,
   // each view's dimensions either lie within one period or step by whole
   // periods, and the parts of the period they take are apart.
   static bool interleaved(const bi_tensor* x, const bi_tensor* y) {
-    const int64_t es = bytes_of(x->dtype);
     const int64_t d = reinterpret_cast<intptr_t>(y->ptr) - reinterpret_cast<intptr_t>(x->ptr);
-    if (es != bytes_of(y->dtype) || d % es != 0) return false;
     for (int i = 0; i < x->ndim; ++i) {
-      const int64_t s = x->stride[i];
+      const int64_t s = x->stride[i] * bytes_of(x->dtype);
       if (x->shape[i] < 2 || s < 1) continue;
       const int64_t xs = within(x, s), ys = within(y, s);
       if (xs <= 0 || ys <= 0) continue;
-      const int64_t off = ((d / es) % s + s) % s;  // y starts this far into x's period
+      const int64_t off = (d % s + s) % s;  // y starts this far into x's period
       if (off >= xs && off + ys <= s) return true;
     }
     return false;
   }
-  // Elements that t spans inside a period of s; 0 when a dimension fits neither way.
+  // Bytes that t spans inside a period of s; 0 when a dimension fits neither way.
   static int64_t within(const bi_tensor* t, int64_t s) {
-    int64_t span = 1;
+    int64_t span = bytes_of(t->dtype);
     for (int i = 0; i < t->ndim; ++i) {
-      if (t->shape[i] < 2 || t->stride[i] % s == 0) continue;
-      if (t->stride[i] > s) return 0;
-      span += (t->shape[i] - 1) * t->stride[i];
+      const int64_t step = t->stride[i] * bytes_of(t->dtype);
+      if (t->shape[i] < 2 || step % s == 0) continue;
+      if (step > s) return 0;
+      span += (t->shape[i] - 1) * step;
     }
     return span <= s ? span : 0;
   }
