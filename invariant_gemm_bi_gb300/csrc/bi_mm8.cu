@@ -298,8 +298,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= kFirstScale) {
       const int q = warp & 3, set = (warp - kFirstScale) >> 2;  // the set takes every other group
       uint32_t first = 0, turn = 0;                             // groups of the tiles before; exchanges
-      bool ok = true;
-      for (int tile = first_tile; ok && tile < p.num_tiles; tile += stride, first += groups) {
+      // A warp whose wait has run out goes on to the set's next exchange, by which all
+      // four leave: none waits there for one that has left.
+      bool ok = true, leave = false;
+      for (int tile = first_tile; !leave && tile < p.num_tiles; tile += stride, first += groups) {
         const TileCoord tc = decode_tile(tile, p.m_tiles, p.n_tiles);
         const int m0 = (2 * tc.mb + (int)crank) * kBM, n0 = tc.nb * BN;
         // A: this lane's row, 32 q + lane (short A has the first quadrant's only);
@@ -322,8 +324,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if constexpr (A_ROWS == kBM) {
             uint32_t* x = exchange + (2 * set + (turn & 1)) * kBM;  // (a warp is at most one turn ahead)
             x[32 * q + lane] = mine;
-            ok = named_barrier_and(1 + set, 32 * kScaleWarps, ok);  // all leave together
-            if (!ok) break;
+            if (!named_barrier_and(1 + set, 32 * kScaleWarps, ok)) {
+              leave = true;
+              break;
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) rows[c] = x[32 * c + lane];
           }
@@ -332,7 +336,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                          wc.limit_ns, status_code(6, kSiteProducerEmpty));
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
-            if constexpr (A_ROWS == kBM) continue;  // to the next exchange, which all leave by
+            if constexpr (A_ROWS == kBM) continue;
+            leave = true;
             break;
           }
           tc_fence_after_sync();
