@@ -84,9 +84,10 @@ namespace {
 constexpr int kMinSplit = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kManySplits = 128;
+constexpr int kLongPieces = 32 * kMinSplit;
 
 __host__ __device__ inline int32_t paged_split_len(int64_t len, bool e4m3) {
-  int64_t s = len <= kMaxCluster * kMinSplit ? kMinSplit : (e4m3 && len > 32 * kMinSplit ? 4 : 2) * kMinSplit;
+  int64_t s = len <= kMaxCluster * kMinSplit ? kMinSplit : (e4m3 && len > kLongPieces ? 4 : 2) * kMinSplit;
   while (len > kManySplits * s) s *= 2;
   return (int32_t)s;
 }
@@ -519,11 +520,13 @@ __global__ void __launch_bounds__(32 * Shape<C, D, NT>::W, Shape<C, D, NT>::kCta
       // in 8 bits: scales of keys 8 r + g, the values' as 2^vlog * vfrac; vsum = 2^-vlog
       float ks[2 * KT], vlog[2 * KT], vfrac[2 * KT], vsum[2 * KT];
       if constexpr (Q8) {
-        // below 2^-60 (zero, and what is not a number) vfrac takes the rest
+        // below 2^-96 (zero, and what is not a number) vfrac takes the rest: sums of up
+        // to 2^30 keys stay in fp32; from 2^126 on, whose inverse fp32 has not, vfrac is
+        // infinite
         const uint32_t bits = __float_as_uint(vs_next), e = (bits >> 23) & 255u;
-        const bool plain = e >= 127 - 60 && e != 255;
-        const float lg = plain ? (float)((int)e - 127) : (bits << 1) == 0 ? -20.0f : -60.0f;
-        const float fr = plain ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : vs_next * 1152921504606846976.0f;
+        const bool plain = e >= 127 - 96 && e < 127 + 126;
+        const float lg = plain ? (float)((int)e - 127) : (bits << 1) == 0 ? -20.0f : -96.0f;
+        const float fr = plain ? __uint_as_float((bits & 0x807fffffu) | 0x3f800000u) : vs_next * 79228162514264337593543950336.0f;
 #pragma unroll
         for (int r = 0; r < 2 * KT; ++r) {
           ks[r] = __shfl_sync(0xffffffffu, ks_next, 8 * r + g);
@@ -983,7 +986,8 @@ cudaError_t launch_dim(PagedAttnParams& p, int num_sms, bool* joined, cudaStream
 int32_t paged_max_splits(int64_t cap, bool e4m3) {
   if (cap <= kMaxCluster * kMinSplit) return split_count(cap, e4m3);
   if (cap >= (int64_t)kManySplits * (e4m3 ? 4 : 2) * kMinSplit) return kManySplits;
-  return std::max(split_count(cap, e4m3), (int32_t)kMaxCluster);  // or a request of 2048 keys
+  // or a request of 2048 keys, or one of 8192 where pieces get longer there
+  return std::max(split_count(cap, e4m3), e4m3 && cap > kLongPieces ? split_count(kLongPieces, true) : (int32_t)kMaxCluster);
 }
 
 bi_status launch_paged_attention(PagedAttnParams& p, cudaStream_t stream, std::string* why) {
