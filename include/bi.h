@@ -586,8 +586,8 @@ bi_status bi_token_logprobs(const bi_tensor* logits, const bi_tensor* tokens,
  * 448 * 2^e >= the block's size (1 for a block of zeros), and numbers
  * RN_e4m3(x / 2^e): scaling is exact, each element is rounded once, ties to
  * even.  A block whose size is a NaN or infinite has a NaN for its scale and
- * NaNs for its elements.  Operands with scales from elsewhere may have any fp32
- * scales.
+ * NaNs for its elements.  Caches with scales from elsewhere may have any fp32
+ * scales; those of bi_mm_blockscaled are powers of two.
  */
 
 /*
@@ -607,15 +607,18 @@ bi_status bi_quantize_blocks(const bi_tensor* x, int32_t block_rows, const bi_te
  *   a [M,K] e4m3, unit stride on K; b [K,N] e4m3, unit stride on K (the weight
  *   as [N,K], transposed); bases and the other strides multiples of 16 bytes.
  *   a_scales [M, ceil(K/128)], b_scales [ceil(K/128), ceil(N/128)] fp32, any
- *   strides (bi_quantize_blocks's of the weight, transposed).  bias [N] bf16,
- *   fp16 or fp32, any stride, or NULL.  c [M,N] fp32, bf16 or fp16, unit stride
- *   on N.  M, N, K <= 2^30.
+ *   strides (bi_quantize_blocks's of the weight, transposed).  The tensor core
+ *   applies them as exponents: a scale is 2^-126 .. 2^127, and anything else
+ *   (zero, a negative, no power of two) counts as a NaN, whose rows or columns
+ *   of c are NaNs then.  bias [N] bf16, fp16 or fp32, any stride, or NULL.
+ *   c [M,N] fp32, bf16 or fp16, unit stride on N.  M, N, K <= 2^30.
  *
- * Order: D = the block's products, four tensor-core steps of 32 in ascending
- * order; acc = fma(D, RN(a_scale b_scale), acc) in fp32, blocks in ascending
- * order, from zero; then bias and one rounding, as bi_addmm.  Tiles are 64, 128
- * or 256 columns wide by the number of tiles; an element's bits do not depend
- * on it, so row m depends on row m of a and a_scales alone.
+ * Order: steps of 32 in ascending order accumulate in fp32 in the tensor core,
+ * each product times its two scales, from zero over a segment of K = 2048; the
+ * segments' sums are added in order in fp32; then bias and one rounding, as
+ * bi_addmm.  Tiles are 64, 128 or 192 columns wide by the number of tiles; an
+ * element's bits do not depend on it, so row m depends on row m of a and
+ * a_scales alone.
  */
 bi_status bi_mm_blockscaled(const bi_tensor* a, const bi_tensor* a_scales, const bi_tensor* b,
                             const bi_tensor* b_scales, const bi_tensor* bias, const bi_tensor* c,
@@ -658,12 +661,16 @@ bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_tensor* k_cac
  * empty requests and the workspace are bi_paged_attention's.  A head of q that
  * holds a NaN or an infinity gives NaNs.
  *
- * Order: as bi_paged_attention with W = 4; t = RN(RN(s k_scale) f), s the
- * fp32 sum of products of fp16 numbers, q brought to fp16 by a power of two of
- * its own for each head (exact down to 2^-27 of its largest element) and f =
- * scale log2 e with that power taken off.  A key's weight in o is v_scale
- * 2^(t - m'), m' the warp's largest t + log2 |v_scale| so far (whole part), and
- * goes into the product as two fp16 of 2^14 times it; sums are of 2^(t - m).
+ * Order: as bi_paged_attention with W = 4 and, beyond 8192 keys, pieces of 1024
+ * 2^k keys, at most 128 of them; t = RN(RN(s k_scale) f), s the fp32 sum of
+ * products of fp16 numbers, q brought to fp16 by a power of two of its own for
+ * each head (exact down to 2^-27 of its largest element) and f = scale log2 e
+ * with that power taken off.  L = the whole part of log2 |v_scale|, -96 at
+ * least, -20 for a scale of 0 (scales from 2^126 on count as infinite); m = the
+ * largest RN(t + L).  A key's weight in o is 2^(t + L - m) v_scale / 2^L, which
+ * goes into the product as two fp16 of 2^14 times it; sums are of 2^(t + L - m)
+ * 2^-L.  So a key whose e^score |v_scale| is below 2^-126 of the largest one's
+ * counts in neither.
  */
 bi_status bi_paged_attention_quantized(const bi_tensor* q, const bi_tensor* k_cache,
                                        const bi_tensor* k_scales, const bi_tensor* v_cache,
@@ -690,10 +697,10 @@ bi_status bi_paged_attention_quantized(const bi_tensor* q, const bi_tensor* k_ca
  * or which has a NaN for a setting; that is reported.
  *
  * Sums are of 64-bit integers, e^(z - max z) to 2^-33 of itself in units of
- * 2^-43 to 2^-46 of the largest by N (what is below half a unit has weight 0):
- * exact, the same in any order, and on the side of a border that the real sums
- * are on unless those are within about 2^-32 of it.  A row's token depends on
- * that row and its settings alone.
+ * 2^-40 of the largest (below half a unit: 0): exact, the same in any order, and
+ * on the side of a border that the real sums are on unless those are within about
+ * 2^-32 of it, or N units.  A row's token depends on that row and its settings
+ * alone.
  */
 bi_status bi_sample_tokens(const bi_tensor* logits, const bi_tensor* uniforms, const bi_tensor* temperature,
                            const bi_tensor* top_k, const bi_tensor* top_p, const bi_tensor* min_p,
