@@ -28,7 +28,8 @@
 //     elements (the weight as three sums of 16 bits in 32).  The elements of the
 //     bin where a limit is reached, a few hundred as a rule, are gathered by every
 //     CTA and sorted; more than 512 are binned again by their bits until one value
-//     or few elements are left.
+//     or few elements are left.  Where all that is kept is among 512 elements, the
+//     first CTA does the rest from a list of those.
 //   bf16  a bin for each number of 2^-8 .. 2^6 of either sign: counts alone, whose
 //     weights come from a table of the row's (3584 weights in place of a row's
 //     128256), and a bin that is reached is a value already.  Numbers nearer to
@@ -36,6 +37,13 @@
 //     fp32.
 // The CTAs add up a share of the bins each.  The draw sums the kept elements by
 // warps' segments in index order, then looks into one.
+//
+// What bounds it: 256 bf16 rows of 128256 with top-p 0.95 take 115 us (9.7 at the
+// copy rate; 20 MB of 66 in flight at a time, three and a half rounds of CTAs, two an
+// SM).  Of a round's 57000 cycles the reads take 10000, counting 15000 (atomics on
+// shared memory, 3.5 lanes to a bank), sums over the kept 7500, the rest are the
+// row's own chain: maximum, table, three exchanges of the cluster.  8 fp32 rows take
+// 40 us with top-p alone, 21 without limits: the chain, and counting in four sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -71,7 +79,7 @@ constexpr Powers powers() {
 }
 __device__ const Powers kPowers = powers();
 
-constexpr int kList = 512, kShort = 128;  // elements of a bin that are sorted; by rank
+constexpr int kList = 512;  // elements that are sorted
 // bf16: numbers of exponents -8 .. 5, in the order of their values: the positive
 // ones, what lies between, the negative ones.
 constexpr int kBase16 = (127 - 8) << 7, kSpan16 = 14 << 7, kMiddle16 = kSpan16, kBins16 = 2 * kSpan16 + 1;
@@ -96,6 +104,7 @@ struct Shared {
   uint64_t found_w;
   uint32_t found_n, found_bin, found_count;
   uint32_t listed;  // the first CTA's counts for all
+  uint32_t mine_n, mine_at;
   uint64_t list[kList];
   // this CTA's own
   uint64_t warp_w[kMaxWarps], middle_w, cut_w;
@@ -106,6 +115,7 @@ struct Shared {
     struct {
       uint32_t n[kBins], w0[kBins], w1[kBins], w2[kBins];
     };
+    uint64_t mine[kList];
     struct {
       uint64_t weight16[KIND == 0 ? kBins16 : 1];
       uint32_t n16[KIND == 0 ? kBins16 / 2 + 1 : 1];  // two bins a word: a slice has fewer than 2^16 elements
@@ -268,19 +278,23 @@ struct Row {
     int base, each;  // its first bin, and how many
   };
   // Adds every CTA's bins up, a share a CTA, starting from (n, w).
+  // (Shares, and a thread's bins where it has several, are of whole words of n16.)
   template <class F>
   __device__ __forceinline__ void scan_bins(int bins, uint32_t n, uint64_t w, Scan& s, F fetch) const {
     cluster_sync_all();  // every CTA's bins are counted
-    const int per = (bins + cl - 1) / cl, end = min(bins, (rank + 1) * per);
+    const int per = ((bins + cl - 1) / cl + 1) & ~1, end = min(bins, (rank + 1) * per);
     s.each = (per + T - 1) / T;
+    if (s.each > 1) s.each += s.each & 1;
     s.base = rank * per + (int)threadIdx.x * s.each;
     uint32_t sn = 0;
     uint64_t sw = 0;
+    static_assert(kEach % 2 == 0, "bins of a thread");
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      s.bn[i] = 0, s.bw[i] = 0;
-      if (i < s.each && s.base + i < end) fetch(s.base + i, s.bn[i], s.bw[i]);
-      sn += s.bn[i], sw += s.bw[i];
+    for (int i = 0; i < kEach; i += 2) {
+      s.bn[i] = s.bn[i + 1] = 0, s.bw[i] = s.bw[i + 1] = 0;
+      if (i < s.each && s.base + i < end)
+        fetch(s.base + i, s.each > 1 && s.base + i + 1 < end, s.bn[i], s.bw[i], s.bn[i + 1], s.bw[i + 1]);
+      sn += s.bn[i] + s.bn[i + 1], sw += s.bw[i] + s.bw[i + 1];
     }
     uint32_t cn = warp_scan(sn, lane);
     uint64_t cw = warp_scan(sw, lane);
@@ -305,7 +319,7 @@ struct Row {
     s.all_n = n, s.all_w = w;
   }
   __device__ __forceinline__ void scan_bins(uint32_t n, uint64_t w, bool weigh, Scan& s) const {
-    scan_bins(kBins, n, w, s, [&](int b, uint32_t& bn, uint64_t& bw) {
+    auto fetch = [&](int b, uint32_t& bn, uint64_t& bw) {
 #pragma unroll
       for (int r0 = 0; r0 < kMaxCl; r0 += 4) {
         if (r0 >= cl) break;
@@ -327,6 +341,10 @@ struct Row {
           if (weigh) bw += (uint64_t)v[r][1] + ((uint64_t)v[r][2] << 16) + ((uint64_t)v[r][3] << 32);
         }
       }
+    };
+    scan_bins(kBins, n, w, s, [&](int b, bool two, uint32_t& bn, uint64_t& bw, uint32_t& bn1, uint64_t& bw1) {
+      fetch(b, bn, bw);
+      if (two) fetch(b + 1, bn1, bw1);
     });
   }
   // The bin where the running count, or weight, reaches the target: its number and
@@ -358,7 +376,7 @@ struct Row {
         st_cluster_u64(&sm.found_w, lane, hit_w);
       }
     }
-    if (threadIdx.x == 0) sm.listed = 0;
+    if (threadIdx.x == 0) sm.listed = sm.mine_n = 0;
     cluster_sync_all();
     bin = (int)sm.found_bin, in_bin = sm.found_count;
     n = sm.found_n, w = sm.found_w;
@@ -386,13 +404,12 @@ struct Row {
     kmax = hi, kmin = ~lo_inv;
   }
 
-  // Where in a bin of at most kList elements, which `in` holds for, the target is
-  // reached: every CTA gathers and sorts them, by value and then by index.
+  // Gathers the elements that `in` holds for, at most kList of them, into the lists of
+  // the first `to` CTAs: (key, ~index).  First into a list of the CTA's own, in the
+  // place of the bins, which nobody reads any more: a place in the cluster's list is
+  // asked for once (by every warp with a hit, 334 elements took 9800 cycles).
   template <class F>
-  __device__ __forceinline__ void within_list(F in, uint32_t size, bool by_weight, bool weigh, uint64_t target, uint32_t n,
-                                              uint64_t w, float& value, uint32_t& ties, uint64_t& sum) const {
-    int m = 32;  // what is sorted: a power of two
-    while (m < (int)size) m *= 2;
+  __device__ __forceinline__ void gather(F in, int to) const {
     constexpr int U = 4;
     for (int i0 = warp * 32; i0 < count; i0 += U * T) {
       float v[U];
@@ -410,53 +427,83 @@ struct Row {
         const uint32_t hits = __ballot_sync(0xffffffffu, hit[j]);
         if (!hits) continue;
         uint32_t at0 = 0;
-        if (lane == 0)
-          asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-                       : "=r"(at0)
-                       : "r"(cluster_map_shared(smem_u32(&sm.listed), 0)), "r"((uint32_t)__popc(hits))
-                       : "memory");
+        if (lane == 0) at0 = atomicAdd(&sm.mine_n, (uint32_t)__popc(hits));
         at0 = __shfl_sync(0xffffffffu, at0, 0) + __popc(hits & ((1u << lane) - 1));
         if (hit[j] && at0 < (uint32_t)kList)
-          for (int r = 0; r < cl; ++r)
-            st_cluster_u64(&sm.list[at0], r, (uint64_t)key_of(v[j]) << 32 | (0xffffffffu - (uint32_t)(first + i0 + j * T + lane)));
+          sm.mine[at0] = (uint64_t)key_of(v[j]) << 32 | (0xffffffffu - (uint32_t)(first + i0 + j * T + lane));
       }
     }
-    if (size > kShort)
-      for (int i = (int)size + (int)threadIdx.x; i < m; i += T) sm.list[i] = 0;
+    __syncthreads();
+    const uint32_t have = min(sm.mine_n, (uint32_t)kList);
+    if (threadIdx.x == 0 && have > 0)
+      asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
+                   : "=r"(sm.mine_at)
+                   : "r"(cluster_map_shared(smem_u32(&sm.listed), 0)), "r"(have)
+                   : "memory");
+    __syncthreads();
+    for (int r = 0; r < to; ++r)
+      for (uint32_t i = threadIdx.x; i < have; i += T)
+        if (sm.mine_at + i < (uint32_t)kList) st_cluster_u64(&sm.list[sm.mine_at + i], r, sm.mine[i]);
     cluster_sync_all();
-    if (size <= kShort) {  // each to its rank
-      const int i = threadIdx.x;
-      uint64_t mine = 0;
-      int place = 0;
-      if (i < (int)size) {
-        mine = sm.list[i];
-        for (int k = 0; k < (int)size; ++k) place += sm.list[k] > mine;
-      }
-      __syncthreads();
-      if (i < (int)size) sm.list[place] = mine;
-      __syncthreads();
-    } else {
-      for (int k = 2; k <= m; k *= 2)
+  }
+  // Sorts the list (no two alike, none 0), largest first, an element a thread: 32 a
+  // warp by exchanges, then each to its place, which is the number of larger ones in
+  // every run.  (By exchanges through shared memory alone, 334 elements took 13600
+  // cycles.)  A barrier before and after.
+  __device__ __forceinline__ void sort_list(uint32_t size) const {
+    const int runs = ((int)size + 31) / 32;
+    uint64_t x = threadIdx.x < size ? sm.list[threadIdx.x] : 0;
+    if (warp < runs) {
+#pragma unroll
+      for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
         for (int j = k / 2; j > 0; j /= 2) {
-          const int i = threadIdx.x;
-          if (i < m && (i ^ j) > i) {
-            const uint64_t a = sm.list[i], b = sm.list[i ^ j];
-            if ((a < b) == ((i & k) == 0)) sm.list[i] = b, sm.list[i ^ j] = a;
-          }
-          __syncthreads();
+          const uint64_t y = __shfl_xor_sync(0xffffffffu, x, j);
+          const bool larger = ((lane & k) == 0) == ((lane & j) == 0);  // this lane keeps the larger one
+          x = (x > y) == larger ? x : y;
         }
+      sm.list[threadIdx.x] = x;  // (where this warp has read)
     }
-    // running weights, a thread an element
+    __syncthreads();
+    int place = lane;
+    if (warp < runs) {
+#pragma unroll 4
+      for (int r = 0; r < runs; ++r) {
+        const uint64_t* run = sm.list + 32 * r;
+        int n = 0;
+#pragma unroll
+        for (int step = 16; step > 0; step /= 2)
+          if (run[n + step - 1] > x) n += step;
+        if (run[n] > x) ++n;
+        place += r == warp ? 0 : n;
+      }
+    }
+    __syncthreads();
+    if (x != 0) sm.list[place] = x;
+    __syncthreads();
+  }
+  // Running sum over the list's elements, a thread each (one barrier).
+  __device__ __forceinline__ uint64_t list_scan(uint64_t own) const {
+    uint64_t upto = warp_scan(own, lane);
+    if (lane == 31) sm.warp_w[warp] = upto;
+    __syncthreads();
+    for (int k = 0; k < min(warp, kList / 32); ++k) upto += sm.warp_w[k];
+    return upto;
+  }
+
+  // Where in a bin of at most kList elements, which `in` holds for, the target is
+  // reached: every CTA gathers and sorts them, by value and then by index.
+  template <class F>
+  __device__ __forceinline__ void within_list(F in, uint32_t size, bool by_weight, bool weigh, uint64_t target, uint32_t n,
+                                              uint64_t w, float& value, uint32_t& ties, uint64_t& sum) const {
+    gather(in, cl);
+    sort_list(size);
     const int i = threadIdx.x;
     const bool there = i < (int)size;
     const uint64_t e = there ? sm.list[i] : 0;
     const uint32_t key = (uint32_t)(e >> 32);
     const uint64_t own = there && weigh ? weight(of_key(key)) : 0;
-    uint64_t upto = warp_scan(own, lane);
-    if (lane == 31) sm.warp_w[warp] = upto;
-    __syncthreads();
-    for (int k = 0; k < min(warp, kList / 32); ++k) upto += sm.warp_w[k];
-    upto += w;
+    const uint64_t upto = list_scan(own) + w;
     const uint64_t to = by_weight ? upto : (uint64_t)n + i + 1, from = by_weight ? upto - own : (uint64_t)n + i;
     if (there && from < target && to >= target) {
       int same = i;  // the first element of its value
@@ -465,6 +512,45 @@ struct Row {
     }
     __syncthreads();
     value = of_key(sm.cut_key), ties = sm.cut_n, sum = sm.cut_w;
+  }
+
+  // The whole draw from at most kList elements, those of the bins up to `bin`, one of
+  // which holds the last one kept: the first CTA gathers and sorts them and finds both
+  // limits there (top-p's of `sum`, or of the first `limit` if that is 0), then sorts
+  // them by index.  A row of 128256 fp32 with k = 50 and p = 0.9 takes 27 us this way;
+  // with a list for each limit and the draw over the slices it took 50.
+  __device__ __forceinline__ int draw_from_list(int bin, uint32_t size, uint32_t limit, bool by_p, float top_p, uint64_t sum,
+                                                float u) const {
+    gather([&](float v, uint32_t) {
+      const float y = bits_below(v);
+      return y < kRange && (int)(y * kBinsPerBit) <= bin;
+    }, 1);
+    if (rank != 0) return -1;
+    sort_list(size);
+    const int i = threadIdx.x;
+    const bool there = i < (int)size;
+    const uint64_t e = there ? sm.list[i] : 0;
+    const float v = of_key((uint32_t)(e >> 32));
+    const uint64_t own = there ? weight(v) : 0, upto = list_scan(own);
+    if (i + 1 == (int)min(limit, size)) sm.cut_w = upto;
+    __syncthreads();
+    if (sum == 0) sum = sm.cut_w;
+    const bool kept = there && (uint32_t)i < limit && v >= sm.floor && (!by_p || upto - own < share(top_p, sum));
+    // by index from here on, the weight in the low bits
+    constexpr int kBits = 41;
+    static_assert(kMaxVocab < 1 << (62 - kBits), "index and weight in a word");
+    if (there) sm.list[i] = (uint64_t)((1u << (62 - kBits)) - 1 - (0xffffffffu - (uint32_t)e)) << kBits | (kept ? own : 0);
+    __syncthreads();
+    sort_list(size);
+    const uint64_t x = there ? sm.list[i] : 0, w = x & (((uint64_t)1 << kBits) - 1), run = list_scan(w);
+    if (i == kList - 1) sm.cut_w = run;
+    __syncthreads();
+    const uint64_t all = sm.cut_w, want = min(all - 1, (uint64_t)((double)u * (double)all));
+    return there && run - w <= want && run > want ? (int)((1u << (62 - kBits)) - 1 - (uint32_t)(x >> kBits)) : -1;
+  }
+  // What top-p keeps of a sum.
+  __device__ __forceinline__ uint64_t share(float top_p, uint64_t sum) const {
+    return min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
   }
 
   // Where in a bin the target is reached: everything above `value`, and its first
@@ -513,6 +599,8 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t r = blockIdx.x / (unsigned)cl;
   const int rank = (int)(blockIdx.x % (unsigned)cl), first = min(p.N, rank * slice), count = min(p.N - first, slice);
+
+  cluster_arrive_relaxed();  // waited for before another CTA's shared memory is written
 
   // --- the row's settings
   const float u = __ldg(p.u + r), t_in = p.temperature ? __ldg(p.temperature + r) : 1.0f;
@@ -588,6 +676,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   Row<KIND, T> row{sm, data + off, count, first, cl, rank, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, warp, lane};
   {
     const uint32_t k = row.block_max(bad ? 0xffffffffu : key_of(top));  // above any number's
+    cluster_wait();
     row.to_all([&](int to) { st_cluster_u32(&sm.top[rank], to, k); });
   }
   cluster_sync_all();
@@ -638,6 +727,13 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
     uint64_t w = 0, sum = 0;
     int bin;
     bool done = false;
+    auto store = [&](int token) {  // of the one thread that has it
+      if (token < 0) return;
+      if (p.tok64)
+        static_cast<long long*>(p.tokens)[r] = token;
+      else
+        static_cast<int*>(p.tokens)[r] = token;
+    };
     if constexpr (KIND == 0) {
       if (tabled) {
         uint64_t mine = 0;
@@ -652,19 +748,27 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
           mine = warp_sum(mine);
           if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.middle_w), (unsigned long long)mine);
         }
-        row.scan_bins(kBins16, 0, 0, s, [&](int b, uint32_t& bn, uint64_t& bw) {
-          uint32_t v[kMaxCl];
+        auto weigh = [&](int b, uint32_t n) -> uint64_t {
+          if (b != kMiddle16) return n * sm.weight16[b];
+          uint64_t w = 0;
+          const uint32_t a = smem_u32(&sm.middle_w);
+          for (int c = 0; c < cl; ++c) w += (uint64_t)ld_cluster_u32(a, c) | (uint64_t)ld_cluster_u32(a + 4, c) << 32;
+          return w;
+        };
+        row.scan_bins(kBins16, 0, 0, s, [&](int b, bool two, uint32_t& bn, uint64_t& bw, uint32_t& bn1, uint64_t& bw1) {
+          uint32_t lo = 0, hi = 0;
 #pragma unroll
-          for (int c = 0; c < kMaxCl; ++c) v[c] = ld_cluster_u32(smem_u32(&sm.n16[b >> 1]), (uint32_t)min(c, cl - 1));
+          for (int c0 = 0; c0 < kMaxCl; c0 += 4) {
+            if (c0 >= cl) break;
+            uint32_t v[4];
 #pragma unroll
-          for (int c = 0; c < kMaxCl; ++c) bn += c < cl ? (b & 1 ? v[c] >> 16 : v[c] & 0xffffu) : 0;
-          if (b != kMiddle16)
-            bw = bn * sm.weight16[b];
-          else
-            for (int c = 0; c < cl; ++c) {
-              const uint32_t a = smem_u32(&sm.middle_w);
-              bw += (uint64_t)ld_cluster_u32(a, c) | (uint64_t)ld_cluster_u32(a + 4, c) << 32;
-            }
+            for (int c = 0; c < 4; ++c) v[c] = ld_cluster_u32(smem_u32(&sm.n16[b >> 1]), (uint32_t)min(c0 + c, cl - 1));
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (c0 + c < cl) lo += v[c] & 0xffffu, hi += v[c] >> 16;
+          }
+          bn = b & 1 ? hi : lo, bw = weigh(b, bn);
+          if (two) bn1 = hi, bw1 = weigh(b + 1, hi);
         });
         done = true;
         const uint64_t all = s.all_w;
@@ -679,7 +783,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
           }
         }
         if (done && by_p) {
-          const uint64_t want = min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
+          const uint64_t want = row.share(top_p, sum);
           if (row.find_bin(s, true, want, n, w, bin, in_bin)) {
             if (bin == kMiddle16) {
               done = false;
@@ -706,12 +810,14 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
       row.scan_bins(0, 0, by_p, s);
       sum = s.all_w;
       if (by_k && row.find_bin(s, false, (uint64_t)top_k, n, w, bin, in_bin)) {
+        if (n + in_bin <= kList) return store(row.draw_from_list(bin, n + in_bin, (uint32_t)top_k, by_p, top_p, 0, u));
         row.within_bin(bin, in_bin, false, by_p, (uint64_t)top_k, n, w, v, m, sum);
         lower(v, m);
       }
       if (by_p) {
-        const uint64_t want = min(sum, max((uint64_t)1, (uint64_t)ceil((double)top_p * (double)sum)));
+        const uint64_t want = row.share(top_p, sum);
         if (row.find_bin(s, true, want, n, w, bin, in_bin)) {
+          if (n + in_bin <= kList) return store(row.draw_from_list(bin, n + in_bin, 0xffffffffu, true, top_p, sum, u));
           row.within_bin(bin, in_bin, true, true, want, n, w, v, m, sum);
           lower(v, m);
         }
