@@ -6,6 +6,10 @@
 // bits); neighbouring threads take neighbouring units of a token, whose heads
 // lie side by side in the cache, and each thread four units, keys and values
 // of two tokens, whose loads are all requested before the first is used.
+//
+// Measured: 131071 tokens of 8 heads of 128 into bf16, 815 MB in and out, 132 us,
+// 6.2 TB/s (0.91 of the copy rate); 1021 tokens 3.5 us, three dependent loads
+// (slot, row, store) and the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

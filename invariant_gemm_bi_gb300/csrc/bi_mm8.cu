@@ -31,7 +31,16 @@
 // At decode sizes the weight's bytes set the pace: BN is then narrower, so that
 // there are pairs enough, and A stages of at most 32 rows leave room for more of
 // B in flight (the tensor core reads 128 rows either way; rows past M are never
-// stored).
+// stored): 16 x 14336 x 4096 15.4 us against 19.5, 16 x 4096 x 4096 9.5 against 13.7.
+//
+// Measured (M x N x K, bf16 results): 8192 x 14336 x 4096 308 us alone, 3.1 PFLOP/s,
+// 344 in a long run under the power limit; 4096^3 50 us, 2.75 PFLOP/s; 2048 x 4096 x
+// 4096 32 us; 300 x 14336 x 4096 23.7 us; 16 x 14336 x 4096 15.4 us, 3.8 TB/s: start
+// (TMEM, barriers, a cluster's exchange, 3 us), the copies, the last segment's sums.
+// Large ones are bound by the issue of MMAs, 65 cycles for the four of a block and 160 of
+// commits and waits (tensor pipe 66 % busy at 4096^3, 75 tiles on 76 pairs).
+// One set of scale warps was waited for (4 % at 8192); stages of two blocks at full A
+// leave too few of them; exponents written a stage at a time cost the issuer a wait each.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -484,6 +493,8 @@ template <int BN>
 cudaError_t launch_width(ScaledParams& p, cudaStream_t stream) {
   constexpr int kSlot = 104 + (BN == 192 ? 0 : BN == 128 ? 3 : 6);
   if (p.M <= kShortARows) return launch_variant<BN, kShortARows, true>(p, stream, kSlot);
+  // (hints to L2: 300 x 14336 x 4096 23.7 us against 24.0, 16 rows of it 15.4 against
+  // 15.9; from three row tiles on no difference, and B is better left where it is)
   return p.m_tiles <= 2 ? launch_variant<BN, kBM, true>(p, stream, kSlot + 1)
                         : launch_variant<BN, kBM, false>(p, stream, kSlot + 2);
 }
@@ -500,7 +511,9 @@ bi_status launch_scaled_gemm(const ScaledProblem& g, cudaStream_t stream, std::s
   p.m_tiles = (int32_t)((g.M + 2 * kBM - 1) / (2 * kBM));
   p.k_blocks = (int32_t)((g.K + kBK8 - 1) / kBK8);
   // The width whose rounds of tiles take least: a K block takes a pair a time of
-  // about BN + 128 columns' (short A: BN + 64); the wider one among equals.
+  // about BN + 128 columns' (short A: BN + 64); the wider one among equals.  (192, 128,
+  // 64 columns: 16 x 14336 x 4096 15.4, 17.1, 19.8 us; 16 x 4096 x 14336 28.7, 22.4,
+  // 21.5; 300 x 4096 x 4096 14.2, 13.1, 19.4; 4096^3 50, 59, 108.)
   const int64_t pairs = dev.num_sms / 2;
   auto tiles = [&](int64_t bn) { return (int64_t)p.m_tiles * ((g.N + bn - 1) / bn); };
   const int64_t each = g.M <= kShortARows ? 64 : 128;

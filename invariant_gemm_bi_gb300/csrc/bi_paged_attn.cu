@@ -43,6 +43,18 @@
 // longer pieces 160 us, 5.97 TB/s, near the memory's rate (161 with p in three
 // pieces, below).
 //
+// Caches in 8 bits (template kCache8): half the bytes and the same work a key, so
+// that issue weighs twice as much.  A slot is 32 keys of D bytes at every D, three of
+// them a warp, 12 warps an SM at D = 128; chunks of 16 dimensions are read back and
+// brought to fp16 in registers, two e4m3 a conversion, for the same mma.sync; values
+// are read by transposing pairs of dimensions and sorted by byte permutes.  The batch
+// above, 493 MB: 109 us, 4.5 TB/s (72.7 us at the copy rate; 40 x 8192 keys 144 us,
+// 4.8 TB/s): 127 of those 144 us are the copies alone, 128 bytes a key and head, and
+// the join and the launch take 8; issue is 51 % busy, tensor pipes 20 %.  16 warps an
+// SM of 16-key tiles 139 us, 8 warps with six slots 133, four slots 123, tiles of 64
+// keys 129 (the kept one 120 at that time), one running maximum for weights and sums
+// in place of two 115.
+//
 // Arithmetic, per query head: t = RN(s c) with c = RN(scale log2 e); a running
 // maximum m per warp over its tiles; p = 2^(t - m) (the SFU's approximation);
 // l sums the unrounded p in fp32; the value product takes p in the cache's
