@@ -37,10 +37,11 @@
 // 344 in a long run under the power limit; 4096^3 50 us, 2.75 PFLOP/s; 2048 x 4096 x
 // 4096 32 us; 300 x 14336 x 4096 23.7 us; 16 x 14336 x 4096 15.4 us, 3.8 TB/s: start
 // (TMEM, barriers, a cluster's exchange, 3 us), the copies, the last segment's sums.
-// Large ones are bound by the issue of MMAs, 65 cycles for the four of a block and 160 of
-// commits and waits (tensor pipe 66 % busy at 4096^3, 75 tiles on 76 pairs).
-// One set of scale warps was waited for (4 % at 8192); stages of two blocks at full A
-// leave too few of them; exponents written a stage at a time cost the issuer a wait each.
+// Large ones are bound by the tensor cores and their power: a block's four MMAs take 400
+// cycles at the 16-bit product's measured rate doubled, and the issuer 225; 4096^3 (352
+// tiles on 76 pairs, 4.6 rounds) keeps the pipe 66 % busy.  One set of scale warps was
+// waited for; stages of two blocks at full A leave too few of them; exponents written a
+// stage at a time cost the issuer a wait each.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -147,6 +148,43 @@ __device__ __forceinline__ float load_now(const float* p) {
 __device__ __forceinline__ uint32_t exponent_byte(float scale) {
   const uint32_t b = __float_as_uint(scale);
   return (b & 0x807fffffu) == 0 && b != 0 ? b >> 23 : 255u;
+}
+
+// A warp's 32 x 32 results at (m0, n0), a row a lane, into rows that 16-byte stores do
+// not fit: through the warp's buffer, so that it writes a row at a time (fp32: half of
+// two).  5157 x 694 x 369 takes 13 us this way; with a row of its own a lane, 2 bytes a
+// sector, a call took 44.
+__device__ __forceinline__ void store_32_rows(const OutDesc& o, uint8_t* buf, int m0, int n0, int lane, const float (&f)[32]) {
+  const uint32_t to = smem_u32(buf);
+  if (!o.out_f32) {
+    __syncwarp();
+    stage_32(o, to, lane, f);
+    __syncwarp();
+    uint16_t* c = static_cast<uint16_t*>(o.c) + (int64_t)m0 * o.ldc + n0 + lane;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const uint16_t v = *reinterpret_cast<const uint16_t*>(buf + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2);
+      if (m0 + i < o.M && n0 + lane < o.N) c[i * o.ldc] = v;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const int i = 16 * h + 4 * cc;
+        st_shared_v4(to + lane * 64 + ((cc ^ ((lane >> 1) & 3)) << 4), __float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+                     __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3]));
+      }
+      __syncwarp();
+      const int col = lane & 15, n = n0 + 16 * h + col;
+#pragma unroll 8
+      for (int i = lane >> 4; i < 32; i += 2) {
+        const float v = *reinterpret_cast<const float*>(buf + i * 64 + (((col >> 2) ^ ((i >> 1) & 3)) << 4) + (col & 3) * 4);
+        if (m0 + i < o.M && n < o.N) static_cast<float*>(o.c)[(int64_t)(m0 + i) * o.ldc + n] = v;
+      }
+    }
+  }
 }
 
 template <int BN, int A_ROWS, bool STREAM_B>
@@ -446,6 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_store_3d(o.tma_c, sbuf, n0 + 32 * j, m0, 0);
             bulk_commit();
           }
+        } else if (Lay::STAGING_BYTES > 0 && !o.vec_store) {
+          store_32_rows(o, smem + (sbuf - base), m0, n0 + 32 * j, lane, f);
         } else {
           store_32_direct(o, 0, m0 + lane, n0 + 32 * j, true, f);
         }
