@@ -38,11 +38,11 @@
 // The CTAs add up a share of the bins each.  The draw sums the kept elements by
 // warps' segments in index order, then looks into one.
 //
-// What bounds it: 256 bf16 rows of 128256 with top-p 0.95 take 115 us (9.7 at the
+// What bounds it: 256 bf16 rows of 128256 with top-p 0.95 take 108 us (9.7 at the
 // copy rate; 20 MB of 66 in flight at a time, three and a half rounds of CTAs, two an
-// SM).  Of a round's 57000 cycles the reads take 10000, counting 15000 (atomics on
-// shared memory, 3.5 lanes to a bank), sums over the kept 7500, the rest are the
-// row's own chain: maximum, table, three exchanges of the cluster.  8 fp32 rows take
+// SM).  Of a round's 50000 cycles the reads take 10000, counting 15000 (atomics on
+// shared memory, 3.5 lanes to a bank), the rest are the row's own chain: maximum,
+// table, three exchanges of the cluster, the draw.  8 fp32 rows take
 // 40 us with top-p alone, 21 without limits: the chain, and counting in four sums.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -840,13 +840,37 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
     w = warp_sum(w);
     n = __reduce_add_sync(0xffffffffu, n);
   };
-  {
+  auto sum_segments = [&] {
     const int from = min(count, warp * len), to = min(count, from + len);
     uint64_t w;
     uint32_t n;
     sum_of(from, to, w, n);
     if (lane == 0) sm.warp_w[warp] = w, sm.warp_n[warp] = n;
     __syncthreads();
+  };
+  // Where the row's values are counted, a CTA's sum follows from its counts, unless
+  // the cut is among the numbers near zero; only the CTA that has the token then goes
+  // over its elements (256 rows: 108 us against 112).
+  const bool counted = KIND == 0 && tabled && (by_k || by_p) && !(fabsf(cut) < 0.00390625f);
+  {
+    if constexpr (KIND == 0) {
+      if (counted) {
+        uint64_t w = 0;
+        uint32_t n = 0;
+        for (int b = threadIdx.x; b < kBins16; b += T) {
+          const uint32_t own = b & 1 ? sm.n16[b >> 1] >> 16 : sm.n16[b >> 1] & 0xffffu;
+          const float v = b == kMiddle16 ? 0.0f : value16(b);
+          if (v > cut)
+            w += b == kMiddle16 ? sm.middle_w : own * sm.weight16[b];
+          else if (v == cut)
+            n += own;
+        }
+        w = warp_sum(w), n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) sm.warp_w[warp] = w, sm.warp_n[warp] = n;
+        __syncthreads();
+      }
+    }
+    if (!counted) sum_segments();
     if (warp == 0) {
       const uint64_t mw = lane < kWarps ? sm.warp_w[lane] : 0;
       const uint64_t all_w = warp_sum(mw);
@@ -874,6 +898,7 @@ __global__ void __launch_bounds__(T, 1024 / T) sample_kernel(const SampleParams 
   }
   const uint64_t upto_cta = run + sm.sum_w[rank] + min(sm.sum_n[rank], ties - seen) * each;
   if (run > want || upto_cta <= want) return;  // another CTA's (none reads another's memory from here on)
+  if (counted) sum_segments();
   // its segments, a lane each
   int seg;
   {
