@@ -13,6 +13,7 @@ from tests import serving_reference as sref
 from tests.gpu_helpers import bits_equal
 from tests.test_gpu_quantized import (BF16, E4M3, F16, F32, _clean_status, _i32, _i64, _normal, _operands,  # noqa: F401
                                       _problem, _uniform)
+from tests.test_gpu_sample import _check, _f32
 
 pytestmark = pytest.mark.gpu
 FAR = 2 ** 32 + 2 ** 20  # elements
@@ -195,6 +196,22 @@ def test_sample_longest_rows(dt, R):
     for r in range(0, R, 1 if R == 2 else 37):
         want, near = ref.sample(x64[r % 2], float(u[r]), 1.0, int(k[r]), float(p[r]))
         assert near or got[r] == want, r
+
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("ties", [False, True])
+def test_sample_lists_of_every_length(dt, ties):
+    # top-k around the lengths of a warp's run and of the whole list, and past it; with few
+    # values, many elements of which are alike, the limit falls among equals
+    ks = (1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 400, 480, 500, 511, 512, 513, 600, 0)
+    x = _normal((3 * len(ks), 5000), F32, 21, 1.5)
+    if ties:
+        x = torch.round(4 * x) / 4
+    R = x.shape[0]
+    k = _i32([v for v in ks for _ in range(3)])
+    p = _f32([1.0, 0.9, 0.3] * len(ks))
+    m = _f32([0.0, 0.0, 0.02, 0.0, 0.2] * R)[:R].contiguous()
+    _check(x.to(dt), _uniform((R,), 22), temperature=_f32([0.8, 1.3] * R)[:R].contiguous(), top_k=k, top_p=p, min_p=m)
 
 
 def test_sample_many_short_rows():

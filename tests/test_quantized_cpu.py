@@ -140,6 +140,23 @@ def test_store_quantized_refusals(lib):
                               _r(a.t([10, 16, 2, 64], E4M3)), _r(a.t([10, 16, 2, 64], E4M3)), None) == DTYPE
 
 
+def test_store_quantized_pages_that_hold_everything(lib):
+    # a page's keys, values and scales side by side in one buffer, 4352 bytes a page
+    def call(keys=0, values=2048, k_scales=4096, v_scales=4224, page=4352):
+        at = 0x7E0000000000
+        cache = lambda off: lambda a, o: a.t([10, 16, 2, 64], E4M3, [page, 128, 64, 1], ptr=at + off)  # noqa: E731
+        scale = lambda off: lambda a, o: a.t([10, 16, 2], F32, [page // 4, 2, 1], ptr=at + off)  # noqa: E731
+        return _store(lib, None, pos=None, q=None, qo=None, kc=cache(keys), vc=cache(values), ks=scale(k_scales), vs=scale(v_scales))
+    if no_gpu:
+        assert call() == REACHED
+        assert call(keys=4352 * 3) == REACHED       # the views start in different pages
+    assert call(k_scales=4092) == INVALID           # the last value's byte is the first scale's
+    assert call(v_scales=4220) == INVALID
+    assert call(v_scales=4352 - 124) == INVALID     # into the next page's keys
+    assert call(values=2047) == INVALID
+    assert "overlap" in binding.last_error_message()
+
+
 def _load(lib, **change):
     a = Arena()
     o = _with(dict(slots=a.t([7], I64), **_caches(a), k=a.t([7, 2, 64], BF16), v=a.t([7, 2, 64], BF16)), a, change)
