@@ -61,6 +61,26 @@ def test_mm_streams_and_graph():
     assert torch.equal(out.float(), 2 * want[0].float())
 
 
+def test_mm_beside_the_library_s_other_kernels():
+    # kernels that take tensor memory too, on other streams at the same time
+    ops = _operands(500, 3000, 2500, 1)
+    x, w = _normal((400, 1024), BF16, 2), _normal((1024, 2048), BF16, 3)
+    q, k, v = (_normal((16, 600, 64), BF16, i) for i in (4, 5, 6))
+    calls = [lambda st: bi.bi_mm_blockscaled(*ops, stream=st), lambda st: bi.bi_mm(x, w, stream=st),
+             lambda st: bi.bi_attention(q, k, v, 0.125, stream=st)]
+    want = [c(None) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = []
+    for _ in range(10):
+        for c, st in zip(calls, streams):
+            with torch.cuda.stream(st):  # allocated for the stream that writes it
+                outs.append(c(st))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert bits_equal(o, want[i % 3])
+
+
 # -- attention over the cache in 8 bits ------------------------------------------------------
 
 @pytest.mark.parametrize("shift", [-90, 60, 118])
