@@ -20,14 +20,15 @@
 // pieces of eight elements, of the first and the second half of the rotated
 // part (their 8 pairs in either layout) or of the unrotated tail -- so
 // neighbouring lanes move neighbouring 16 bytes.  Each lane copies its units to
-// places of its own in shared memory, six heads ahead, by asynchronous copies:
+// places of its own in shared memory, three heads ahead, by asynchronous copies:
 // no registers and no barrier, and its 8 sines and cosines stay in registers
 // over its heads.  (8191 tokens of 32 + 8 + 8 heads of 128, 201 MB: loads into
-// registers, eight heads a thread, 47 us; this way 38 us.  16383 tokens of 32
-// heads, 268 MB: 52 and 40 us, 6.64 TB/s.  The 8191 are 2048 blocks, 3.37 waves
-// of four an SM, each with the position's, then the slot's latency at its start.
-// Types other than bf16 or fp16 throughout take rings twice as large, two
-// blocks an SM: 8191 x 32 x 128 fp32 73 us, 1.8 times its bytes.)  Operands
+// registers, eight heads a thread, 47 us; this way 36 us, six heads ahead 38.
+// 16383 tokens of 32 heads, 268 MB: 52 and 41 us, 6.5 TB/s.  The 8191 are 2048
+// blocks, 3.37 waves of four an SM, each with the position's, then the slot's
+// latency at its start.  Types other than bf16 or fp16 throughout take rings twice
+// as large: 8191 x 32 x 128 fp32 60 us, 1.5 times its bytes; two blocks an SM and
+// six heads ahead 73.)  Operands
 // whose rows or split are not 16-byte aligned take units of one pair with the
 // same arithmetic, so the bits do not depend on the layout; heads one after the
 // other, 8191 x 32 x 96 bf16 with 24 rotated 77 us, 5.2 times its bytes.  The
@@ -185,9 +186,10 @@ __device__ __forceinline__ char* target(const RopeParams& p, const TokenPlace& a
 // way or the other next to 448 2^e, would decide a whole head's scale).  It is
 // up to twice the largest element: at most one binade at the small end.
 //
-// Measured: 8191 tokens of 32 + 8 + 8 heads of 128, bf16, 185 MB, 44 us, 4.2 TB/s: by
+// Measured: 8191 tokens of 32 + 8 + 8 heads of 128, bf16, 185 MB, 41.5 us, 4.5 TB/s: by
 // issue (57 %, 285 instructions a warp and unit) and by waves (2048 blocks are 3.37
-// of 608); 64 tokens 4.0 us.  Three blocks an SM of more slots gained nothing.
+// of 608); fp32 85 us (105 with two blocks an SM); 64 tokens 4.0 us.  Six heads ahead
+// 44.8 us, two 41.6; half the heads a block 51.6 (each block has its sines to compute).
 __device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t pair_size(float x1, float x2, float magnitude) {
   return size_bits(__fmul_rn(__fadd_rn(fabsf(x1), fabsf(x2)), magnitude));
@@ -206,7 +208,7 @@ __device__ __forceinline__ float* scale_target(const RopeParams& p, const TokenP
 // units z * 32 ...  kSlots: heads that a lane requests ahead.
 constexpr int kMaxTokens = 32;
 template <int QK, int QO, int KV, int CK, int kSlots>
-__global__ void __launch_bounds__(256, QK == kAny ? 2 : 4)
+__global__ void __launch_bounds__(256, 4)
     rope_vec_kernel(const __grid_constant__ RopeParams p, int units, int tokens, int heads) {
   constexpr int kPieces = QK == kAny ? 4 : 2;  // 16-byte pieces of a unit: fp32 has two an octet
   extern __shared__ __align__(16) unsigned char dyn[];
@@ -433,16 +435,16 @@ cudaError_t launch_vec(const RopeParams& p, int num_sms, cudaStream_t stream) {
   const unsigned z = (unsigned)((units + 31) / 32);
   const size_t turns = sizeof(float2) * tokens * p.half;
   constexpr size_t kSlot = (QK == kAny ? 4 : 2) * 256 * 16;
-  // All heads a block, six a warp requested ahead, once that fills the GPU
+  // All heads a block, three a warp requested ahead, once that fills the GPU
   // twice; below, a head a warp (a latency-bound call wants every load in
   // flight at once).
   if (blocks * z >= 4 * (int64_t)num_sms || heads > 8 * 65535) {
-    constexpr size_t kRing = 6 * kSlot;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&rope_vec_kernel<QK, QO, KV, CK, 6>),
+    constexpr size_t kRing = 3 * kSlot;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(&rope_vec_kernel<QK, QO, KV, CK, 3>),
                                   (int)(kRing + sizeof(float2) * kMaxTokens * BI_ROPE_MAX_PAIRS),
                                   (CK == kE4m3 ? 96 : 56) + QK + 1);
     if (e != cudaSuccess) return e;
-    rope_vec_kernel<QK, QO, KV, CK, 6>
+    rope_vec_kernel<QK, QO, KV, CK, 3>
         <<<dim3((unsigned)blocks, 1, z), 256, kRing + turns, stream>>>(p, units, tokens, heads);
   } else {
     const unsigned y = (unsigned)((heads + 7) / 8);
