@@ -334,11 +334,13 @@ struct Row {
             v[r][3] = ld_cluster_u32(smem_u32(&sm.w2[b]), from);
           }
         }
+        // (A CTA that there is not adds zeros.  With an exit from the loop in their place the
+        // bf16 kernels came out of the compiler without the lower words of some of the sums.)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if (r0 + r >= cl) break;
-          bn += v[r][0];
-          if (weigh) bw += (uint64_t)v[r][1] + ((uint64_t)v[r][2] << 16) + ((uint64_t)v[r][3] << 32);
+          const uint64_t there = r0 + r < cl ? 1 : 0;
+          bn += (uint32_t)there * v[r][0];
+          if (weigh) bw += there * ((uint64_t)v[r][1] + ((uint64_t)v[r][2] << 16) + ((uint64_t)v[r][3] << 32));
         }
       }
     };
