@@ -80,6 +80,29 @@ constexpr Powers powers() {
 __device__ const Powers kPowers = powers();
 
 constexpr int kList = 512;  // elements that are sorted
+
+// Shared memory that other CTAs of the cluster write or read, and the barrier of the
+// cluster between a word's last use and its next one.  ("Searches" are calls of
+// find_bin; a scan, scan_bins, has a barrier before it reads and one after.)
+//   top              written once, behind the start-up barrier.
+//   lo, hi           range_of: read behind its barrier; written by the next range_of
+//                    of a limit behind the scan's barriers between them, by the other
+//                    limit's behind its search's.
+//   part_n, part_w   scan_bins: read behind its second barrier; written again behind
+//                    the next scan's first.
+//   found_*          find_bin: read behind its barrier.  The same limit's next search
+//                    comes behind range_of's barrier (within_bin's loop) or a scan's
+//                    (bf16 rows that go on without their table).  Between a search by
+//                    count and one by weight there need not be any: two sets.
+//   listed           reset by the first CTA before a search's barrier, added to behind
+//                    it; the list before was closed by gather's barrier.
+//   list             gather: read behind its barrier by its own CTA; written again
+//                    behind the next search's, which every CTA reaches when it has read.
+//   sum_w, sum_n     written once, in the draw; read behind its barrier.
+//   n, w0-w2, n16, middle_w  read by scans, between their two barriers; cleared, counted
+//                    again or used as `mine` behind the second.
+// Behind the last barrier of a row's path no CTA reads or writes another's memory, so
+// each leaves when it is done.
 // bf16: numbers of exponents -8 .. 5, in the order of their values: the positive
 // ones, what lies between, the negative ones.
 constexpr int kBase16 = (127 - 8) << 7, kSpan16 = 14 << 7, kMiddle16 = kSpan16, kBins16 = 2 * kSpan16 + 1;
@@ -101,8 +124,8 @@ struct Shared {
   uint32_t top[kMaxCl], lo[kMaxCl], hi[kMaxCl];
   uint64_t part_w[kMaxCl], sum_w[kMaxCl];
   uint32_t part_n[kMaxCl], sum_n[kMaxCl];
-  uint64_t found_w;
-  uint32_t found_n, found_bin, found_count;
+  uint64_t found_w[2];  // [0]: where a count is reached, [1]: where a weight is
+  uint32_t found_n[2], found_bin[2], found_count[2];
   uint32_t listed;  // the first CTA's counts for all
   uint32_t mine_n, mine_at;
   uint64_t list[kList];
@@ -351,7 +374,8 @@ struct Row {
   }
   // The bin where the running count, or weight, reaches the target: its number and
   // count; n and w get what lies before it.  False if all of them hold less (the
-  // same in every CTA).
+  // same in every CTA).  A search by weight may follow one by count at once, with
+  // warps that have yet to read the first one's answer: each has words of its own.
   __device__ __forceinline__ bool find_bin(const Scan& s, bool by_weight, uint64_t target, uint32_t& n, uint64_t& w, int& bin,
                                            uint32_t& in_bin) const {
     if ((by_weight ? s.all_w : (uint64_t)s.all_n) < target) return false;
@@ -372,16 +396,16 @@ struct Row {
       hit_count = __shfl_sync(0xffffffffu, hit_count, from);
       hit_w = __shfl_sync(0xffffffffu, hit_w, from);
       if (lane < cl) {
-        st_cluster_u32(&sm.found_bin, lane, (uint32_t)hit);
-        st_cluster_u32(&sm.found_count, lane, hit_count);
-        st_cluster_u32(&sm.found_n, lane, hit_n);
-        st_cluster_u64(&sm.found_w, lane, hit_w);
+        st_cluster_u32(&sm.found_bin[by_weight], lane, (uint32_t)hit);
+        st_cluster_u32(&sm.found_count[by_weight], lane, hit_count);
+        st_cluster_u32(&sm.found_n[by_weight], lane, hit_n);
+        st_cluster_u64(&sm.found_w[by_weight], lane, hit_w);
       }
     }
     if (threadIdx.x == 0) sm.listed = sm.mine_n = 0;
     cluster_sync_all();
-    bin = (int)sm.found_bin, in_bin = sm.found_count;
-    n = sm.found_n, w = sm.found_w;
+    bin = (int)sm.found_bin[by_weight], in_bin = sm.found_count[by_weight];
+    n = sm.found_n[by_weight], w = sm.found_w[by_weight];
     return true;
   }
 
