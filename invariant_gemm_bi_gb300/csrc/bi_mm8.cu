@@ -307,10 +307,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          // (CTA scope: what is waited for are copies and TMEM stores, complete
-          // when they arrive; the cluster's costs 150 cycles more a wait)
-          if ((kb % kGroup == 0 && !mbar_wait_bounded(sfull0 + 8 * slot, (grp / Lay::SLOTS) & 1, wc.abort, wc.status_word,
-                                                      wc.limit_ns, status_code(6, kSiteMmaFull))) ||
+          // (Exponents, some of them the other CTA's: cluster scope.  Copies: CTA scope,
+          // their bytes are counted here when they have landed; the cluster's would cost
+          // 150 cycles more a wait.)
+          if ((kb % kGroup == 0 && !mbar_wait_bounded<true>(sfull0 + 8 * slot, (grp / Lay::SLOTS) & 1, wc.abort,
+                                                            wc.status_word, wc.limit_ns, status_code(6, kSiteMmaFull))) ||
               !mbar_wait_bounded(bars.full(s), (it / Lay::STAGES) & 1, wc.abort, wc.status_word, wc.limit_ns,
                                  status_code(6, kSiteMmaFull))) {
             ok = false;
@@ -402,8 +403,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_store_4cols(to + j * Lay::SF_COLS + Lay::SFA_COLS, w[0], w[1], w[2], w[3]);
             if (Lay::SFB_COLS > 4) tmem_store_4cols(to + j * Lay::SF_COLS + Lay::SFA_COLS + 4, w[4], w[5], w[6], w[7]);
           }
-          // (The stores to TMEM are complete by now; an arrival that also releases
-          // memory to the cluster would take a thousand cycles.)
+          // (the issuer, in the even CTA, has the pair's MMAs read both CTAs' exponents:
+          // stores, fence, arrival and its wait are ordered as mbar_arrive_remote says)
           tmem_store_wait();
           tc_fence_before_sync();
           __syncwarp();

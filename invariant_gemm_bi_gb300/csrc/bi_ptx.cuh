@@ -74,16 +74,20 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 }
 
 // Arrives on the mbarrier at shared-memory offset `bar` of CTA `rank` of this
-// cluster.  Default (CTA-scope release) semantics: it signals that this
-// thread's tensor-memory reads are done -- ordered before it by
-// tcgen05.wait::ld and tcgen05.fence::before_thread_sync -- and publishes no
-// generic memory writes to the other CTA.  (A cluster-scope release would
-// wait for this thread's outstanding global stores, about a microsecond.)
+// cluster.  It tells a thread of that CTA that this thread's tensor-memory
+// accesses are done, reads or stores; it publishes no memory.  What orders
+// tensor memory between threads are the tcgen05 instructions, the accesses
+// completed by tcgen05.wait::ld or ::st and the two fences
+// (tcgen05.fence::before_thread_sync ahead of the arrival,
+// ::after_thread_sync behind the wait); the barrier between the fences may be
+// relaxed, but its scope has to span both threads, here and at the wait.  (A
+// release at that scope waits for this thread's outstanding global accesses,
+// about a microsecond.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
       "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar),
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [ra];\n\t}" ::"r"(bar),
       "r"(rank)
       : "memory");
 }
