@@ -404,7 +404,9 @@ extern "C" bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_te
   c.that(k_cache->shape[2] == H && k_cache->shape[3] == D, BI_ERR_SHAPE_MISMATCH,
          "the caches must be [P, page_size, Hkv, D] with k's Hkv and D");
   c.that(ps >= 1 && P * ps <= INT32_MAX, BI_ERR_INVALID_ARG, "page_size must be positive and P * page_size < 2^31");
-  c.that(H <= kMaxHeads && (double)T * H * D <= 5e11, BI_ERR_INVALID_ARG, "too many elements");
+  // a token's heads of k and v, and its units of 16 elements, are counted in 32 bits
+  c.that(2 * H <= kMaxHeads && H * ((D + 15) / 16) <= INT32_MAX, BI_ERR_INVALID_ARG, "too many heads");
+  c.that((double)T * H * D <= 5e11, BI_ERR_INVALID_ARG, "too many elements");
   if (!c.ok()) return abi_finish(c.st, c.why);
   const bi_tensor* in[5] = {slots, k_cache, k_scales, v_cache, v_scales};
   c.distinct(k, "k");
