@@ -97,22 +97,53 @@ __device__ __forceinline__ void store_one(void* p, int kind, float v) {
     *reinterpret_cast<unsigned short*>(p) = (unsigned short)f_to_half(v, kind);
 }
 
-// a cos and a sin of position n's angle for pair i.  FINE (caches in 8 bits):
-// with what the angle's rounding to fp32 left out, as a small turn d more,
-// sin + d cos and cos - d sin.  An element next to a border of two e4m3 numbers
-// is put on one side or the other, a sixteenth of it apart, by errors of any
-// size; with the angle's 2^-24 there are 1.7 times as many on the wrong side.
+// Sine and cosine of t 2^-64 turns, each off by at most 0.71 and 0.62 of its last place.
+// The nearest whole number of quarter turns is taken off in integers; what is left,
+// theta in [-pi/4, pi/4], is the sum of two fp32, and the polynomials (the series to
+// theta^9 and theta^10, whose next terms are below 2^-28 of the result) only give what
+// is added, in the one last rounding, to theta or to 1 - theta^2 / 2:
+//   sin = h + (l (1 - z/2) + h z S(z)),   cos = (1 - z/2) + (z^2 C(z) - h l),   z = h^2,
+// with what 1 - z/2 and z leave out.  (2097152 angles: one sine in 58 and one cosine
+// in 144 are not the nearest fp32.)
+__device__ __forceinline__ void sine_cosine(int64_t t, float& s, float& c) {
+  const uint64_t quarters = ((uint64_t)t + (1ull << 61)) >> 62;
+  const int64_t r = (int64_t)((uint64_t)t - (quarters << 62));
+  const float a = __ll2float_rn(r), rest = __ll2float_rn(r - __float2ll_rz(a));
+  constexpr float kUnit = 3.4061215800865545e-19f;  // 2 pi 2^-64, and what fp32 leaves out
+  constexpr float kUnitLow = (float)(3.4061215800865545e-19 - (double)kUnit);
+  const float h = __fmul_rn(a, kUnit);
+  const float l = __fmaf_rn(rest, kUnit, __fmaf_rn(a, kUnitLow, __fmaf_rn(a, kUnit, -h)));
+  const float z = __fmul_rn(h, h), half = __fmul_rn(0.5f, z);
+  float u = __fmaf_rn(z, 1.0f / 362880, -1.0f / 5040);
+  u = __fmaf_rn(z, u, 1.0f / 120);
+  u = __fmaf_rn(z, u, -1.0f / 6);
+  const float sine = __fadd_rn(h, __fmaf_rn(__fmul_rn(h, z), u, __fmaf_rn(l, -half, l)));
+  float v = __fmaf_rn(z, -1.0f / 3628800, 1.0f / 40320);
+  v = __fmaf_rn(z, v, -1.0f / 720);
+  v = __fmaf_rn(z, v, 1.0f / 24);
+  const float w = __fsub_rn(1.0f, half);
+  float d = __fmaf_rn(__fmul_rn(z, z), v, __fsub_rn(__fsub_rn(1.0f, w), half));
+  d = __fmaf_rn(h, -l, d);
+  d = __fmaf_rn(-0.5f, __fmaf_rn(h, h, -z), d);
+  const float cosine = __fadd_rn(w, d);
+  s = quarters & 1 ? cosine : sine;
+  c = quarters & 1 ? sine : cosine;
+  if (quarters & 2) s = -s;
+  if ((quarters + 1) & 2) c = -c;
+}
+
+// a cos and a sin of position n's angle for pair i.  FINE (caches in 8 bits): by
+// sine_cosine.  An element next to a border of two e4m3 numbers is put on one side or
+// the other, a sixteenth of it apart, by errors of any size: sines of the angle
+// rounded to fp32, off by a last place or two, put two to four times as many on the
+// wrong side as sines rounded once.
 template <bool FINE = false>
 __device__ __forceinline__ void turn(const RopeParams& p, int64_t n, int i, float& c, float& s) {
   const uint64_t t = p.phase[i] * (uint64_t)n;
-  const float a = __ll2float_rn((long long)t);
-  sincospif(__fmul_rn(a, 1.0842021724855044e-19f /* 2^-63 */), &s, &c);
-  if constexpr (FINE) {
-    const float d = __ll2float_rn((long long)t - __float2ll_rz(a)) * 3.4061215800865545e-19f;  // pi 2^-63
-    const float s0 = s;
-    s = __fmaf_rn(d, c, s);
-    c = __fmaf_rn(-d, s0, c);
-  }
+  if constexpr (FINE)
+    sine_cosine((int64_t)t, s, c);
+  else
+    sincospif(__fmul_rn(__ll2float_rn((long long)t), 1.0842021724855044e-19f /* 2^-63 */), &s, &c);
   c = __fmul_rn(c, p.magnitude);
   s = __fmul_rn(p.transpose ? -s : s, p.magnitude);
 }
