@@ -632,9 +632,11 @@ bi_status bi_mm_blockscaled(const bi_tensor* a, const bi_tensor* a_scales, const
  * its rotated pairs, before they are turned, and of |x| over its other elements:
  * turned elements do not exceed it, and a key's scale does not depend on its
  * position.  (It is at most twice the largest element: one binade of the
- * range's small end.)  Turned keys are rounded once, from fp32 to e4m3.  All
- * else is as in bi_paged_store; rows of tokens that are not stored keep their
- * scales too.
+ * range's small end.)  Turned keys are rounded once, from fp32 to e4m3.  Keys
+ * and q are turned by sines and cosines of the angle in 64 bits, rounded once;
+ * bi_rope and bi_paged_store round the angle to fp32 first, so that q_out may
+ * differ from theirs in the last places.  All else is as in bi_paged_store; rows
+ * of tokens that are not stored keep their scales too.
  */
 bi_status bi_paged_store_quantized(const bi_rope_config* config, const bi_tensor* positions,
                                    const bi_tensor* slots, const bi_tensor* q, const bi_tensor* q_out,

@@ -787,7 +787,7 @@ def bi_paged_store_quantized(k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
                              q_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor | None:
     """bi_paged_store into caches [P, page_size, Hkv, D] of float8_e4m3fn with scales
     [P, page_size, Hkv], one a token and head.  q_out is allocated in q_dtype, or in
-    q's dtype, when not given."""
+    q's dtype, when not given, and may differ from bi_rope's result in the last places."""
     lib = _lib or load()
     dev = _call_device(k, "k")
     if q is not None and q_out is None:

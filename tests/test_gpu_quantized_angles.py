@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from invariant_gemm_bi_gb300 import binding as bi
+from tests.gpu_helpers import bits_equal
 from tests.test_gpu_quantized import BF16, F32, _cache, _clean_status, _gen, _normal  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,22 @@ def test_sines_and_cosines_to_less_than_a_last_place(D):
         err = np.abs(got.astype(np.float64) - want) / place
         assert err.max() <= 0.86
     assert (y[:, R:] == 0).all()
+
+
+def test_turned_queries_beside_bi_rope():
+    # the same angles, sines rounded otherwise: within two last places of the pair's size,
+    # and where no angle has to be rounded the same bits
+    D, T = 128, 300
+    cfg = bi.bi_rope_config(D)
+    q = _normal((T, 4, D), F32, 5)
+    pos = torch.randint(0, 2 ** 20, (T,), generator=_gen(2), device="cuda")
+    a, b = _turned(q, pos, cfg), bi.bi_rope(q, pos, cfg)
+    size = torch.hypot(q[..., :64], q[..., 64:]).repeat(1, 1, 2)
+    # sines of either: under 2^-22 off (bi_rope's angle 2^-24 of pi, sincospif two last
+    # places), times |x1| + |x2|, at most sqrt(2) of the size; products and sums 2^-24 each
+    assert ((a - b).abs() <= 2.0 ** -20 * size).all()
+    zero = torch.zeros_like(pos)
+    assert bits_equal(_turned(q, zero, cfg), bi.bi_rope(q, zero, cfg))
+    quarter = bi.bi_rope_config(2, frequencies=[np.pi / 2])  # whole quarter turns
+    at = torch.arange(T, device="cuda")
+    assert torch.equal(_turned(q, at, quarter), bi.bi_rope(q, at, quarter))
