@@ -44,7 +44,7 @@
 // pieces, below).
 //
 // Caches in 8 bits (template kCache8): half the bytes and the same work a key, so
-// that issue weighs twice as much.  A slot is 32 keys of D bytes at every D, three of
+// that issue weighs twice as much.  A slot is a tile of keys of D bytes, three of
 // them a warp, 12 warps an SM at D = 128; chunks of 16 dimensions are read back and
 // brought to fp16 in registers, two e4m3 a conversion, for the same mma.sync; values
 // are read by transposing pairs of dimensions and sorted by byte permutes.  The batch
