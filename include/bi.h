@@ -663,7 +663,7 @@ bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_tensor* k_cac
  * empty requests and the workspace are bi_paged_attention's.  A head of q that
  * holds a NaN or an infinity gives NaNs.
  *
- * Order: as bi_paged_attention with W = 4 and, beyond 8192 keys, pieces of 1024
+ * Order: as bi_paged_attention with W = 4 and, beyond 16384 keys, pieces of 1024
  * 2^k keys, at most 128 of them; t = RN(RN(s k_scale) f), s the fp32 sum of
  * products of fp16 numbers, q brought to fp16 by a power of two of its own for
  * each head (exact down to 2^-27 of its largest element) and f = scale log2 e
