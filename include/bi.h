@@ -646,10 +646,12 @@ bi_status bi_paged_store_quantized(const bi_rope_config* config, const bi_tensor
 
 /*
  * Rows of caches in 8 bits read back: k[t] = k_cache[slots[t]] * k_scales, v
- * likewise, one rounding to the outputs' type; slots [T] int64 in any order,
- * the same one as often as wanted; a negative slot gives a row of zeros, one
- * past the cache too, and is reported.  k, v [T,Hkv,D] of one type, bf16, fp16
- * or fp32, unit stride on D, D <= 1024.
+ * likewise: the product in fp32, exact when the scale is a power of two and
+ * rounded once otherwise, then rounded to the outputs' type; slots [T] int64 in
+ * any order, the same one as often as wanted; a negative slot gives a row of
+ * zeros, one past the cache too, and is reported.  k, v [T,Hkv,D] of one type,
+ * bf16, fp16 or fp32, unit stride on D, D <= 1024; at most 2^29 heads, and fewer
+ * than 2^31 units of 16 elements a token.
  */
 bi_status bi_paged_load_quantized(const bi_tensor* slots, const bi_tensor* k_cache,
                                   const bi_tensor* k_scales, const bi_tensor* v_cache,
