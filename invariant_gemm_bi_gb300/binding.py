@@ -766,7 +766,8 @@ def bi_mm_blockscaled(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, 
     """a [M, K] times b [K, N] (a weight [N, K], transposed), both e4m3 with scales of
     blocks of 1 x 128 and 128 x 128: a_scales [M, ceil(K / 128)], b_scales
     [ceil(K / 128), ceil(N / 128)] (the weight's, transposed), powers of two as
-    bi_quantize_blocks makes them; plus bias [N]."""
+    bi_quantize_blocks makes them (any other number counts as a NaN, and so do the
+    results it reaches); plus bias [N]."""
     lib = _lib or load()
     dev = _call_device(a, "a")
     if out is None:
