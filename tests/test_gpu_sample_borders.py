@@ -101,3 +101,29 @@ def test_top_k_at_borders(R, N, dt):
     k = torch.tensor([(2, 40, 600, 5000, N // 2, N - 3)[i % 6] for i in range(R)], dtype=torch.int32, device="cuda")
     for t0 in (1.0, 4.0):
         check(x, torch.full((R,), t0, device="cuda"), k=k, seed=int(t0))
+
+
+@pytest.mark.parametrize("R,N", [(400, 3000), (320, 40000), (310, 80000), (60, 30000), (16, 128256)])
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+def test_all_limits_together_at_borders(R, N, dt):
+    # min-p keeps what is at least its share of the largest: by the value, below every other limit or above
+    x = _normal((R, N), dt, R + N + 2, 2.0)
+    k = torch.tensor([(3, 513, N // 3, N // 2, 0, N + 9)[i % 6] for i in range(R)], dtype=torch.int32, device="cuda")
+    p = _f32([(0.4, 0.9, 0.999, 1.0)[i % 4] for i in range(R)])
+    m = _f32([(0.0, 0.3, 0.01, -1.0, 0.0005)[i % 5] for i in range(R)])
+    for t0 in (1.0, 4.0):
+        t = torch.full((R,), t0, device="cuda")
+        w, near = kept(x, t, torch.where(k <= 0, N, k), torch.where(p >= 1, 2.0, p))
+        top = x.double().amax(1, keepdim=True)
+        share = torch.exp((x.double() - top) / t0)
+        least = m.double()[:, None]
+        near |= ((share - least).abs() < MARGIN * least).any(1)
+        w = torch.where(share >= least, w, torch.zeros_like(w))
+        u = at_borders(w, int(t0))
+        want, close = token(w, u)
+        skip = near | close
+        expected = NEAR * R
+        assert int(skip.sum()) <= expected + 4 * expected ** 0.5 + 3
+        got = bi.bi_sample_tokens(x, u, temperature=t, top_k=k, top_p=p, min_p=m)
+        wrong = (got != want) & ~skip
+        assert not wrong.any(), (wrong.nonzero()[:5, 0].tolist(), got[wrong][:5].tolist(), want[wrong][:5].tolist())
