@@ -34,7 +34,7 @@
 // stored): 16 x 14336 x 4096 15.4 us against 19.5, 16 x 4096 x 4096 9.5 against 13.7.
 //
 // Measured (M x N x K, bf16 results): 8192 x 14336 x 4096 308 us alone, 3.1 PFLOP/s,
-// 344 in a long run under the power limit; 4096^3 50 us, 2.75 PFLOP/s; 2048 x 4096 x
+// 342-354 in a long run under the power limit; 4096^3 50 us, 2.75 PFLOP/s; 2048 x 4096 x
 // 4096 32 us; 300 x 14336 x 4096 23.7 us; 16 x 14336 x 4096 15.4 us, 3.8 TB/s: start
 // (TMEM, barriers, a cluster's exchange, 3 us), the copies, the last segment's sums.
 // Large ones are bound by the tensor cores and their power: a block's four MMAs take 400

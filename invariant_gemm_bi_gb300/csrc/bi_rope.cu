@@ -217,10 +217,11 @@ __device__ __forceinline__ char* target(const RopeParams& p, const TokenPlace& a
 // way or the other next to 448 2^e, would decide a whole head's scale).  It is
 // up to twice the largest element: at most one binade at the small end.
 //
-// Measured: 8191 tokens of 32 + 8 + 8 heads of 128, bf16, 185 MB, 41.5 us, 4.5 TB/s: by
+// Measured: 8191 tokens of 32 + 8 + 8 heads of 128, bf16, 185 MB, 40.8 us, 4.5 TB/s: by
 // issue (57 %, 285 instructions a warp and unit) and by waves (2048 blocks are 3.37
-// of 608); fp32 85 us (105 with two blocks an SM); 64 tokens 4.0 us.  Six heads ahead
+// of 608); fp32 85 us (105 with two blocks an SM); 64 tokens 3.8 us.  Six heads ahead
 // 44.8 us, two 41.6; half the heads a block 51.6 (each block has its sines to compute).
+// These instances spill 28 to 52 bytes at 64 registers, the 16-bit ones none.
 __device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t pair_size(float x1, float x2, float magnitude) {
   return size_bits(__fmul_rn(__fadd_rn(fabsf(x1), fabsf(x2)), magnitude));

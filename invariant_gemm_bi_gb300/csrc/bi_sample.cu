@@ -44,6 +44,8 @@
 // shared memory, 3.5 lanes to a bank), the rest are the row's own chain: maximum,
 // table, three exchanges of the cluster, the draw.  8 fp32 rows take
 // 40 us with top-p alone, 21 without limits: the chain, and counting in four sums.
+// All kernels spill at 64 registers, two CTAs of 512 threads or one of 1024 an SM: what a
+// thread knows of the bins, kept over both searches, most in bf16 (730 bytes stored).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
