@@ -611,8 +611,9 @@ bi_status bi_quantize_blocks(const bi_tensor* x, int32_t block_rows, const bi_te
  *   applies them as exponents: a scale is 2^-126 .. 2^127, and anything else
  *   (zero, a negative, no power of two) counts as a NaN, whose rows or columns
  *   of c are NaNs then; bi_device_status does not tell, since a NaN is also what
- *   bi_quantize_blocks gives a block that holds one.  A weight with other scales is
- *   brought here by dequantising it and bi_quantize_blocks.  bias [N] bf16, fp16 or fp32, any stride, or NULL.
+ *   bi_quantize_blocks gives a block that holds one.  A weight with other scales
+ *   is brought here by dequantising it and bi_quantize_blocks.  bias [N] bf16,
+ *   fp16 or fp32, any stride, or NULL.
  *   c [M,N] fp32, bf16 or fp16, unit stride on N.  M, N, K <= 2^30.
  *
  * Order: steps of 32 in ascending order accumulate in fp32 in the tensor core,

@@ -2,13 +2,15 @@
 //   k[t, h, :] = k_cache[slots[t]][h, :] * k_scales[slots[t]][h],  v likewise.
 //
 // Every byte is read once and every result written once: the call is bound by
-// memory.  Products are rounded to fp32, where those with a power of two for a scale
-// are exact (the library's own scales), then to a result of 16 bits; with any other
-// scale that is a second rounding, which puts about one result in 2^17 of bf16, one in
-// 2^14 of fp16, on the other side of a tie.  A thread takes 16 elements of one head (16 bytes in, 32 out in 16
+// memory.  A thread takes 16 elements of one head (16 bytes in, 32 out in 16
 // bits); neighbouring threads take neighbouring units of a token, whose heads
 // lie side by side in the cache, and each thread four units, keys and values
 // of two tokens, whose loads are all requested before the first is used.
+//
+// Products are rounded to fp32, where those with a power of two for a scale (the
+// library's own) are exact, then to a result of 16 bits.  With any other scale that
+// is a second rounding: about one result in 2^17 of bf16, one in 2^14 of fp16, is
+// put on the other side of a tie.
 //
 // Measured: 131071 tokens of 8 heads of 128 into bf16, 815 MB in and out, 132 us,
 // 6.2 TB/s (0.91 of the copy rate); 1021 tokens 3.5 us, three dependent loads

@@ -9,7 +9,7 @@
 // then the rounding of each.  A 128 x 128 block is a block of 512 threads, four
 // rows a half-warp, the maximum joined through shared memory.
 //
-// Measured: a weight of 14336 x 4096 bf16, 176 MB in and out, 30.2 us, 5.8 TB/s (0.86
+// Measured: a weight of 14336 x 4096 bf16, 176 MB in and out, 29.4-30.2 us, 5.9 TB/s (0.87
 // of the copy rate; what is left is the barrier between a block's reads and its
 // writes: 256 threads of eight rows, three blocks an SM, 32.0 us, four 30.6 but fp32
 // 29.8 for 24.1; 1024 threads 37.8).  Rows of 16 x 4096 take 1.6 us, of 8192 x 4096 23.2:

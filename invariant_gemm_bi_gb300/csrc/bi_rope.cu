@@ -97,14 +97,14 @@ __device__ __forceinline__ void store_one(void* p, int kind, float v) {
     *reinterpret_cast<unsigned short*>(p) = (unsigned short)f_to_half(v, kind);
 }
 
-// Sine and cosine of t 2^-64 turns, each off by at most 0.71 and 0.62 of its last place.
+// Sine and cosine of t 2^-64 turns, off by at most 0.71 and 0.62 of a last place.
 // The nearest whole number of quarter turns is taken off in integers; what is left,
 // theta in [-pi/4, pi/4], is the sum of two fp32, and the polynomials (the series to
 // theta^9 and theta^10, whose next terms are below 2^-28 of the result) only give what
 // is added, in the one last rounding, to theta or to 1 - theta^2 / 2:
 //   sin = h + (l (1 - z/2) + h z S(z)),   cos = (1 - z/2) + (z^2 C(z) - h l),   z = h^2,
-// with what 1 - z/2 and z leave out.  (2097152 angles: one sine in 58 and one cosine
-// in 144 are not the nearest fp32.)
+// with what 1 - z/2 and z leave out.  (Of 3 million results one in 65 is not the
+// nearest fp32.)
 __device__ __forceinline__ void sine_cosine(int64_t t, float& s, float& c) {
   const uint64_t quarters = ((uint64_t)t + (1ull << 61)) >> 62;
   const int64_t r = (int64_t)((uint64_t)t - (quarters << 62));

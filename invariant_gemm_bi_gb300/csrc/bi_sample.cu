@@ -105,6 +105,7 @@ constexpr int kList = 512;  // elements that are sorted
 //                    again or used as `mine` behind the second.
 // Behind the last barrier of a row's path no CTA reads or writes another's memory, so
 // each leaves when it is done.
+
 // bf16: numbers of exponents -8 .. 5, in the order of their values: the positive
 // ones, what lies between, the negative ones.
 constexpr int kBase16 = (127 - 8) << 7, kSpan16 = 14 << 7, kMiddle16 = kSpan16, kBins16 = 2 * kSpan16 + 1;
